@@ -8,6 +8,9 @@ used for device memory and streams only.
 
 from ._lib import FP8BWError, PROTOTYPES, load_library, lib_path  # noqa: F401
 from .ops import (  # noqa: F401
+    RMSNormOut,
+    adamw_scales,
+    adamw_step,
     colmajor_empty,
     fp8_blockwise_quant,
     fp8_blockwise_quant_dual,
@@ -26,6 +29,10 @@ from .ops import (  # noqa: F401
     gemm_plan,
     linear_saved_bytes,
     linear_workspace,
+    linear_xent_bwd,
+    linear_xent_fwd,
+    rms_norm_bwd,
+    rms_norm_fwd,
     scale_grid,
 )
 from .torch_ops import Float8BlockwiseLinear  # noqa: E402,F401  (registers torch.ops.fp8bw.*)

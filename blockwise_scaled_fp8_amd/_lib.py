@@ -12,8 +12,19 @@ c_i64 = ctypes.c_int64
 c_int = ctypes.c_int
 c_size = ctypes.c_size_t
 c_ptr = ctypes.c_void_p
+c_f32 = ctypes.c_float
+c_f64 = ctypes.c_double
+c_u64 = ctypes.c_uint64
 
 ABI_VERSION = 2   # fp8bw_abi_version() of the sources these prototypes mirror
+
+
+class AdamwTensor(ctypes.Structure):
+    """fp8bw_adamw_tensor of include/fp8bw.h."""
+    _fields_ = [("param", c_ptr), ("grad", c_ptr), ("exp_avg", c_ptr), ("exp_avg_sq", c_ptr),
+                ("exp_avg_scale", c_ptr), ("root_scale", c_ptr), ("master", c_ptr),
+                ("numel", c_i64), ("param_dtype", c_int), ("grad_dtype", c_int)]
+
 
 # name -> (restype, argtypes), mirroring include/fp8bw.h
 PROTOTYPES = {
@@ -63,6 +74,20 @@ PROTOTYPES = {
                                     c_size, c_ptr]),
     "fp8_linear_bwd": (c_int, [c_ptr, c_ptr, c_ptr, c_size, c_ptr, c_ptr, c_i64, c_i64, c_i64,
                                c_ptr, c_size, c_ptr]),
+    "fp8bw_rms_norm_fwd": (c_int, [c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_int, c_f32, c_i64, c_i64,
+                                   c_ptr, c_i64, c_ptr, c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_i64,
+                                   c_i64, c_ptr, c_i64, c_ptr, c_i64, c_i64, c_ptr]),
+    "fp8bw_rms_norm_bwd_ws_bytes": (c_size, [c_i64, c_i64]),
+    "fp8bw_rms_norm_bwd": (c_int, [c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_ptr, c_int, c_ptr, c_i64,
+                                   c_i64, c_i64, c_ptr, c_i64, c_ptr, c_ptr, c_size, c_ptr]),
+    "fp8bw_linear_xent_ws_bytes": (c_size, [c_i64, c_i64, c_i64, c_int]),
+    "fp8bw_linear_xent_fwd": (c_int, [c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_i64, c_i64, c_i64,
+                                      c_i64, c_ptr, c_ptr, c_ptr, c_size, c_ptr]),
+    "fp8bw_linear_xent_bwd": (c_int, [c_ptr, c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_i64, c_ptr,
+                                      c_i64, c_i64, c_i64, c_ptr, c_i64, c_ptr, c_i64, c_ptr,
+                                      c_size, c_ptr]),
+    "fp8bw_adamw_step": (c_int, [ctypes.POINTER(AdamwTensor), c_int, c_int, c_i64, c_f64, c_f64,
+                                 c_f64, c_f64, c_f64, c_ptr, c_int, c_u64, c_ptr]),
 }
 
 STATUS = {0: "FP8BW_OK", 1: "FP8BW_ERR_NULL", 2: "FP8BW_ERR_SHAPE", 3: "FP8BW_ERR_LAYOUT",

@@ -23,10 +23,12 @@ LIB = os.path.join(HERE, "libfp8bw.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["quant.hip", "gemm.hip", "api.cpp"]
-# Per-source extra flags.  gemm.hip: select the VGPR form of MFMA so the
-# rescale's VALU reads the MFMA results without AGPR->VGPR copies.
-EXTRA = {"gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+SOURCES = ["quant.hip", "gemm.hip", "rmsnorm.hip", "xent.hip", "adamw.hip", "api.cpp",
+           "train_api.cpp"]
+# Per-source extra flags.  gemm.hip, xent.hip: select the VGPR form of MFMA so
+# that the rescale's and the epilogues' VALU read the MFMA results without
+# AGPR->VGPR copies.
+EXTRA = {s: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for s in ("gemm.hip", "xent.hip")}
 
 FLAGS = [
     f"--offload-arch={ARCH}",

@@ -93,4 +93,88 @@ hipError_t launch_grouped_gemm(const GemmProblem& p, int groups, const int* grou
                                int64_t b_s_group, int64_t rb_s_group, hipStream_t stream);
 hipError_t launch_zero_bf16(void* out, int64_t rows, int64_t cols, hipStream_t stream);
 
+// ---- RMS norm (rmsnorm.hip) ----
+struct NormWeight {
+  const void* p;   // bf16 or fp32 [cols]
+  int f32;
+};
+constexpr int64_t kNormMaxCols = 32768;   // 1024 threads x 4 chunks of 8 columns
+struct NormFwdArgs {
+  int64_t rows, cols;
+  const uint16_t* x; int64_t ld_x;
+  const uint16_t* residual; int64_t ld_res;   // nullptr: s = x
+  uint16_t* sum; int64_t ld_sum;              // s, written with a residual (may be x or residual)
+  NormWeight weight;
+  float eps;
+  float* rstd;
+  uint16_t* y; int64_t ld_y;                                          // nullptr: not written
+  uint8_t* q; int64_t ld_q; float* recip; int64_t rs_row, rs_kb;      // nullptr: not written
+  uint8_t* qt; int64_t ld_qt; float* recip_t; int64_t rst_row, rst_kb;
+};
+struct NormBwdArgs {
+  int64_t rows, cols;
+  const uint16_t* dy; int64_t ld_dy;
+  const uint16_t* s; int64_t ld_s;
+  const float* rstd;
+  NormWeight weight;
+  const uint16_t* dres; int64_t ld_dres;      // nullptr: none
+  uint16_t* dx; int64_t ld_dx;
+  void* dweight;                              // the weight's type
+  float* partial;                             // rms_norm_bwd_ws_bytes
+};
+hipError_t launch_rms_norm_fwd(const NormFwdArgs& p, hipStream_t stream);
+size_t rms_norm_bwd_ws_bytes(int64_t rows, int64_t cols);
+hipError_t launch_rms_norm_bwd(const NormBwdArgs& p, hipStream_t stream);
+
+// ---- AdamW (adamw.hip) ----
+enum AdamwFlags { kAdamwParamF32 = 1, kAdamwGradF32 = 2 };
+struct AdamwTensor {
+  void* param;
+  const void* grad;
+  void* m;             // fp32, or E4M3 codes
+  void* v;             // fp32, or E4M3 codes of the root
+  float* m_scale;      // 8-bit states: one per 128 elements
+  float* root_scale;
+  float* master;       // nullptr: none
+  int64_t numel;
+  uint32_t key;        // of the tensor's random bits
+  int flags;
+};
+// One launch's tensors and constants, passed by value: 40 tensors keep the
+// kernel's arguments below 4 KB.
+constexpr int kAdamwTensors = 40;
+struct AdamwLaunch {
+  AdamwTensor t[kAdamwTensors];
+  int first[kAdamwTensors];   // first workgroup of each tensor
+  int count, iters;           // tensors; runs of 2048 elements per workgroup
+  const float* grad_scale;    // device scalar or nullptr
+  float beta1, one_minus_beta1, beta2, one_minus_beta2;
+  float decay;                // 1 - lr * weight_decay
+  float step_size;            // lr / (1 - beta1^t)
+  float root_factor;          // 1 / sqrt(1 - beta2^t)
+  float eps;
+};
+uint32_t adamw_key(uint64_t seed, int ordinal);
+hipError_t launch_adamw(const AdamwLaunch& L, int workgroups, bool eight, bool random,
+                        hipStream_t stream);
+
+// ---- linear cross entropy (xent.hip) ----
+struct XentArgs {
+  int64_t T, V, K;
+  const void* h; int64_t ld_h;        // bf16 [T, K]
+  const void* w; int64_t ld_w;        // bf16 [V, K]
+  const int64_t* target;              // [T]
+  int64_t ignore_index;
+  float* loss;                        // [T] (forward)
+  float* lse;                         // [T] (forward writes, backward reads)
+  const float* dloss;                 // [T] (backward)
+  void* dh; int64_t ld_dh;            // bf16 [T, K] or nullptr
+  void* dw; int64_t ld_dw;            // bf16 [V, K] or nullptr
+};
+size_t xent_ws_bytes(int64_t T, int64_t V, int64_t K, bool backward);
+hipError_t launch_xent_fwd(const XentArgs& p, void* ws, hipStream_t stream);
+hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream);
+// +0 in a bf16 [rows, cols] matrix of leading dimension ld.
+hipError_t launch_zero_rows_bf16(void* out, int64_t rows, int64_t cols, int64_t ld, hipStream_t stream);
+
 }  // namespace fp8bw

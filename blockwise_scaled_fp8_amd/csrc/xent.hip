@@ -1,0 +1,632 @@
+// Cross entropy of a linear head, logits = H W^T, without keeping the logits
+// (gfx950).
+//
+//   z[t, v] = sum_k h[t, k] w[v, k]
+//   lse[t]  = log sum_v exp z[t, v],   loss[t] = lse[t] - z[t, target[t]]
+//   G[t, v] = (exp(z[t, v] - lse[t]) - [v == target[t]]) dloss[t]
+//   dH = G W,   dW = G^T H
+//
+// Forward: one product whose epilogue keeps, per token and tile of 256
+// vocabulary columns, the maximum and the sum of exponentials over it; a
+// second kernel joins the tiles.  Backward: the vocabulary is taken in
+// pieces; per piece the logits are made again, their epilogue turns them into
+// G (bf16), and two products add G's share to dH and finish the piece's rows
+// of dW.  The workspace holds one piece, whatever the vocabulary.
+//
+// Every product is the same kernel on bf16 operands whose rows run along the
+// contraction (C = A B^T, v_mfma_f32_16x16x32_bf16, fp32 accumulators).  It
+// is bound by the matrix cores from a few hundred tokens on, by the reading of
+// W below.
+//
+// Rounding: G is held as bf16, the accuracy of the matrix cores' operands.
+// It is formed with dloss divided by its largest magnitude, which the
+// epilogues multiply back in fp32: with the usual equal weights of a mean
+// loss nothing but G's own rounding remains.
+
+#include "device_common.h"
+#include "launch.h"
+
+namespace fp8bw {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// What a product's epilogue does with its tile.
+enum XentEpilogue {
+  kStats = 0,    // maximum and sum of exponentials per row; the targets' logits
+  kGrad = 1,     // G in bf16
+  kOut = 2,      // bf16, times *scale
+  kAcc = 3       // fp32 partial [split][M][N], written or added to
+};
+
+struct XentGemm {
+  const uint8_t* a; int64_t lda;   // rows of the contraction, in bytes
+  const uint8_t* b; int64_t ldb;
+  int M, N;
+  int kblocks;                     // of 64 elements (128 bytes)
+  int kb_per_split;
+  int tiles_m, tiles_n;
+  // kStats
+  float2* part;                    // [tiles_n][M] (max, sum of exp(z - max))
+  const int64_t* target;
+  float* target_logit;             // [M]
+  // kGrad
+  const float2* row;               // [M] (lse, dloss / scale)
+  const int* local_target;         // [M] target column of the whole vocabulary, or -1
+  int v0;                          // first vocabulary column of this piece
+  // outputs
+  void* out; int64_t ldo;          // kGrad, kOut: bf16 elements
+  const float* scale;
+  float* acc;                      // kAcc
+  int add;
+};
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int64_t bytes) {
+  const uint32_t n = bytes >= 0xFFFFFFFFll ? 0xFFFFFFFFu : (uint32_t)bytes;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)n, 0x00020000);
+}
+
+// Waits of the two-stage ring (gfx9 s_waitcnt encoding): this wave's direct
+// loads have landed and its LDS reads returned, then the barrier.
+__device__ __forceinline__ void ring_sync() {
+  __builtin_amdgcn_s_waitcnt(0x7 << 4);
+  __builtin_amdgcn_s_barrier();
+}
+
+// 16-byte chunk c of LDS row r sits at c ^ swz(r): a fragment read (rows
+// l % 16, chunk pair l / 16) and the 1 KB direct writes then meet no bank
+// twice in a pass of 16 lanes (rows are 128 bytes).
+__device__ __forceinline__ int chunk_swz(int row) { return (row >> 1) & 5; }
+
+__device__ __forceinline__ void tile_order(int tile, int tiles_m, int tiles_n, int* tm, int* tn) {
+  constexpr int kGroup = 8;   // row blocks per column sweep: they share W's columns in an XCD's L2
+  const int per = kGroup * tiles_n;
+  const int g = tile / per, first = g * kGroup;
+  const int gm = min(tiles_m - first, kGroup);
+  const int in = tile - g * per;
+  *tm = first + in % gm;
+  *tn = in / gm;
+}
+// Workgroups are dealt to the 8 XCDs in turn; give each XCD a contiguous range.
+__device__ __forceinline__ int xcd_order(int bid, int n) {
+  const int x = bid % 8, q = bid / 8, full = n / 8, rem = n % 8;
+  return x * full + min(x, rem) + q;
+}
+
+__device__ __forceinline__ bf16x8 frag(const uint8_t* tile, uint32_t off) {
+  return __builtin_bit_cast(bf16x8, *(const uint4*)(tile + off));
+}
+
+// C = A B^T on BM x BN tiles of WGM x WGN waves.  Two stages of 128-byte
+// contraction slabs in LDS, filled by direct buffer -> LDS loads from waves 0
+// and 1 (a direct load keeps the issuing wave for about 16 cycles; the others
+// go straight to their MFMAs).  Each stage is an LDS variable of its own and
+// the stage loop is unrolled, so that the compiler sees that reads of one
+// stage do not depend on loads into the other.
+//
+// Edges: with CLAMP every lane's row is clamped to the last one (any M, N);
+// without, M >= BM and N >= BN, and an edge tile's window moves back to end
+// at the last row, so no load needs a register of its own for its row.
+// Either way a tile's epilogue handles only its own rows and columns.
+template <int BM, int BN, int WGM, int WGN, bool CLAMP, int EPI>
+__global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGemm p) {
+  constexpr int NW = WGM * WGN, LW = 2;
+  constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16;
+  constexpr int AI = BM / 8 / LW, BI = BN / 8 / LW;
+  __shared__ __attribute__((aligned(1024))) uint8_t sA0[BM * 128], sA1[BM * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t sB0[BN * 128], sB1[BN * 128];
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm0 = (wave / WGN) * WM, wn0 = (wave % WGN) * WN;
+  const int frow = lane & 15, fq = lane >> 4;
+  // (split, tile), split-major, contiguous per XCD
+  const int id = xcd_order(blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
+  const int split = id / gridDim.x;
+  int tm, tn;
+  tile_order(id - split * gridDim.x, p.tiles_m, p.tiles_n, &tm, &tn);
+  const int m0 = tm * BM, n0 = tn * BN;
+  const int ml = CLAMP ? m0 : min(m0, p.M - BM), nl = CLAMP ? n0 : min(n0, p.N - BN);
+  const int kb0 = split * p.kb_per_split, kb1 = min(p.kblocks, kb0 + p.kb_per_split);
+
+  // Lane 8 q + c of a direct load fills physical chunk c of row 8 o + q (o =
+  // wave + LW i, so o and wave have the same parity).
+  const int lrow = lane >> 3;
+  const int lchunk = (lane & 7) ^ ((4 * (wave & 1) + (lrow >> 1)) & 5);
+  [[maybe_unused]] const __amdgpu_buffer_rsrc_t ars = rsrc_of(p.a + (int64_t)ml * p.lda, (int64_t)BM * p.lda);
+  [[maybe_unused]] const __amdgpu_buffer_rsrc_t brs = rsrc_of(p.b + (int64_t)nl * p.ldb, (int64_t)BN * p.ldb);
+  uint32_t av[CLAMP ? AI : 1], bv[CLAMP ? BI : 1];
+#pragma unroll
+  for (int i = 0; i < (CLAMP ? AI : 1); ++i) {
+    const int r = 8 * (wave + LW * i) + lrow;
+    av[i] = (uint32_t)((CLAMP ? min(r, p.M - 1 - ml) : r) * (int)p.lda + lchunk * 16);
+  }
+#pragma unroll
+  for (int i = 0; i < (CLAMP ? BI : 1); ++i) {
+    const int r = 8 * (wave + LW * i) + lrow;
+    bv[i] = (uint32_t)((CLAMP ? min(r, p.N - 1 - nl) : r) * (int)p.ldb + lchunk * 16);
+  }
+  auto issue = [&](int kb, uint8_t* sa, uint8_t* sb) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if (wave < LW) {
+      const int ko = kb * 128;
+#pragma unroll
+      for (int i = 0; i < AI; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ars, (lds_void*)(sa + (wave + LW * i) * 1024), 16,
+                                                 av[CLAMP ? i : 0],
+                                                 ko + (CLAMP ? 0 : 8 * LW * i * (int)p.lda), 0, 0);
+#pragma unroll
+      for (int i = 0; i < BI; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(brs, (lds_void*)(sb + (wave + LW * i) * 1024), 16,
+                                                 bv[CLAMP ? i : 0],
+                                                 ko + (CLAMP ? 0 : 8 * LW * i * (int)p.ldb), 0, 0);
+    }
+#endif
+  };
+
+  v4f acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  if (kb0 < kb1) issue(kb0, sA0, sB0);
+  ring_sync();
+  for (int it = kb0; it < kb1; it += 2) {
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      const int kb = it + st;
+      if (kb >= kb1) break;
+      // past the end the last slab is loaded again, into a stage nobody reads
+      issue(min(kb + 1, kb1 - 1), st ? sA0 : sA1, st ? sB0 : sB1);
+      const uint8_t* const ta = st ? sA1 : sA0;
+      const uint8_t* const tb = st ? sB1 : sB0;
+      // A lane's two 16-byte chunks of a row, the same on both sides: which k
+      // they are does not matter to the sum.  Made opaque, so that the
+      // compiler keeps two base addresses and constant offsets.
+      uint32_t a0 = (wm0 + frow) * 128 + (((2 * fq) ^ chunk_swz(wm0 + frow)) << 4);
+      uint32_t a1 = (wm0 + frow) * 128 + (((2 * fq + 1) ^ chunk_swz(wm0 + frow)) << 4);
+      uint32_t b0 = (wn0 + frow) * 128 + (((2 * fq) ^ chunk_swz(wn0 + frow)) << 4);
+      uint32_t b1 = (wn0 + frow) * 128 + (((2 * fq + 1) ^ chunk_swz(wn0 + frow)) << 4);
+      asm volatile("" : "+v"(a0), "+v"(a1), "+v"(b0), "+v"(b1));
+      bf16x8 bl[TN], bh[TN], al[2], ah[2];
+      bl[0] = frag(tb, b0);
+      al[0] = frag(ta, a0);
+#pragma unroll
+      for (int j = 1; j < TN; ++j) bl[j] = frag(tb, b0 + 2048 * j);
+      ah[0] = frag(ta, a1);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) bh[j] = frag(tb, b1 + 2048 * j);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        if (i + 1 < TM) {
+          al[(i + 1) & 1] = frag(ta, a0 + 2048 * (i + 1));
+          ah[(i + 1) & 1] = frag(ta, a1 + 2048 * (i + 1));
+          __builtin_amdgcn_sched_barrier(0);   // keep the next row's reads ahead of this row's MFMAs
+        }
+        // B first: lane l then holds row 16 i + l % 16, columns 16 j + 4 (l / 16) + 0..3
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bl[j], al[i & 1], acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bh[j], ah[i & 1], acc[i][j], 0, 0, 0);
+      }
+      ring_sync();
+    }
+  }
+  ring_sync();   // the stages are free
+
+  const int row0 = ml + wm0 + frow;            // + 16 i
+  const int col0 = nl + wn0 + 4 * fq;          // + 16 j + v
+  if constexpr (EPI == kStats) {
+    // Maximum and sum of exponentials of each row over this wave's columns
+    // (a row's columns lie in lanes frow + 16 q), then over the waves.
+    float2* const red = (float2*)sA0;          // [WGN][BM]
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int r = row0 + 16 * i;
+      const bool mine = r >= m0 && r < p.M;
+      const int64_t tgt = mine ? p.target[r] : -1;
+      float m = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int n = col0 + 16 * j + v;
+          const bool in = n >= n0 && n < p.N;
+          if (in && (int64_t)n == tgt) p.target_logit[r] = acc[i][j][v];
+          // A NaN logit has to reach the sum: fmaxf drops it, the sum does not.
+          if (in) m = fmaxf(m, acc[i][j][v]);
+        }
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float base = m == -INFINITY ? 0.f : m;   // no column, or all at -inf
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int n = col0 + 16 * j + v;
+          if (n >= n0 && n < p.N) s += __builtin_amdgcn_exp2f((acc[i][j][v] - base) * kLog2e);
+        }
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      if (fq == 0) red[(wave % WGN) * BM + wm0 + 16 * i + frow] = make_float2(m, s);
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < BM; r += 64 * NW) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < WGN; ++w) m = fmaxf(m, red[w * BM + r].x);
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < WGN; ++w) {
+        const float2 e = red[w * BM + r];
+        if (e.x != -INFINITY) s += e.y * __builtin_amdgcn_exp2f((e.x - m) * kLog2e);
+        else s += e.y;     // 0, or NaN
+      }
+      const int row = ml + r;
+      if (row >= m0 && row < p.M) p.part[(int64_t)tn * p.M + row] = make_float2(m, s);
+    }
+  } else if constexpr (EPI == kAcc) {
+    float* const base = p.acc + (int64_t)split * p.M * p.N;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int r = row0 + 16 * i;
+      if (r < m0 || r >= p.M) continue;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        // N is a multiple of 64 and a window starts on a multiple of 64, so
+        // four columns are all this tile's or none is
+        const int n = col0 + 16 * j;
+        if (n < n0 || n >= p.N) continue;
+        float4* const at = (float4*)(base + (int64_t)r * p.N + n);
+        float4 o = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+        if (p.add) {
+          const float4 e = *at;
+          o.x += e.x; o.y += e.y; o.z += e.z; o.w += e.w;
+        }
+        *at = o;
+      }
+    }
+  } else {
+    float scale = 1.f;
+    if constexpr (EPI == kOut) scale = *p.scale;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int r = row0 + 16 * i;
+      if (r < m0 || r >= p.M) continue;
+      float lse = 0.f, weight = 0.f;
+      int tgt = -1;
+      if constexpr (EPI == kGrad) {
+        const float2 info = p.row[r];
+        lse = info.x;
+        weight = info.y;
+        tgt = p.local_target[r] - p.v0;
+      }
+      uint16_t* const out = (uint16_t*)p.out + (int64_t)r * p.ldo;
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int n = col0 + 16 * j;
+        float val[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if constexpr (EPI == kGrad) {
+            float e = __builtin_amdgcn_exp2f((acc[i][j][v] - lse) * kLog2e);
+            if (n + v == tgt) e -= 1.f;
+            // a row of weight zero (an ignored target) has no gradient, whatever its logits
+            val[v] = weight == 0.f ? 0.f : e * weight;
+          } else {
+            val[v] = acc[i][j][v] * scale;
+          }
+        }
+        if (n >= n0 && n + 3 < p.N && (n & 3) == 0) {
+          *(uint2*)(out + n) = make_uint2(pack_bf16x2_rne(val[0], val[1]), pack_bf16x2_rne(val[2], val[3]));
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (n + v >= n0 && n + v < p.N) out[n + v] = (uint16_t)f32_to_bf16_rne(val[v]);
+        }
+      }
+    }
+  }
+}
+
+// Joins the tiles' (max, sum) of 16 tokens: 64 threads a token over the
+// tiles, then over the threads in a fixed order.
+__global__ __launch_bounds__(1024) void xent_join_kernel(const float2* __restrict__ part, int tiles,
+                                                         int T, int64_t V,
+                                                         const float* __restrict__ target_logit,
+                                                         const int64_t* __restrict__ target,
+                                                         int64_t ignore_index, float* __restrict__ loss,
+                                                         float* __restrict__ lse) {
+  __shared__ float2 red[64][17];
+  const int c = threadIdx.x & 15, g = threadIdx.x >> 4;
+  const int t = blockIdx.x * 16 + c;
+  float m = -INFINITY, s = 0.f;
+  if (t < T) {
+    for (int i = g; i < tiles; i += 64) {
+      const float2 e = part[(int64_t)i * T + t];
+      const float top = fmaxf(m, e.x);
+      const float base = top == -INFINITY ? 0.f : top;
+      s = s * __builtin_amdgcn_exp2f((m - base) * kLog2e) + e.y * __builtin_amdgcn_exp2f((e.x - base) * kLog2e);
+      m = top;
+    }
+  }
+  red[g][c] = make_float2(m, s);
+  __syncthreads();
+  if (g == 0 && t < T) {
+    for (int i = 0; i < 64; ++i) m = fmaxf(m, red[i][c].x);
+    const float base = m == -INFINITY ? 0.f : m;
+    s = 0.f;
+    for (int i = 0; i < 64; ++i) s += red[i][c].y * __builtin_amdgcn_exp2f((red[i][c].x - base) * kLog2e);
+    const float l = base + __logf(s);
+    lse[t] = l;
+    const int64_t y = target[t];
+    float d = 0.f;
+    if (y != ignore_index) d = (y >= 0 && y < V) ? l - target_logit[t] : __builtin_nanf("");
+    loss[t] = d;
+  }
+}
+
+// scale = max |dloss| over the tokens that count, and per token (lse, dloss /
+// scale) and the target column; ignored and out-of-range targets get weight 0.
+__global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, const int64_t* __restrict__ target,
+                                                         int64_t ignore_index, const float* __restrict__ dloss,
+                                                         const float* __restrict__ lse, float2* __restrict__ row,
+                                                         int* __restrict__ local_target, float* __restrict__ scale) {
+  __shared__ float red[16];
+  float m = 0.f;
+  for (int t = threadIdx.x; t < T; t += 1024) {
+    const int64_t y = target[t];
+    if (y != ignore_index && y >= 0 && y < V) m = fmaxf(m, fabsf(dloss[t]));
+  }
+  m = wave_max(m);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  m = 0.f;
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, red[i]);
+  if (threadIdx.x == 0) *scale = m;
+  for (int t = threadIdx.x; t < T; t += 1024) {
+    const int64_t y = target[t];
+    const bool counts = y != ignore_index && y >= 0 && y < V;
+    row[t] = make_float2(lse[t], counts && dloss[t] != 0.f ? dloss[t] / m : 0.f);
+    local_target[t] = counts ? (int)y : -1;
+  }
+}
+
+// out[c, r] = in[r, c] of bf16; rows past `rows` up to `rows_pad` come out as
+// zeros, so that a contraction over them is unchanged.  64 x 64 tiles through
+// LDS, 8-byte reads and writes.
+__global__ __launch_bounds__(256) void transpose_bf16_kernel(const uint16_t* __restrict__ in, int64_t ld_in,
+                                                             int rows, int rows_pad, int cols,
+                                                             uint16_t* __restrict__ out, int64_t ld_out) {
+  __shared__ uint16_t tile[64][68];
+  const int c0 = blockIdx.y * 64, r0 = blockIdx.x * 64;
+  const int x = (threadIdx.x & 15) * 4, y = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + y + 16 * i;
+    uint16_t e[4] = {0, 0, 0, 0};
+    if (r < rows) {
+      const uint16_t* const src = in + (int64_t)r * ld_in + c0 + x;
+      if (c0 + x + 3 < cols && ((uintptr_t)src & 7) == 0) {
+        const uint2 u = *(const uint2*)src;
+        e[0] = u.x & 0xFFFF; e[1] = u.x >> 16; e[2] = u.y & 0xFFFF; e[3] = u.y >> 16;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (c0 + x + k < cols) e[k] = src[k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tile[x + k][y + 16 * i] = e[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int c = c0 + y + 16 * i;
+    if (c < cols && r0 + x < rows_pad)   // rows_pad is a multiple of 64
+      *(uint2*)(out + (int64_t)c * ld_out + r0 + x) = *(const uint2*)&tile[y + 16 * i][x];
+  }
+}
+
+// Zeros in columns [c0, c1) of bf16 rows, one wave a row.
+__global__ __launch_bounds__(256) void zero_columns_kernel(uint16_t* out, int64_t ld, int64_t rows, int64_t c0,
+                                                           int64_t c1) {
+  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (r >= rows) return;
+  for (int64_t c = c0 + (threadIdx.x & 63); c < c1; c += 64) out[r * ld + c] = 0;
+}
+
+// dH = scale * sum over the splits of their fp32 shares, to bf16.
+__global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ acc, int splits, int64_t T,
+                                                      int64_t K, const float* __restrict__ scale,
+                                                      uint16_t* __restrict__ dh, int64_t ld_dh) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= T * K) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < splits; ++k) {
+    const float4 e = *(const float4*)(acc + (int64_t)k * T * K + i);
+    s.x += e.x; s.y += e.y; s.z += e.z; s.w += e.w;
+  }
+  const float f = *scale;
+  const int64_t t = i / K;
+  *(uint2*)(dh + t * ld_dh + (i - t * K)) =
+      make_uint2(pack_bf16x2_rne(s.x * f, s.y * f), pack_bf16x2_rne(s.z * f, s.w * f));
+}
+
+constexpr int kCus = 256;
+
+// Large tiles once they fill half the chip's compute units; below that 64-row
+// tiles give four times the workgroups (and take any M and N).
+bool large_tiles(int64_t M, int64_t N) {
+  return M >= 256 && N >= 256 && ((M + 255) / 256) * ((N + 255) / 256) >= kCus / 2;
+}
+
+template <int EPI>
+hipError_t run_gemm(XentGemm p, int splits, hipStream_t stream) {
+  const bool large = large_tiles(p.M, p.N);
+  const int bm = large ? 256 : 64;
+  p.tiles_m = (p.M + bm - 1) / bm;
+  p.tiles_n = (p.N + 255) / 256;
+  p.kb_per_split = (p.kblocks + splits - 1) / splits;
+  const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)splits);
+  if (large) hipLaunchKernelGGL((xent_gemm_kernel<256, 256, 2, 4, false, EPI>), grid, dim3(512), 0, stream, p);
+  else hipLaunchKernelGGL((xent_gemm_kernel<64, 256, 1, 4, true, EPI>), grid, dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
+int64_t pad64(int64_t n) { return (n + 63) & ~(int64_t)63; }
+size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Vocabulary columns per piece: as many as keep G, its transpose and W's
+// transpose at 256 MB each (the memory-side cache's size), in whole tiles.
+constexpr int64_t kPieceBytes = (int64_t)256 << 20;
+
+struct XentLayout {
+  int64_t tp, piece, vp;       // padded tokens, columns of a piece, padded
+  int64_t ld_ht, ld_g, ld_gt, ld_wt;
+  int splits;                  // of dH's contraction over the piece
+  size_t part, logit, row, target, scale, ht, g, gt, wt, acc, total;
+};
+
+XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
+  XentLayout L = {};
+  size_t off = 0;
+  auto take = [&](size_t bytes) { const size_t at = off; off += pad256(bytes); return at; };
+  if (!backward) {
+    L.part = take((size_t)((V + 255) / 256) * T * sizeof(float2));
+    L.logit = take((size_t)T * 4);
+    L.total = off;
+    return L;
+  }
+  L.tp = pad64(T);
+  int64_t piece = kPieceBytes / 2 / (L.tp > K ? L.tp : K) / 256 * 256;
+  if (piece < 256) piece = 256;
+  if (piece > V) piece = V;
+  const int64_t n = (V + piece - 1) / piece;
+  if (n > 1) piece = ((V + n - 1) / n + 255) / 256 * 256;   // even pieces
+  L.piece = piece;
+  L.vp = pad64(piece);
+  // an odd number of 128-byte lines a row: rows do not all start on one memory channel
+  L.ld_ht = L.ld_gt = (L.tp / 64 | 1) * 64;
+  L.ld_g = L.ld_wt = (L.vp / 64 | 1) * 64;
+  const bool large = large_tiles(T, K);
+  const int64_t tiles = ((T + (large ? 255 : 63)) / (large ? 256 : 64)) * ((K + 255) / 256);
+  int64_t s = kCus / tiles, most = L.vp / 64 / 8;   // at least 8 slabs a split
+  if (s > most) s = most;
+  L.splits = s < 1 ? 1 : (int)s;
+  L.row = take((size_t)T * sizeof(float2));
+  L.target = take((size_t)T * 4);
+  L.scale = take(4);
+  L.ht = take((size_t)K * L.ld_ht * 2);
+  L.g = take((size_t)T * L.ld_g * 2);
+  L.gt = take((size_t)L.piece * L.ld_gt * 2);
+  L.wt = take((size_t)K * L.ld_wt * 2);
+  L.acc = take((size_t)L.splits * T * K * 4);
+  L.total = off;
+  return L;
+}
+
+hipError_t transpose(const void* in, int64_t ld_in, int64_t rows, int64_t cols, void* out, int64_t ld_out,
+                     hipStream_t stream) {
+  const int64_t rp = pad64(rows);
+  hipLaunchKernelGGL(transpose_bf16_kernel, dim3((unsigned)(rp / 64), (unsigned)((cols + 63) / 64)), dim3(256), 0,
+                     stream, (const uint16_t*)in, ld_in, (int)rows, (int)rp, (int)cols, (uint16_t*)out, ld_out);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t xent_ws_bytes(int64_t T, int64_t V, int64_t K, bool backward) {
+  return xent_layout(T, V, K, backward).total;
+}
+
+hipError_t launch_xent_fwd(const XentArgs& p, void* ws, hipStream_t stream) {
+  const XentLayout L = xent_layout(p.T, p.V, p.K, false);
+  uint8_t* const base = (uint8_t*)ws;
+  XentGemm g = {};
+  g.a = (const uint8_t*)p.h; g.lda = p.ld_h * 2;
+  g.b = (const uint8_t*)p.w; g.ldb = p.ld_w * 2;
+  g.M = (int)p.T; g.N = (int)p.V; g.kblocks = (int)(p.K / 64);
+  g.part = (float2*)(base + L.part);
+  g.target = p.target;
+  g.target_logit = (float*)(base + L.logit);
+  hipError_t e = run_gemm<kStats>(g, 1, stream);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(xent_join_kernel, dim3((unsigned)((p.T + 15) / 16)), dim3(1024), 0, stream, g.part,
+                     (int)((p.V + 255) / 256), (int)p.T, p.V, g.target_logit, p.target, p.ignore_index,
+                     p.loss, p.lse);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
+  const XentLayout L = xent_layout(p.T, p.V, p.K, true);
+  uint8_t* const base = (uint8_t*)ws;
+  float2* const row = (float2*)(base + L.row);
+  int* const target = (int*)(base + L.target);
+  float* const scale = (float*)(base + L.scale);
+  uint16_t* const ht = (uint16_t*)(base + L.ht);
+  uint16_t* const g = (uint16_t*)(base + L.g);
+  uint16_t* const gt = (uint16_t*)(base + L.gt);
+  uint16_t* const wt = (uint16_t*)(base + L.wt);
+  float* const acc = (float*)(base + L.acc);
+  hipLaunchKernelGGL(xent_rows_kernel, dim3(1), dim3(1024), 0, stream, (int)p.T, p.V, p.target,
+                     p.ignore_index, p.dloss, p.lse, row, target, scale);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (p.dw && (e = transpose(p.h, p.ld_h, p.T, p.K, ht, L.ld_ht, stream)) != hipSuccess) return e;
+  for (int64_t v0 = 0; v0 < p.V; v0 += L.piece) {
+    const int64_t nv = p.V - v0 < L.piece ? p.V - v0 : L.piece;
+    const uint16_t* const w = (const uint16_t*)p.w + v0 * p.ld_w;
+    XentGemm z = {};
+    z.a = (const uint8_t*)p.h; z.lda = p.ld_h * 2;
+    z.b = (const uint8_t*)w; z.ldb = p.ld_w * 2;
+    z.M = (int)p.T; z.N = (int)nv; z.kblocks = (int)(p.K / 64);
+    z.row = row; z.local_target = target; z.v0 = (int)v0;
+    z.out = g; z.ldo = L.ld_g;
+    if ((e = run_gemm<kGrad>(z, 1, stream)) != hipSuccess) return e;
+    if (p.dw) {
+      if ((e = transpose(g, L.ld_g, p.T, nv, gt, L.ld_gt, stream)) != hipSuccess) return e;
+      XentGemm d = {};
+      d.a = (const uint8_t*)gt; d.lda = L.ld_gt * 2;
+      d.b = (const uint8_t*)ht; d.ldb = L.ld_ht * 2;
+      d.M = (int)nv; d.N = (int)p.K; d.kblocks = (int)(L.tp / 64);
+      d.out = (uint16_t*)p.dw + v0 * p.ld_dw; d.ldo = p.ld_dw; d.scale = scale;
+      if ((e = run_gemm<kOut>(d, 1, stream)) != hipSuccess) return e;
+    }
+    if (p.dh) {
+      if (nv % 64) {
+        hipLaunchKernelGGL(zero_columns_kernel, dim3((unsigned)((p.T + 3) / 4)), dim3(256), 0, stream, g,
+                           L.ld_g, p.T, nv, pad64(nv));
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+      }
+      if ((e = transpose(w, p.ld_w, nv, p.K, wt, L.ld_wt, stream)) != hipSuccess) return e;
+      XentGemm d = {};
+      d.a = (const uint8_t*)g; d.lda = L.ld_g * 2;
+      d.b = (const uint8_t*)wt; d.ldb = L.ld_wt * 2;
+      d.M = (int)p.T; d.N = (int)p.K; d.kblocks = (int)(pad64(nv) / 64);
+      d.acc = acc; d.add = v0 > 0;
+      if ((e = run_gemm<kAcc>(d, L.splits, stream)) != hipSuccess) return e;
+    }
+  }
+  if (!p.dh) return hipSuccess;
+  hipLaunchKernelGGL(xent_dh_kernel, dim3((unsigned)((p.T * p.K / 4 + 255) / 256)), dim3(256), 0, stream, acc,
+                     L.splits, p.T, p.K, scale, (uint16_t*)p.dh, p.ld_dh);
+  return hipGetLastError();
+}
+
+hipError_t launch_zero_rows_bf16(void* out, int64_t rows, int64_t cols, int64_t ld, hipStream_t stream) {
+  hipLaunchKernelGGL(zero_columns_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, (uint16_t*)out,
+                     ld, rows, (int64_t)0, cols);
+  return hipGetLastError();
+}
+
+}  // namespace fp8bw

@@ -5,10 +5,11 @@ the current HIP stream, and raises FP8BWError on a non-OK status.  Every step
 of the computation runs in the HIP kernels of libfp8bw.so."""
 
 import functools
+from typing import NamedTuple, Optional
 
 import torch
 
-from ._lib import check, load_library
+from ._lib import AdamwTensor, check, load_library
 
 BLOCKS = {"1x128": 0, "128x128": 1}
 OUT_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
@@ -493,3 +494,234 @@ def fp8_linear_wgrad(dy, x, ws=None):
     K = x.shape[1]
     _check_shape(x, (M, K), "x")
     return _linear("fp8_linear_wgrad", 2, dy, x, (N, K), M, N, K, ws)
+
+
+# ---------------------------------------------------------------------------
+# The operators around the linear in a training step (include/fp8bw.h):
+# RMS norm, vocabulary cross entropy, AdamW.
+
+class RMSNormOut(NamedTuple):
+    """Outputs of rms_norm_fwd; what was not asked for is None."""
+    s: torch.Tensor                  # x + residual in bf16 (x itself without a residual)
+    rstd: torch.Tensor               # fp32 [rows]
+    y: Optional[torch.Tensor]        # bf16 [rows, cols]
+    q: Optional[torch.Tensor]        # uint8 codes [rows, cols]
+    recip: Optional[torch.Tensor]    # fp32 [rows, ceil(cols / 128)], column-major
+    qt: Optional[torch.Tensor]       # uint8 codes [cols, rows]
+    recip_t: Optional[torch.Tensor]  # fp32 [cols, ceil(rows / 128)], column-major
+
+
+def _bf16_matrix(t, name, shape=None):
+    _rowmajor(t, name)
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bf16")
+    if shape is not None:
+        _check_shape(t, shape, name)
+
+
+def _norm_weight(weight, cols):
+    if weight.dim() != 1 or weight.dtype not in OUT_DTYPES or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous bf16 or float32 vector")
+    _check_shape(weight, (cols,), "weight")
+
+
+def _vector(t, n, dtype, name):
+    if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} vector")
+    _check_shape(t, (n,), name)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _ld(t):
+    return 0 if t is None else t.stride(0)
+
+
+@_on_tensor_device
+def rms_norm_fwd(x, weight, residual=None, eps=1e-6, y=True, q=False, qt=False, s=None):
+    """RMS norm of s = x + residual (bf16) times weight, as RMSNormOut.
+
+    x, residual bf16 [rows, cols] (unit column stride); weight bf16 or fp32
+    [cols].  y, q, qt choose the outputs: bf16, E4M3 codes in 1x128 blocks
+    along the columns, and transposed codes in 1x128 blocks along the rows
+    (rows % 16 == 0).  s: where to write x + residual, possibly x or residual
+    itself (default: a new tensor)."""
+    lib = load_library()
+    _need_cuda(x, weight)
+    _bf16_matrix(x, "x")
+    rows, cols = x.shape
+    _norm_weight(weight, cols)
+    dev = x.device
+    if residual is not None:
+        _bf16_matrix(residual, "residual", (rows, cols))
+        if s is None:
+            s = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+        _bf16_matrix(s, "s", (rows, cols))
+    elif s is not None:
+        raise ValueError("s is written only with a residual")
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    ty = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if y else None
+    tq = torch.empty((rows, cols), dtype=torch.uint8, device=dev) if q else None
+    tr = colmajor_empty(rows, _cdiv(cols, 128), dev) if q else None
+    tqt = torch.empty((cols, rows), dtype=torch.uint8, device=dev) if qt else None
+    trt = colmajor_empty(cols, _cdiv(rows, 128), dev) if qt else None
+    check(lib.fp8bw_rms_norm_fwd(
+        x.data_ptr(), x.stride(0), _ptr(residual), _ld(residual), weight.data_ptr(),
+        OUT_DTYPES[weight.dtype], float(eps), rows, cols, _ptr(s), _ld(s), rstd.data_ptr(),
+        _ptr(ty), _ld(ty), _ptr(tq), _ld(tq), _ptr(tr), tr.stride(0) if q else 0,
+        tr.stride(1) if q else 0, _ptr(tqt), _ld(tqt), _ptr(trt), trt.stride(0) if qt else 0,
+        trt.stride(1) if qt else 0, _stream(x)))
+    return RMSNormOut(x if residual is None else s, rstd, ty, tq, tr, tqt, trt)
+
+
+@_on_tensor_device
+def rms_norm_bwd(dy, s, rstd, weight, dres=None):
+    """(dx, dweight) of rms_norm_fwd from dy, its s and rstd, and dres, the
+    gradient that reaches s past the norm (or None).  dx bf16 is the gradient
+    of x and of the residual; dweight has the weight's type."""
+    lib = load_library()
+    _need_cuda(dy, s, rstd, weight)
+    _bf16_matrix(dy, "dy")
+    rows, cols = dy.shape
+    _bf16_matrix(s, "s", (rows, cols))
+    _vector(rstd, rows, torch.float32, "rstd")
+    _norm_weight(weight, cols)
+    if dres is not None:
+        _bf16_matrix(dres, "dres", (rows, cols))
+    dx = torch.empty((rows, cols), dtype=torch.bfloat16, device=dy.device)
+    if rows == 0:
+        return dx, torch.zeros_like(weight)
+    dweight = torch.empty_like(weight)
+    nws = lib.fp8bw_rms_norm_bwd_ws_bytes(rows, cols)
+    ws = torch.empty(max(nws, 1), dtype=torch.uint8, device=dy.device)
+    check(lib.fp8bw_rms_norm_bwd(dy.data_ptr(), dy.stride(0), s.data_ptr(), s.stride(0),
+                                 rstd.data_ptr(), weight.data_ptr(), OUT_DTYPES[weight.dtype],
+                                 _ptr(dres), _ld(dres), rows, cols, dx.data_ptr(), dx.stride(0),
+                                 dweight.data_ptr(), ws.data_ptr(), nws, _stream(dy)))
+    return dx, dweight
+
+
+def _check_xent(h, w, target):
+    _need_cuda(h, w, target)
+    _bf16_matrix(h, "h")
+    T, K = h.shape
+    _bf16_matrix(w, "w")
+    _check_shape(w, (w.shape[0], K), "w")
+    _vector(target, T, torch.int64, "target")
+    return T, w.shape[0], K
+
+
+@_on_tensor_device
+def linear_xent_fwd(h, w, target, ignore_index=-100):
+    """(loss, lse), both fp32 [T], of softmax cross entropy with logits
+    h . w^T: h bf16 [T, K], w bf16 [V, K], target int64 [T].  A token whose
+    target is ignore_index has loss 0; any other target outside the
+    vocabulary gives NaN."""
+    lib = load_library()
+    T, V, K = _check_xent(h, w, target)
+    loss = torch.empty(T, dtype=torch.float32, device=h.device)
+    lse = torch.empty(T, dtype=torch.float32, device=h.device)
+    nws = lib.fp8bw_linear_xent_ws_bytes(T, V, K, 0)
+    ws = torch.empty(max(nws, 1), dtype=torch.uint8, device=h.device)
+    check(lib.fp8bw_linear_xent_fwd(h.data_ptr(), h.stride(0), w.data_ptr(), w.stride(0),
+                                    target.data_ptr(), int(ignore_index), T, V, K, loss.data_ptr(),
+                                    lse.data_ptr(), ws.data_ptr(), nws, _stream(h)))
+    return loss, lse
+
+
+@_on_tensor_device
+def linear_xent_bwd(dloss, h, w, target, lse, ignore_index=-100, need_dh=True, need_dw=True):
+    """(dh, dw), bf16, of linear_xent_fwd from dloss fp32 [T], one weight per
+    token's loss, and the forward's lse; a gradient not needed is None."""
+    lib = load_library()
+    T, V, K = _check_xent(h, w, target)
+    _need_cuda(dloss, lse)
+    _vector(dloss, T, torch.float32, "dloss")
+    _vector(lse, T, torch.float32, "lse")
+    dh = torch.empty((T, K), dtype=torch.bfloat16, device=h.device) if need_dh else None
+    dw = torch.empty((V, K), dtype=torch.bfloat16, device=h.device) if need_dw else None
+    nws = lib.fp8bw_linear_xent_ws_bytes(T, V, K, 1)
+    ws = torch.empty(max(nws, 1), dtype=torch.uint8, device=h.device)
+    check(lib.fp8bw_linear_xent_bwd(dloss.data_ptr(), h.data_ptr(), h.stride(0), w.data_ptr(),
+                                    w.stride(0), target.data_ptr(), int(ignore_index),
+                                    lse.data_ptr(), T, V, K, _ptr(dh), _ld(dh), _ptr(dw), _ld(dw),
+                                    ws.data_ptr(), nws, _stream(h)))
+    return dh, dw
+
+
+def adamw_scales(n):
+    """Scales of n elements of 8-bit AdamW state."""
+    return _cdiv(n, 128)
+
+
+def _adamw_list(ts, n, name):
+    if len(ts) != n:
+        raise ValueError(f"{len(ts)} {name} for {n} params")
+    return ts
+
+
+def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
+               weight_decay=0.0, exp_avg_scales=None, root_scales=None, masters=None,
+               grad_scale=None, seed=None):
+    """One AdamW step over lists of contiguous tensors, in place.
+
+    params and grads bf16 or fp32.  With fp32 exp_avgs and exp_avg_sqs the
+    states are the moments; with uint8 (or float8_e4m3fn) ones they are E4M3
+    codes of m and of sqrt(v), whose scales per 128 elements (adamw_scales)
+    are exp_avg_scales and root_scales.  masters: fp32 weights behind bf16
+    params (a list, None for tensors without one).  grad_scale: one-element
+    fp32 tensor that multiplies every gradient.  seed: a new integer each step
+    to round codes and bf16 params at random; None rounds to nearest."""
+    lib = load_library()
+    n = len(params)
+    if n == 0:
+        return
+    eight = exp_avgs[0].dtype in CODE_DTYPES if len(exp_avgs) else False
+    if eight != (exp_avg_scales is not None) or eight != (root_scales is not None):
+        raise ValueError("exp_avg_scales and root_scales belong to 8-bit states")
+    for ts, name in ((grads, "grads"), (exp_avgs, "exp_avgs"), (exp_avg_sqs, "exp_avg_sqs"),
+                     (exp_avg_scales, "exp_avg_scales"), (root_scales, "root_scales"),
+                     (masters, "masters")):
+        if ts is not None:
+            _adamw_list(ts, n, name)
+    device = params[0].device
+    arr = (AdamwTensor * n)()
+    none = [None] * n
+    state_dtypes = CODE_DTYPES if eight else (torch.float32,)
+    for d, p, g, m, v, ms, rs, w in zip(arr, params, grads, exp_avgs, exp_avg_sqs,
+                                        exp_avg_scales or none, root_scales or none,
+                                        masters or none):
+        numel = p.numel()
+        for t in (p, g, m, v):
+            if t.device != device or not t.is_cuda:
+                raise ValueError("fp8bw ops take CUDA (HIP) tensors on one device")
+            if not t.is_contiguous() or t.numel() != numel:
+                raise ValueError("params, grads and states must be contiguous and of equal size")
+        if m.dtype not in state_dtypes or v.dtype not in state_dtypes:
+            raise ValueError("states must all be float32, or all be E4M3 codes")
+        if p.dtype not in OUT_DTYPES or g.dtype not in OUT_DTYPES:
+            raise ValueError("params and grads must be bfloat16 or float32")
+        if eight:
+            for t in (ms, rs):
+                if t.device != device:
+                    raise ValueError("fp8bw ops take CUDA (HIP) tensors on one device")
+                _vector(t, _cdiv(numel, 128), torch.float32, "scales")
+            d.exp_avg_scale, d.root_scale = ms.data_ptr(), rs.data_ptr()
+        if w is not None:
+            if w.device != device or w.dtype != torch.float32 or not w.is_contiguous() or w.numel() != numel:
+                raise ValueError("masters must be contiguous float32 tensors like params")
+            d.master = w.data_ptr()
+        d.param, d.grad, d.exp_avg, d.exp_avg_sq = p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr()
+        d.numel = numel
+        d.param_dtype, d.grad_dtype = OUT_DTYPES[p.dtype], OUT_DTYPES[g.dtype]
+    if grad_scale is not None and (grad_scale.device != device or grad_scale.dtype != torch.float32
+                                   or grad_scale.numel() != 1):
+        raise ValueError("grad_scale must be a one-element float32 tensor on the params' device")
+    with torch.cuda.device(device):
+        check(lib.fp8bw_adamw_step(arr, n, int(eight), int(step), float(lr), float(beta1),
+                                   float(beta2), float(eps), float(weight_decay), _ptr(grad_scale),
+                                   int(seed is not None),
+                                   0 if seed is None else int(seed) & 0xFFFFFFFFFFFFFFFF,
+                                   _stream(params[0])))

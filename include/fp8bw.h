@@ -397,6 +397,138 @@ int fp8_linear_bwd(const void* dy, const void* w, const void* saved, size_t save
                    void* dw, int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
                    void* stream);
 
+/*
+ * fp8bw_rms_norm_fwd -- root-mean-square norm in front of an FP8 linear, with
+ * the residual's addition and the linear's operand codes from the same pass:
+ *
+ *   s[r, c]  = bf16(x[r, c] + residual[r, c])     (s = x without a residual)
+ *   rstd[r]  = 1 / sqrt(mean_c s[r, c]^2 + eps)
+ *   v[r, c]  = s[r, c] * rstd[r] * weight[c]      (fp32)
+ *   y = bf16(v); (q, recip) = codes of v in 1x128 blocks along the columns;
+ *   (qt, recip_t) = codes of v^T in 1x128 blocks along the rows
+ *
+ *   x, residual  device bf16 [rows, cols] (ld_x, ld_res); residual may be NULL.
+ *   sum          device bf16 [rows, cols] (ld_sum): s.  Required with a
+ *                residual, not used without; it may be x or residual itself
+ *                (same pointer and leading dimension), no other overlap.
+ *   weight       device [cols], bf16 (weight_dtype FP8BW_OUT_BF16) or fp32
+ *                (FP8BW_OUT_F32), 16-byte aligned.
+ *   rstd         device fp32 [rows], for the backward.
+ *   y, q, qt     outputs, each may be NULL: y bf16 (ld_y); q E4M3 [rows, cols]
+ *                (ld_q) with recip[r*rs_row + kb*rs_kb]; qt E4M3 [cols, rows]
+ *                (ld_qt) with recip_t[c*rst_row + mb*rst_kb].  The codes
+ *                follow the quantizers' recipe on the fp32 v (not on y).
+ *   Requires cols % 16 == 0, cols <= 32768, and rows % 16 == 0 with qt (one
+ *   more launch, which reads s again).  eps >= 0.
+ */
+int fp8bw_rms_norm_fwd(const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
+                       const void* weight, int weight_dtype, float eps, int64_t rows, int64_t cols,
+                       void* sum, int64_t ld_sum, float* rstd, void* y, int64_t ld_y, void* q,
+                       int64_t ld_q, float* recip, int64_t rs_row, int64_t rs_kb, void* qt,
+                       int64_t ld_qt, float* recip_t, int64_t rst_row, int64_t rst_kb,
+                       void* stream);
+
+/*
+ * fp8bw_rms_norm_bwd -- its gradients (codes pass gradients straight through):
+ *   h = s * rstd, d = dy * weight
+ *   dx[r, c]   = bf16(rstd * (d - h * mean_c(d * h)) + dres)
+ *   dweight[c] = sum_r dy * h                (in the weight's type)
+ * dx is the gradient of x and of the residual alike.
+ *
+ *   dy, s, dres  device bf16 [rows, cols]; dres, the gradient that reaches s
+ *                past the norm, may be NULL.  rstd as the forward wrote it.
+ *   dx           device bf16 [rows, cols]; dweight device [cols].
+ *   ws           fp8bw_rms_norm_bwd_ws_bytes(rows, cols) bytes, 16-byte
+ *                aligned (fp32 partial sums of dweight, joined in a fixed
+ *                order: results repeat bit for bit).
+ * With rows == 0 dweight is not written.
+ */
+size_t fp8bw_rms_norm_bwd_ws_bytes(int64_t rows, int64_t cols);
+int fp8bw_rms_norm_bwd(const void* dy, int64_t ld_dy, const void* s, int64_t ld_s,
+                       const float* rstd, const void* weight, int weight_dtype, const void* dres,
+                       int64_t ld_dres, int64_t rows, int64_t cols, void* dx, int64_t ld_dx,
+                       void* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * fp8bw_linear_xent_fwd / _bwd -- softmax cross entropy of a linear head over
+ * a large vocabulary, logits z = h . w^T, without keeping the logits:
+ *
+ *   lse[t]  = log sum_v exp(z[t, v]);  loss[t] = lse[t] - z[t, target[t]]
+ *   G[t, v] = (exp(z[t, v] - lse[t]) - [v == target[t]]) * dloss[t]
+ *   dh = G . w,  dw = G^T . h
+ *
+ *   h, w     device bf16 [T, K] (ld_h) and [V, K] (ld_w).
+ *   target   device int64 [T].  A target equal to ignore_index gives loss 0
+ *            and no gradient.  Any other target outside [0, V) gives a NaN
+ *            loss and no gradient.
+ *   loss, lse, dloss  device fp32 [T]; one loss per token, so that a caller's
+ *            mean, sum or weights are dloss.
+ *   dh, dw   device bf16 [T, K] (ld_dh) and [V, K] (ld_dw); either may be NULL.
+ *   The backward takes the vocabulary in pieces: each piece's logits are made
+ *   again and become its part of G (bf16) in the workspace, whose size does
+ *   not grow with V beyond one piece.
+ *   ws       fp8bw_linear_xent_ws_bytes(T, V, K, backward) bytes, 256-byte
+ *            aligned (backward: 0 or 1).
+ *   Requires K % 64 == 0, 64 <= K <= 2^20, V <= 2^28, T <= 2^24, leading
+ *   dimensions a multiple of 8 and at most 2^22 - K / 128, and
+ *   ceil(T / 64) * ceil(V / 256) < 2^31.  With V == 0 every call with T > 0 is
+ *   rejected (an empty sum has no logarithm); with T == 0 dw is set to zero.
+ */
+size_t fp8bw_linear_xent_ws_bytes(int64_t T, int64_t V, int64_t K, int backward);
+int fp8bw_linear_xent_fwd(const void* h, int64_t ld_h, const void* w, int64_t ld_w,
+                          const int64_t* target, int64_t ignore_index, int64_t T, int64_t V,
+                          int64_t K, float* loss, float* lse, void* ws, size_t ws_bytes,
+                          void* stream);
+int fp8bw_linear_xent_bwd(const float* dloss, const void* h, int64_t ld_h, const void* w,
+                          int64_t ld_w, const int64_t* target, int64_t ignore_index,
+                          const float* lse, int64_t T, int64_t V, int64_t K, void* dh,
+                          int64_t ld_dh, void* dw, int64_t ld_dw, void* ws, size_t ws_bytes,
+                          void* stream);
+
+/*
+ * fp8bw_adamw_step -- one AdamW step over many tensors, in place:
+ *
+ *   g = grad * grad_scale[0]                       (1 if grad_scale is NULL)
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *
+ *   tensors  host array of `count`; each is contiguous, at the alignment of
+ *            its elements.  p is the fp32 master where there is one (param,
+ *            bf16, then receives its rounding), else param.
+ *   state    FP8BW_STATE_F32: exp_avg and exp_avg_sq are fp32 [numel].
+ *            FP8BW_STATE_E4M3: they hold E4M3 codes [numel] of m and of
+ *            sqrt(v), with fp32 scales [ceil(numel / 128)] per 128 elements,
+ *            m = code * exp_avg_scale, sqrt(v) = code * root_scale; the step
+ *            writes power-of-two scales, the least that hold the block's
+ *            largest value within 448 (1 for a block of zeros).  A positive
+ *            sqrt(v) is never rounded to code 0.  Codes 0 with any finite
+ *            scale are the start.
+ *   stochastic  nonzero: codes, and bf16 parameters without a master, are
+ *            rounded up or down at random, in proportion to the remainder, by
+ *            16 bits per value of a hash of (seed, index of the tensor in
+ *            `tensors`, element).  Equal arguments give equal results; use
+ *            another seed each step.  Zero: to nearest.
+ *   step     counts from 1.  lr, weight_decay and eps >= 0; 0 <= beta1, beta2 < 1.
+ * One launch per 40 tensors.
+ */
+typedef enum { FP8BW_STATE_F32 = 0, FP8BW_STATE_E4M3 = 1 } fp8bw_state;
+typedef struct {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale; /* NULL with fp32 states */
+  float* root_scale;    /* NULL with fp32 states */
+  float* master;        /* NULL: none */
+  int64_t numel;
+  int param_dtype;      /* fp8bw_out */
+  int grad_dtype;       /* fp8bw_out */
+} fp8bw_adamw_tensor;
+int fp8bw_adamw_step(const fp8bw_adamw_tensor* tensors, int count, int state, int64_t step,
+                     double lr, double beta1, double beta2, double eps, double weight_decay,
+                     const float* grad_scale, int stochastic, uint64_t seed, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
