@@ -128,28 +128,37 @@ __device__ __forceinline__ int scale_exponent(float amax) {
   return max(-126, min(127, e));
 }
 
-// A value on the E4M3 grid next to y: to nearest, or with RANDOM up with the
-// probability of the remainder (r16: 16 random bits).  |y| <= 448.
-template <bool RANDOM, bool KEEP>
-__device__ __forceinline__ float to_e4m3_grid(float y, uint32_t r16) {
-  const float a = fabsf(y);
-  // spacing of the grid at a: 2^(e - 3), e the exponent of a, at least -6
-  const int e = max((int)(__float_as_uint(a) >> 23) - 127, -6) - 3;
-  float steps = __builtin_amdgcn_ldexpf(a, -e);
-  if constexpr (RANDOM) steps = __builtin_floorf(steps + (float)r16 * 0x1p-16f);
-  else steps = __builtin_rintf(steps);
-  float v = __builtin_amdgcn_ldexpf(steps, e);
-  if constexpr (KEEP) v = a > 0.f ? fmaxf(v, 0x1p-9f) : v;
-  return __builtin_copysignf(v, y);
-}
-
+// 8 values times 2^-exponent as E4M3 codes, magnitudes at most 448.  RANDOM:
+// v_cvt_sr_fp8_f32 adds its random number, aligned to the bits that the code
+// drops, and cuts: up with the probability of the remainder in units of
+// 2^-16, subnormal codes included (checked on the GPU against that definition
+// on a million values of 22 octaves).  `shift` picks the 16 random bits.
+// KEEP: what is not zero gets at least the smallest code.
 template <bool RANDOM, bool KEEP>
 __device__ __forceinline__ uint2 encode8(const float (&f)[8], int exponent, const uint32_t (&rnd)[8], int shift) {
-  float v[8];
+  const float inv = __builtin_amdgcn_ldexpf(1.f, -exponent);
+  float y[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    v[j] = to_e4m3_grid<RANDOM, KEEP>(__builtin_amdgcn_ldexpf(f[j], -exponent), (rnd[j] >> shift) & 0xFFFF);
-  return make_uint2(cvt4_e4m3(v[0], v[1], v[2], v[3]), cvt4_e4m3(v[4], v[5], v[6], v[7]));
+  for (int j = 0; j < 8; ++j) {
+    y[j] = f[j] * inv;
+    if constexpr (KEEP) y[j] = f[j] > 0.f ? fmaxf(y[j], 0x1p-9f) : 0.f;
+  }
+  if constexpr (!RANDOM) {
+    return make_uint2(cvt4_e4m3(y[0], y[1], y[2], y[3]), cvt4_e4m3(y[4], y[5], y[6], y[7]));
+  } else {
+    uint32_t r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = shift ? rnd[j] & 0xFFFF0000u : rnd[j] << 16;
+    int lo = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], r[0], 0, 0);
+    lo = __builtin_amdgcn_cvt_sr_fp8_f32(y[1], r[1], lo, 1);
+    lo = __builtin_amdgcn_cvt_sr_fp8_f32(y[2], r[2], lo, 2);
+    lo = __builtin_amdgcn_cvt_sr_fp8_f32(y[3], r[3], lo, 3);
+    int hi = __builtin_amdgcn_cvt_sr_fp8_f32(y[4], r[4], 0, 0);
+    hi = __builtin_amdgcn_cvt_sr_fp8_f32(y[5], r[5], hi, 1);
+    hi = __builtin_amdgcn_cvt_sr_fp8_f32(y[6], r[6], hi, 2);
+    hi = __builtin_amdgcn_cvt_sr_fp8_f32(y[7], r[7], hi, 3);
+    return make_uint2((uint32_t)lo, (uint32_t)hi);
+  }
 }
 
 // One workgroup takes `iters` runs of 2048 elements of one tensor; a thread's
@@ -196,20 +205,24 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamwLaunch L) {
       const float gj = g[j] * gs;
       m[j] = m[j] * L.beta1 + gj * L.one_minus_beta1;
       v[j] = v[j] * L.beta2 + gj * gj * L.one_minus_beta2;
-      root[j] = __builtin_sqrtf(v[j]);
-      p[j] = p[j] * L.decay - m[j] / (root[j] * L.root_factor + L.eps) * L.step_size;
+      // Hardware square root and reciprocal, each within 1 ulp (9.2e-8 and
+      // 9.0e-8 measured): the step they form is far smaller than p, and with
+      // IEEE forms the 8-bit kernel was bound by its arithmetic.
+      root[j] = __builtin_amdgcn_sqrtf(v[j]);
+      p[j] = p[j] * L.decay - m[j] * __builtin_amdgcn_rcpf(root[j] * L.root_factor + L.eps) * L.step_size;
       rnd[j] = RANDOM ? mix32(T.key + (uint32_t)i + j) : 0u;
     }
     if constexpr (EIGHT) {
-      float am = 0.f, ar = 0.f;
+      float am = 0.f, av = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (j < n) {
           am = fmaxf(am, fabsf(m[j]));
-          ar = fmaxf(ar, root[j]);
+          av = fmaxf(av, v[j]);
         }
       }
-      const int em = scale_exponent(row16_max(am)), er = scale_exponent(row16_max(ar));
+      // The root's scale comes from the correctly rounded root of the largest v.
+      const int em = scale_exponent(row16_max(am)), er = scale_exponent(__builtin_sqrtf(row16_max(av)));
       store8_codes((uint8_t*)T.m + at, n, encode8<RANDOM, false>(m, em, rnd, 0));
       store8_codes((uint8_t*)T.v + at, n, encode8<RANDOM, true>(root, er, rnd, 16));
       if ((threadIdx.x & 15) == 0) {

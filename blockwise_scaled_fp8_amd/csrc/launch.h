@@ -98,7 +98,7 @@ struct NormWeight {
   const void* p;   // bf16 or fp32 [cols]
   int f32;
 };
-constexpr int64_t kNormMaxCols = 32768;   // 1024 threads x 4 chunks of 8 columns
+constexpr int64_t kNormMaxCols = 16384;   // 1024 threads x 2 chunks of 8 columns
 struct NormFwdArgs {
   int64_t rows, cols;
   const uint16_t* x; int64_t ld_x;

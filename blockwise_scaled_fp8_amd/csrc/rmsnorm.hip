@@ -23,6 +23,14 @@
 
 namespace fp8bw {
 
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+// 16 bytes that nothing reads again soon: a load that leaves the caches alone.
+__device__ __forceinline__ uint4 load_stream(const uint16_t* p) {
+  const u32x4 t = __builtin_nontemporal_load((const u32x4*)p);
+  return make_uint4(t.x, t.y, t.z, t.w);
+}
+
 // Sum over the 16 lanes of a DPP row, then over the wavefront; every lane
 // receives the same value.
 __device__ __forceinline__ float row16_sum(float v) {
@@ -79,6 +87,36 @@ __device__ __forceinline__ void load_weight8(const NormWeight& w, int col, float
   }
 }
 
+// 8 weights as they are stored, kept packed between uses.
+template <bool F32>
+struct Weight8 {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const void* p, int col) {
+    if constexpr (F32) {
+      a = *(const uint4*)((const float*)p + col);
+      b = *(const uint4*)((const float*)p + col + 4);
+    } else {
+      a = *(const uint4*)((const uint16_t*)p + col);
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if constexpr (F32) {
+      f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
+      f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+      f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y);
+      f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+    } else {
+      unpack8(a, f);
+    }
+  }
+};
+
+// The compiler may not look through this: without it, it keeps a packed value's
+// 8 floats instead of its 4 registers across a reduction or a loop.
+__device__ __forceinline__ void keep_packed(uint4& u) {
+  asm volatile("" : "+v"(u.x), "+v"(u.y), "+v"(u.z), "+v"(u.w));
+}
+
 // v of 8 columns: the product order (s * rstd) * weight is the same in the
 // row kernel and the transposing kernel, so both quantize the same values.
 __device__ __forceinline__ void normed8(const uint4& s, float rstd, const float (&w)[8], float (&v)[8]) {
@@ -88,6 +126,13 @@ __device__ __forceinline__ void normed8(const uint4& s, float rstd, const float 
 }
 
 // ---------------------------------------------------------------------------
+// Which of a workgroup's rows this wave works on, known to be the same for all
+// its lanes: row addresses then stay in scalar registers.
+template <int TPR>
+__device__ __forceinline__ int row_slot() {
+  return TPR == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0;
+}
+
 // Forward, one row per TPR threads: thread t holds chunks t, t + TPR, .. of 8
 // columns, so a 16-lane DPP row holds one 1x128 block.  The row stays in
 // registers between the sum of squares and the outputs.
@@ -95,7 +140,7 @@ template <int TPR, int CH>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_fwd_kernel(const NormFwdArgs p) {
   constexpr int BLOCK = TPR < 256 ? 256 : TPR;
   __shared__ float red[BLOCK / 64];
-  const int64_t r = (int64_t)blockIdx.x * (BLOCK / TPR) + threadIdx.x / TPR;
+  const int64_t r = (int64_t)blockIdx.x * (BLOCK / TPR) + row_slot<TPR>();
   const int t = threadIdx.x % TPR;
   if (r >= p.rows) return;   // whole waves (TPR 64: no barrier; else one row a workgroup)
   const uint16_t* const x = p.x + r * p.ld_x;
@@ -104,7 +149,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_fwd_kernel(con
   for (int k = 0; k < CH; ++k) {
     const int col = (k * TPR + t) * 8;
     s[k] = make_uint4(0, 0, 0, 0);
-    if (col < p.cols) s[k] = *(const uint4*)(x + col);
+    if (col < p.cols) s[k] = load_stream(x + col);
   }
   if (p.residual) {
     const uint16_t* const res = p.residual + r * p.ld_res;
@@ -113,7 +158,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_fwd_kernel(con
     for (int k = 0; k < CH; ++k) {
       const int col = (k * TPR + t) * 8;
       u[k] = make_uint4(0, 0, 0, 0);
-      if (col < p.cols) u[k] = *(const uint4*)(res + col);
+      if (col < p.cols) u[k] = load_stream(res + col);
     }
     uint16_t* const sum = p.sum + r * p.ld_sum;
 #pragma unroll
@@ -239,36 +284,64 @@ __global__ __launch_bounds__(256) void rms_norm_quant_t_kernel(const NormFwdArgs
 // Backward: workgroup b takes rows b RPW + sub, + gridDim.x RPW, ..; a thread
 // keeps the weight gradient of its columns in registers over all its rows and
 // writes one partial row at the end, which a second kernel sums in order.
-template <int TPR, int CH>
+// While a row is reduced and written, the next row's s and dy are on their
+// way; rows stay packed in registers, and bf16 weights over all rows.
+template <int TPR, int CH, bool WF32>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_bwd_kernel(const NormBwdArgs p) {
   constexpr int BLOCK = TPR < 256 ? 256 : TPR;
   constexpr int RPW = BLOCK / TPR;
   __shared__ float red[2][BLOCK / 64];
-  const int sub = threadIdx.x / TPR, t = threadIdx.x % TPR;
+  const int sub = row_slot<TPR>(), t = threadIdx.x % TPR;
+  const int cols = (int)p.cols;
   float acc[CH][8] = {};
-  int flip = 0;
-  for (int64_t r = (int64_t)blockIdx.x * RPW + sub; r < p.rows; r += (int64_t)gridDim.x * RPW) {
-    uint4 u[CH], g[CH], e[CH];
+  Weight8<WF32> wk[CH];
+  if constexpr (!WF32) {
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int col = (k * TPR + t) * 8;
-      const bool in = col < p.cols;
-      u[k] = g[k] = e[k] = make_uint4(0, 0, 0, 0);
-      if (in) {
-        u[k] = *(const uint4*)(p.s + r * p.ld_s + col);
-        g[k] = *(const uint4*)(p.dy + r * p.ld_dy + col);
-        if (p.dres) e[k] = *(const uint4*)(p.dres + r * p.ld_dres + col);
+      wk[k].load(p.weight.p, col < cols ? col : 0);
+    }
+  }
+  uint4 u[CH], g[CH];
+  auto load_row = [&](int64_t r) {
+    const uint16_t* const s = p.s + r * p.ld_s;
+    const uint16_t* const dy = p.dy + r * p.ld_dy;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int col = (k * TPR + t) * 8;
+      u[k] = g[k] = make_uint4(0, 0, 0, 0);
+      if (col < cols) {
+        u[k] = load_stream(s + col);
+        g[k] = load_stream(dy + col);
       }
     }
+  };
+  int flip = 0;
+  const int64_t step = (int64_t)gridDim.x * RPW;
+  int64_t r = (int64_t)blockIdx.x * RPW + sub;
+  if (r < p.rows) load_row(r);
+  for (; r < p.rows; r += step) {
+    uint4 e[CH], cu[CH], cg[CH];
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int col = (k * TPR + t) * 8;
+      e[k] = make_uint4(0, 0, 0, 0);
+      if (p.dres && col < cols) e[k] = load_stream(p.dres + r * p.ld_dres + col);
+      cu[k] = u[k];
+      cg[k] = g[k];
+    }
+    if (r + step < p.rows) load_row(r + step);
     const float rstd = p.rstd[r];
     float dot = 0.f;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
       const int col = (k * TPR + t) * 8;
       float h[8], d[8], w[8];
-      load_weight8(p.weight, col < p.cols ? col : 0, w);
-      unpack8(u[k], h);
-      unpack8(g[k], d);
+      if constexpr (WF32) wk[k].load(p.weight.p, col < cols ? col : 0);
+      else keep_packed(wk[k].a);
+      wk[k].get(w);
+      unpack8(cu[k], h);
+      unpack8(cg[k], d);
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         h[c] *= rstd;
@@ -277,23 +350,23 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_bwd_kernel(con
       }
     }
     // the two halves of `red` alternate, so one barrier a row suffices
-    const float mean = row_sum<TPR>(dot, red[flip]) / (float)p.cols;
+    const float mean = row_sum<TPR>(dot, red[flip]) / (float)cols;
     flip ^= 1;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      // Opaque, so that the packed row stays in registers over the reduction
-      // and not its fp32 values (twice the registers: half the waves).
-      asm volatile("" : "+v"(u[k].x), "+v"(u[k].y), "+v"(u[k].z), "+v"(u[k].w));
-      asm volatile("" : "+v"(g[k].x), "+v"(g[k].y), "+v"(g[k].z), "+v"(g[k].w));
       const int col = (k * TPR + t) * 8;
+      keep_packed(cu[k]);
+      keep_packed(cg[k]);
       float h[8], d[8], w[8], z[8];
-      load_weight8(p.weight, col < p.cols ? col : 0, w);
-      unpack8(u[k], h);
-      unpack8(g[k], d);
+      if constexpr (WF32) wk[k].load(p.weight.p, col < cols ? col : 0);
+      else keep_packed(wk[k].a);
+      wk[k].get(w);
+      unpack8(cu[k], h);
+      unpack8(cg[k], d);
       unpack8(e[k], z);
 #pragma unroll
       for (int c = 0; c < 8; ++c) z[c] += rstd * (d[c] * w[c] - (h[c] * rstd) * mean);
-      if (col < p.cols) *(uint4*)(p.dx + r * p.ld_dx + col) = pack8(z);
+      if (col < cols) *(uint4*)(p.dx + r * p.ld_dx + col) = pack8(z);
     }
   }
   float* const part = p.partial + ((int64_t)blockIdx.x * RPW + sub) * p.cols;
@@ -307,22 +380,23 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_bwd_kernel(con
   }
 }
 
-// dweight[c] = sum over the partial rows, in order: 16 columns x 16 row
-// groups a workgroup, the groups joined through LDS.
-__global__ __launch_bounds__(256) void rms_norm_dweight_kernel(const float* __restrict__ partial,
-                                                               int parts, int64_t cols,
-                                                               void* __restrict__ dw, int f32) {
-  __shared__ float red[16][17];
-  const int c = threadIdx.x & 15, grp = threadIdx.x >> 4;
-  const int64_t col = (int64_t)blockIdx.x * 16 + c;   // cols is a multiple of 16
+// dweight[c] = sum over the partial rows, in order: 32 columns (one 128-byte
+// line a row) x 32 row groups a workgroup, the groups joined through LDS.
+__global__ __launch_bounds__(1024) void rms_norm_dweight_kernel(const float* __restrict__ partial,
+                                                                int parts, int64_t cols,
+                                                                void* __restrict__ dw, int f32) {
+  __shared__ float red[32][33];
+  const int c = threadIdx.x & 31, grp = threadIdx.x >> 5;
+  const int64_t col = (int64_t)blockIdx.x * 32 + c;
   float v = 0.f;
-  for (int i = grp; i < parts; i += 16) v += partial[(int64_t)i * cols + col];
+  if (col < cols)
+    for (int i = grp; i < parts; i += 32) v += partial[(int64_t)i * cols + col];
   red[grp][c] = v;
   __syncthreads();
-  if (grp == 0) {
+  if (grp == 0 && col < cols) {
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += red[i][c];
+    for (int i = 0; i < 32; ++i) v += red[i][c];
     if (f32) ((float*)dw)[col] = v;
     else ((uint16_t*)dw)[col] = (uint16_t)f32_to_bf16_rne(v);
   }
@@ -355,19 +429,22 @@ static void norm_shape(int64_t rows, int64_t cols, int* tpr, int* ch) {
     else if (tpr == 256 && ch == 2) KERNEL(256, 2);                          \
     else if (tpr == 256) KERNEL(256, 4);                                     \
     else if (ch == 1) KERNEL(1024, 1);                                       \
-    else if (ch == 2) KERNEL(1024, 2);                                       \
-    else KERNEL(1024, 4);                                                    \
+    else KERNEL(1024, 2);                                                    \
   } while (0)
 
-hipError_t launch_rms_norm_fwd(const NormFwdArgs& p, hipStream_t stream) {
-  int tpr, ch;
-  norm_shape(p.rows, p.cols, &tpr, &ch);
+static hipError_t launch_norm_rows(const NormFwdArgs& p, int tpr, int ch, hipStream_t stream) {
   const int block = tpr < 256 ? 256 : tpr;
   const unsigned grid = (unsigned)((p.rows + block / tpr - 1) / (block / tpr));
 #define FP8BW_K(T, C) hipLaunchKernelGGL((rms_norm_fwd_kernel<T, C>), dim3(grid), dim3(block), 0, stream, p)
   FP8BW_NORM_DISPATCH(FP8BW_K);
 #undef FP8BW_K
-  hipError_t e = hipGetLastError();
+  return hipGetLastError();
+}
+
+hipError_t launch_rms_norm_fwd(const NormFwdArgs& p, hipStream_t stream) {
+  int tpr, ch;
+  norm_shape(p.rows, p.cols, &tpr, &ch);
+  const hipError_t e = launch_norm_rows(p, tpr, ch, stream);
   if (e != hipSuccess || !p.qt) return e;
   hipLaunchKernelGGL(rms_norm_quant_t_kernel,
                      dim3((unsigned)((p.cols + 127) / 128), (unsigned)((p.rows + 127) / 128)),
@@ -395,12 +472,16 @@ hipError_t launch_rms_norm_bwd(const NormBwdArgs& p, hipStream_t stream) {
   const int block = tpr < 256 ? 256 : tpr;
   const int rpw = block / tpr;
   const int grid = norm_bwd_grid(p.rows, rpw);
-#define FP8BW_K(T, C) hipLaunchKernelGGL((rms_norm_bwd_kernel<T, C>), dim3(grid), dim3(block), 0, stream, p)
+#define FP8BW_K(T, C)                                                                                    \
+  do {                                                                                                   \
+    if (p.weight.f32) hipLaunchKernelGGL((rms_norm_bwd_kernel<T, C, true>), dim3(grid), dim3(block), 0, stream, p); \
+    else hipLaunchKernelGGL((rms_norm_bwd_kernel<T, C, false>), dim3(grid), dim3(block), 0, stream, p);  \
+  } while (0)
   FP8BW_NORM_DISPATCH(FP8BW_K);
 #undef FP8BW_K
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(rms_norm_dweight_kernel, dim3((unsigned)(p.cols / 16)), dim3(256), 0, stream,
+  hipLaunchKernelGGL(rms_norm_dweight_kernel, dim3((unsigned)((p.cols + 31) / 32)), dim3(1024), 0, stream,
                      p.partial, grid * rpw, p.cols, p.dweight, p.weight.f32);
   return hipGetLastError();
 }

@@ -464,15 +464,16 @@ __global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ 
 
 constexpr int kCus = 256;
 
-// Large tiles once they fill half the chip's compute units; below that 64-row
-// tiles give four times the workgroups (and take any M and N).
-bool large_tiles(int64_t M, int64_t N) {
-  return M >= 256 && N >= 256 && ((M + 255) / 256) * ((N + 255) / 256) >= kCus / 2;
+// Large tiles once they (times the splits of the contraction) fill half the
+// chip's compute units; below that 64-row tiles give four times the workgroups
+// (and take any M and N).
+bool large_tiles(int64_t M, int64_t N, int64_t splits) {
+  return M >= 256 && N >= 256 && ((M + 255) / 256) * ((N + 255) / 256) * splits >= kCus / 2;
 }
 
 template <int EPI>
 hipError_t run_gemm(XentGemm p, int splits, hipStream_t stream) {
-  const bool large = large_tiles(p.M, p.N);
+  const bool large = large_tiles(p.M, p.N, splits);
   const int bm = large ? 256 : 64;
   p.tiles_m = (p.M + bm - 1) / bm;
   p.tiles_n = (p.N + 255) / 256;
@@ -518,11 +519,18 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
   // an odd number of 128-byte lines a row: rows do not all start on one memory channel
   L.ld_ht = L.ld_gt = (L.tp / 64 | 1) * 64;
   L.ld_g = L.ld_wt = (L.vp / 64 | 1) * 64;
-  const bool large = large_tiles(T, K);
-  const int64_t tiles = ((T + (large ? 255 : 63)) / (large ? 256 : 64)) * ((K + 255) / 256);
-  int64_t s = kCus / tiles, most = L.vp / 64 / 8;   // at least 8 slabs a split
-  if (s > most) s = most;
-  L.splits = s < 1 ? 1 : (int)s;
+  // dH's contraction is split until its tiles fill one round of the chip, at
+  // least 8 slabs a split; large tiles if that many splits let them.  (1777 x
+  // 2048 outputs over 50001 columns: 56 large tiles x 4 splits.)
+  auto splits_of = [&](int64_t bm) {
+    const int64_t tiles = ((T + bm - 1) / bm) * ((K + 255) / 256);
+    int64_t s = kCus / tiles;
+    if (s > L.vp / 512) s = L.vp / 512;
+    return s < 1 ? (int64_t)1 : s;
+  };
+  const int64_t s_large = splits_of(256);
+  L.splits = (int)(large_tiles(T, K, s_large) ? s_large : splits_of(64));
+  // (splits_of(64) <= s_large, so run_gemm takes the same decision.)
   L.row = take((size_t)T * sizeof(float2));
   L.target = take((size_t)T * 4);
   L.scale = take(4);

@@ -418,7 +418,7 @@ int fp8_linear_bwd(const void* dy, const void* w, const void* saved, size_t save
  *                (ld_q) with recip[r*rs_row + kb*rs_kb]; qt E4M3 [cols, rows]
  *                (ld_qt) with recip_t[c*rst_row + mb*rst_kb].  The codes
  *                follow the quantizers' recipe on the fp32 v (not on y).
- *   Requires cols % 16 == 0, cols <= 32768, and rows % 16 == 0 with qt (one
+ *   Requires cols % 16 == 0, cols <= 16384, and rows % 16 == 0 with qt (one
  *   more launch, which reads s again).  eps >= 0.
  */
 int fp8bw_rms_norm_fwd(const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
