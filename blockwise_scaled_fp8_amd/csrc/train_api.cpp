@@ -44,11 +44,14 @@ int check_codes(const void* q, int64_t rows, int64_t cols, int64_t ld, const flo
   return FP8BW_OK;
 }
 
+constexpr int64_t kNormMaxRows = (int64_t)1 << 22;
+
 int check_norm(int64_t rows, int64_t cols, int weight_dtype) {
   if (rows < 0 || cols < 0) return fail(FP8BW_ERR_SHAPE, "negative dimension");
   if (weight_dtype != FP8BW_OUT_BF16 && weight_dtype != FP8BW_OUT_F32)
     return fail(FP8BW_ERR_UNSUPPORTED, "unknown weight type %d", weight_dtype);
-  if (rows > kMaxDim) return fail(FP8BW_ERR_SHAPE, "rows=%lld too large", (long long)rows);
+  // A launch has fewer than 2^32 threads, at most 1024 a row.
+  if (rows >= kNormMaxRows) return fail(FP8BW_ERR_SHAPE, "rows=%lld must be below 2^22", (long long)rows);
   if (cols % 16 || cols > fp8bw::kNormMaxCols)
     return fail(FP8BW_ERR_SHAPE, "cols=%lld must be a multiple of 16 and at most %lld", (long long)cols,
                 (long long)fp8bw::kNormMaxCols);
@@ -72,9 +75,8 @@ FP8BW_API int fp8bw_rms_norm_fwd(const void* x, int64_t ld_x, const void* residu
   int st = check_norm(rows, cols, weight_dtype);
   if (st != FP8BW_OK) return st;
   if (!(eps >= 0.f)) return fail(FP8BW_ERR_UNSUPPORTED, "eps must be >= 0");
-  if (qt && (rows % 16 || cdiv(rows, 128) > kMaxGridY))
-    return fail(FP8BW_ERR_SHAPE, "transposed codes need rows %% 16 == 0 and rows <= 128 * 65535 (rows=%lld)",
-                (long long)rows);
+  if (qt && rows % 16)
+    return fail(FP8BW_ERR_SHAPE, "transposed codes need rows %% 16 == 0 (rows=%lld)", (long long)rows);
   if (rows == 0 || cols == 0) return ok();
   if ((st = check_bf16(x, rows, cols, ld_x, "x")) != FP8BW_OK) return st;
   if ((st = check_weight(weight)) != FP8BW_OK) return st;
@@ -105,7 +107,7 @@ FP8BW_API int fp8bw_rms_norm_fwd(const void* x, int64_t ld_x, const void* residu
 }
 
 FP8BW_API size_t fp8bw_rms_norm_bwd_ws_bytes(int64_t rows, int64_t cols) {
-  if (rows <= 0 || cols <= 0 || rows > kMaxDim || cols > fp8bw::kNormMaxCols) return 0;
+  if (rows <= 0 || cols <= 0 || rows >= kNormMaxRows || cols > fp8bw::kNormMaxCols) return 0;
   return align_up(fp8bw::rms_norm_bwd_ws_bytes(rows, cols));
 }
 
@@ -146,11 +148,13 @@ FP8BW_API int fp8bw_rms_norm_bwd(const void* dy, int64_t ld_dy, const void* s, i
 
 namespace {
 
+// A launch has fewer than 2^32 threads, 512 a tile.
+constexpr int64_t kXentMaxTiles = (int64_t)1 << 23;
 constexpr int64_t kXentMaxT = (int64_t)1 << 24, kXentMaxV = (int64_t)1 << 28, kXentMaxK = (int64_t)1 << 20;
 
 bool xent_dims_ok(int64_t T, int64_t V, int64_t K) {
   return T >= 0 && V >= 0 && T <= kXentMaxT && V <= kXentMaxV && K >= 64 && K <= kXentMaxK && K % 64 == 0 &&
-         cdiv(T, 64) * cdiv(V, 256) < ((int64_t)1 << 31);
+         cdiv(T, 256) * cdiv(V, 256) < kXentMaxTiles && cdiv(T, 256) * cdiv(K, 256) < kXentMaxTiles;
 }
 
 // The products address a tile of 256 rows with 32-bit byte offsets.
@@ -167,7 +171,7 @@ int check_xent(const void* h, int64_t ld_h, const void* w, int64_t ld_w, const i
   if (!xent_dims_ok(T, V, K))
     return fail(FP8BW_ERR_SHAPE,
                 "T=%lld V=%lld K=%lld: K must be a multiple of 64 in [64, 2^20], V <= 2^28, T <= 2^24, "
-                "ceil(T / 64) ceil(V / 256) < 2^31",
+                "ceil(T / 256) ceil(max(V, K) / 256) < 2^23",
                 (long long)T, (long long)V, (long long)K);
   if (T == 0) return FP8BW_OK;
   if (V == 0) return fail(FP8BW_ERR_SHAPE, "an empty vocabulary has no cross entropy");
@@ -248,7 +252,8 @@ namespace {
 
 int check_adamw_tensor(const fp8bw_adamw_tensor& t, int i, bool eight) {
   auto type_ok = [](int d) { return d == FP8BW_OUT_BF16 || d == FP8BW_OUT_F32; };
-  if (t.numel < 0 || t.numel >= ((int64_t)1 << 40)) return fail(FP8BW_ERR_SHAPE, "tensor %d: numel %lld", i, (long long)t.numel);
+  // At most 2^24 workgroups of 2048 elements a launch (2^32 threads).
+  if (t.numel < 0 || t.numel >= ((int64_t)1 << 35)) return fail(FP8BW_ERR_SHAPE, "tensor %d: numel %lld", i, (long long)t.numel);
   if (!type_ok(t.param_dtype) || !type_ok(t.grad_dtype)) return fail(FP8BW_ERR_UNSUPPORTED, "tensor %d: unknown type", i);
   if (t.master && t.param_dtype != FP8BW_OUT_BF16)
     return fail(FP8BW_ERR_UNSUPPORTED, "tensor %d: a master belongs to a bf16 parameter", i);
@@ -313,8 +318,7 @@ FP8BW_API int fp8bw_adamw_step(const fp8bw_adamw_tensor* tensors, int count, int
     const fp8bw_adamw_tensor& t = tensors[i];
     if (t.numel == 0) continue;
     const int64_t n = cdiv(t.numel, chunk);
-    if (n >= ((int64_t)1 << 31)) return fail(FP8BW_ERR_SHAPE, "tensor %d too large", i);
-    if (L.count == fp8bw::kAdamwTensors || groups + n >= ((int64_t)1 << 31)) {
+    if (L.count == fp8bw::kAdamwTensors || groups + n >= ((int64_t)1 << 24)) {
       const hipError_t e = flush();
       if (e != hipSuccess) return hip_status(e, "fp8bw_adamw_step");
     }

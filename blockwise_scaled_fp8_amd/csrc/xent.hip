@@ -13,10 +13,12 @@
 // G (bf16), and two products add G's share to dH and finish the piece's rows
 // of dW.  The workspace holds one piece, whatever the vocabulary.
 //
-// Every product is the same kernel on bf16 operands whose rows run along the
-// contraction (C = A B^T, v_mfma_f32_16x16x32_bf16, fp32 accumulators).  It
-// is bound by the matrix cores from a few hundred tokens on, by the reading of
-// W below.
+// Every product is the same kernel on bf16 operands (v_mfma_f32_16x16x32_bf16,
+// fp32 accumulators).  An operand's rows run along the contraction (H and W in
+// the logits, G in dH) or across it (W in dH; G and H in dW): the latter are
+// turned by transposing LDS reads, so nothing is ever transposed in memory.
+// The products are bound by the matrix cores from a few hundred tokens on, by
+// the reading of W below.
 //
 // Rounding: G is held as bf16, the accuracy of the matrix cores' operands.
 // It is formed with dloss divided by its largest magnitude, which the
@@ -45,8 +47,11 @@ enum XentEpilogue {
 };
 
 struct XentGemm {
-  const uint8_t* a; int64_t lda;   // rows of the contraction, in bytes
+  // Operands by rows of ld bytes: [M or N][contraction], or, for the product
+  // kernels' *_KM operands, [contraction][M or N] with a_rows / b_rows rows.
+  const uint8_t* a; int64_t lda;
   const uint8_t* b; int64_t ldb;
+  int a_rows, b_rows;
   int M, N;
   int kblocks;                     // of 64 elements (128 bytes)
   int kb_per_split;
@@ -102,22 +107,153 @@ __device__ __forceinline__ bf16x8 frag(const uint8_t* tile, uint32_t off) {
   return __builtin_bit_cast(bf16x8, *(const uint4*)(tile + off));
 }
 
-// C = A B^T on BM x BN tiles of WGM x WGN waves.  Two stages of 128-byte
-// contraction slabs in LDS, filled by direct buffer -> LDS loads from waves 0
-// and 1 (a direct load keeps the issuing wave for about 16 cycles; the others
-// go straight to their MFMAs).  Each stage is an LDS variable of its own and
-// the stage loop is unrolled, so that the compiler sees that reads of one
-// stage do not depend on loads into the other.
+// A slab of an operand whose rows run across the contraction: 64 contraction
+// rows of C columns, 2 C bytes a row, in units of 32 bytes (16 columns).  Unit
+// u of row r sits at u ^ km_swz(r).  A fragment is four consecutive k of one
+// column per transposing read (ds_read_b64_tr_b16: element e of lane i of a
+// 16-lane group is element i % 4 of the 8 bytes that lane 4 e + i / 4
+// addresses), so half a wave reads rows {0-3, 16-19} (+ a constant) of one
+// unit column: the swizzle spreads these 8 pieces of 32 bytes over all banks.
+template <int C>
+__device__ __forceinline__ int km_swz(int row) {
+  return C == 256 ? (row & 3) | ((row >> 4) & 1) << 2 : ((row >> 1) & 1) | ((row >> 4) & 1) << 1;
+}
+template <int C>
+__device__ __forceinline__ bf16x8 frag_km(const uint8_t* tile, uint32_t off) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  typedef __attribute__((address_space(3))) uint8_t lds_u8;
+  lds_u8* const t = (lds_u8*)const_cast<uint8_t*>(tile) + off;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)t);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + 4 * 2 * C));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// One operand's slab by direct loads from waves 0 and 1: C rows of 128 bytes,
+// or with KM 64 rows of 2 C bytes; 1 KB an instruction either way.
+template <int C, bool KM, bool CLAMP>
+struct SlabLoader {
+  static constexpr int N = C / 16;                 // loads a wave
+  static constexpr int RPL = KM ? 512 / C : 8;     // rows a load covers
+  uint32_t off[KM ? 2 : CLAMP ? N : 1];
+  uint32_t col[2];                                 // KM: a lane's column bytes, by the swizzle's top bit
+  const uint8_t* base;
+  int64_t ld;
+  int rows, lrow, wave;
+  __amdgpu_buffer_rsrc_t rsrc;
+
+  // first: first row (KM: column) of the tile's window; limit: rows (columns)
+  // of the operand; k_rows: its contraction rows (KM).
+  __device__ __forceinline__ void init(const uint8_t* p, int64_t ld_, int first, int limit, int k_rows,
+                                       int wave_, int lane) {
+    ld = ld_;
+    wave = wave_;
+    rows = k_rows;
+    if constexpr (KM) {
+      base = p + 2 * (int64_t)first;
+      lrow = lane / (64 / RPL);
+      const int chunk = lane % (64 / RPL);
+#pragma unroll
+      for (int top = 0; top < 2; ++top) {
+        // row = RPL (wave + 2 i) + lrow; its bit 4 comes from i alone
+        const int swz = km_swz<C>((RPL * wave + lrow) & 15) | top << (C == 256 ? 2 : 1);
+        int c = 16 * ((chunk >> 1) ^ swz) + 8 * (chunk & 1);
+        if (CLAMP) c = min(c, limit - first - 8);   // past the last column: any of them
+        col[top] = 2 * c;
+        off[top] = (uint32_t)((RPL * wave + lrow) * (int)ld) + col[top];
+      }
+    } else {
+      base = p + (int64_t)first * ld;
+      rsrc = rsrc_of(base, (int64_t)C * ld);
+      lrow = lane >> 3;
+      const int chunk = (lane & 7) ^ ((4 * (wave & 1) + (lrow >> 1)) & 5);
+#pragma unroll
+      for (int i = 0; i < (CLAMP ? N : 1); ++i) {
+        const int r = 8 * (wave + 2 * i) + lrow;
+        off[i] = (uint32_t)((CLAMP ? min(r, limit - 1 - first) : r) * (int)ld + chunk * 16);
+      }
+    }
+  }
+  __device__ __forceinline__ void issue(int kb, uint8_t* lds) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (!KM) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (wave + 2 * i) * 1024), 16,
+                                                 off[CLAMP ? i : 0],
+                                                 kb * 128 + (CLAMP ? 0 : 16 * i * (int)ld), 0, 0);
+    } else {
+      // A descriptor of its own per slab: offsets stay within 64 rows.
+      const __amdgpu_buffer_rsrc_t rs = rsrc_of(base + (int64_t)kb * 64 * ld, 64 * ld);
+      const int left = rows - kb * 64;
+      if (left >= 64) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + (wave + 2 * i) * 1024), 16,
+                                                   off[(2 * RPL * i >> 4) & 1], 2 * RPL * i * (int)ld, 0, 0);
+      } else {
+        // Rows past the last read that one: the other operand is zero there.
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              rs, (lds_void*)(lds + (wave + 2 * i) * 1024), 16,
+              (uint32_t)(min(RPL * (wave + 2 * i) + lrow, left - 1) * (int)ld) + col[(2 * RPL * i >> 4) & 1], 0, 0,
+              0);
+      }
+    }
+#endif
+  }
+};
+
+// Fragment addresses of one operand's 16-row (16-column) sub-tiles.
+template <int C, bool KM>
+struct FragReader {
+  uint32_t lo, hi;   // !KM: a lane's two 16-byte chunks; KM: lo its row and place in a unit
+  int unit, swz;
+  // first: the wave's first row (column) in the tile, a multiple of 64
+  __device__ __forceinline__ void init(int first, int lane) {
+    const int frow = lane & 15, fq = lane >> 4;
+    if constexpr (KM) {
+      const int row = 16 * fq + (frow >> 2);
+      swz = km_swz<C>(row);
+      unit = first >> 4;
+      lo = row * 2 * C + 8 * (frow & 3);
+      hi = lo + 8 * 2 * C;
+    } else {
+      lo = (first + frow) * 128 + (((2 * fq) ^ chunk_swz(first + frow)) << 4);
+      hi = (first + frow) * 128 + (((2 * fq + 1) ^ chunk_swz(first + frow)) << 4);
+    }
+    // Opaque, so that the compiler keeps these and adds constants, instead of
+    // one address per fragment and stage.
+    asm volatile("" : "+v"(lo), "+v"(hi));
+  }
+  // k = 16 fq + 0 .. 7 (low) and 16 fq + 8 .. 15 (high) of sub-tile i
+  __device__ __forceinline__ bf16x8 low(const uint8_t* tile, int i) const {
+    if constexpr (KM) return frag_km<C>(tile, lo + (((unit + i) ^ swz) << 5));
+    else return frag(tile, lo + 2048 * i);
+  }
+  __device__ __forceinline__ bf16x8 high(const uint8_t* tile, int i) const {
+    if constexpr (KM) return frag_km<C>(tile, hi + (((unit + i) ^ swz) << 5));
+    else return frag(tile, hi + 2048 * i);
+  }
+};
+
+// C[m, n] = sum_k A[m, k] B[n, k] on BM x BN tiles of WGM x WGN waves.  Two
+// stages of 64 contraction elements in LDS, filled by direct buffer -> LDS
+// loads from waves 0 and 1 (a direct load keeps the issuing wave for about 16
+// cycles; the others go straight to their MFMAs).  Each stage is an LDS
+// variable of its own and the stage loop is unrolled, so that the compiler
+// sees that reads of one stage do not depend on loads into the other.
 //
 // Edges: with CLAMP every lane's row is clamped to the last one (any M, N);
 // without, M >= BM and N >= BN, and an edge tile's window moves back to end
-// at the last row, so no load needs a register of its own for its row.
+// at the last row, so no load needs a register of its own for its row.  A
+// KM operand A needs neither: its rows are at least tiles_m BM columns long.
 // Either way a tile's epilogue handles only its own rows and columns.
-template <int BM, int BN, int WGM, int WGN, bool CLAMP, int EPI>
+template <int BM, int BN, int WGM, int WGN, bool CLAMP, int EPI, bool AKM, bool BKM>
 __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGemm p) {
-  constexpr int NW = WGM * WGN, LW = 2;
+  constexpr int NW = WGM * WGN;
   constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16;
-  constexpr int AI = BM / 8 / LW, BI = BN / 8 / LW;
   __shared__ __attribute__((aligned(1024))) uint8_t sA0[BM * 128], sA1[BM * 128];
   __shared__ __attribute__((aligned(1024))) uint8_t sB0[BN * 128], sB1[BN * 128];
 
@@ -130,42 +266,18 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
   int tm, tn;
   tile_order(id - split * gridDim.x, p.tiles_m, p.tiles_n, &tm, &tn);
   const int m0 = tm * BM, n0 = tn * BN;
-  const int ml = CLAMP ? m0 : min(m0, p.M - BM), nl = CLAMP ? n0 : min(n0, p.N - BN);
+  const int ml = CLAMP || AKM ? m0 : min(m0, p.M - BM), nl = CLAMP ? n0 : min(n0, p.N - BN);
   const int kb0 = split * p.kb_per_split, kb1 = min(p.kblocks, kb0 + p.kb_per_split);
 
-  // Lane 8 q + c of a direct load fills physical chunk c of row 8 o + q (o =
-  // wave + LW i, so o and wave have the same parity).
-  const int lrow = lane >> 3;
-  const int lchunk = (lane & 7) ^ ((4 * (wave & 1) + (lrow >> 1)) & 5);
-  [[maybe_unused]] const __amdgpu_buffer_rsrc_t ars = rsrc_of(p.a + (int64_t)ml * p.lda, (int64_t)BM * p.lda);
-  [[maybe_unused]] const __amdgpu_buffer_rsrc_t brs = rsrc_of(p.b + (int64_t)nl * p.ldb, (int64_t)BN * p.ldb);
-  uint32_t av[CLAMP ? AI : 1], bv[CLAMP ? BI : 1];
-#pragma unroll
-  for (int i = 0; i < (CLAMP ? AI : 1); ++i) {
-    const int r = 8 * (wave + LW * i) + lrow;
-    av[i] = (uint32_t)((CLAMP ? min(r, p.M - 1 - ml) : r) * (int)p.lda + lchunk * 16);
-  }
-#pragma unroll
-  for (int i = 0; i < (CLAMP ? BI : 1); ++i) {
-    const int r = 8 * (wave + LW * i) + lrow;
-    bv[i] = (uint32_t)((CLAMP ? min(r, p.N - 1 - nl) : r) * (int)p.ldb + lchunk * 16);
-  }
+  SlabLoader<BM, AKM, CLAMP && !AKM> la;
+  SlabLoader<BN, BKM, CLAMP> lb;
+  la.init(p.a, p.lda, ml, p.M, p.a_rows, wave, lane);
+  lb.init(p.b, p.ldb, nl, p.N, p.b_rows, wave, lane);
   auto issue = [&](int kb, uint8_t* sa, uint8_t* sb) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    if (wave < LW) {
-      const int ko = kb * 128;
-#pragma unroll
-      for (int i = 0; i < AI; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ars, (lds_void*)(sa + (wave + LW * i) * 1024), 16,
-                                                 av[CLAMP ? i : 0],
-                                                 ko + (CLAMP ? 0 : 8 * LW * i * (int)p.lda), 0, 0);
-#pragma unroll
-      for (int i = 0; i < BI; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(brs, (lds_void*)(sb + (wave + LW * i) * 1024), 16,
-                                                 bv[CLAMP ? i : 0],
-                                                 ko + (CLAMP ? 0 : 8 * LW * i * (int)p.ldb), 0, 0);
+    if (wave < 2) {
+      la.issue(kb, sa);
+      lb.issue(kb, sb);
     }
-#endif
   };
 
   v4f acc[TM][TN];
@@ -185,28 +297,24 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
       issue(min(kb + 1, kb1 - 1), st ? sA0 : sA1, st ? sB0 : sB1);
       const uint8_t* const ta = st ? sA1 : sA0;
       const uint8_t* const tb = st ? sB1 : sB0;
-      // A lane's two 16-byte chunks of a row, the same on both sides: which k
-      // they are does not matter to the sum.  Made opaque, so that the
-      // compiler keeps two base addresses and constant offsets.
-      uint32_t a0 = (wm0 + frow) * 128 + (((2 * fq) ^ chunk_swz(wm0 + frow)) << 4);
-      uint32_t a1 = (wm0 + frow) * 128 + (((2 * fq + 1) ^ chunk_swz(wm0 + frow)) << 4);
-      uint32_t b0 = (wn0 + frow) * 128 + (((2 * fq) ^ chunk_swz(wn0 + frow)) << 4);
-      uint32_t b1 = (wn0 + frow) * 128 + (((2 * fq + 1) ^ chunk_swz(wn0 + frow)) << 4);
-      asm volatile("" : "+v"(a0), "+v"(a1), "+v"(b0), "+v"(b1));
+      FragReader<BM, AKM> ra;
+      FragReader<BN, BKM> rb;
+      ra.init(wm0, lane);
+      rb.init(wn0, lane);
       bf16x8 bl[TN], bh[TN], al[2], ah[2];
-      bl[0] = frag(tb, b0);
-      al[0] = frag(ta, a0);
+      bl[0] = rb.low(tb, 0);
+      al[0] = ra.low(ta, 0);
 #pragma unroll
-      for (int j = 1; j < TN; ++j) bl[j] = frag(tb, b0 + 2048 * j);
-      ah[0] = frag(ta, a1);
+      for (int j = 1; j < TN; ++j) bl[j] = rb.low(tb, j);
+      ah[0] = ra.high(ta, 0);
 #pragma unroll
-      for (int j = 0; j < TN; ++j) bh[j] = frag(tb, b1 + 2048 * j);
+      for (int j = 0; j < TN; ++j) bh[j] = rb.high(tb, j);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         if (i + 1 < TM) {
-          al[(i + 1) & 1] = frag(ta, a0 + 2048 * (i + 1));
-          ah[(i + 1) & 1] = frag(ta, a1 + 2048 * (i + 1));
+          al[(i + 1) & 1] = ra.low(ta, i + 1);
+          ah[(i + 1) & 1] = ra.high(ta, i + 1);
           __builtin_amdgcn_sched_barrier(0);   // keep the next row's reads ahead of this row's MFMAs
         }
         // B first: lane l then holds row 16 i + l % 16, columns 16 j + 4 (l / 16) + 0..3
@@ -220,7 +328,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
       ring_sync();
     }
   }
-  ring_sync();   // the stages are free
+  __syncthreads();   // every wave's reads and loads are done: the stages are free
 
   const int row0 = ml + wm0 + frow;            // + 16 i
   const int col0 = nl + wn0 + 4 * fq;          // + 16 j + v
@@ -298,40 +406,81 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
   } else {
     float scale = 1.f;
     if constexpr (EPI == kOut) scale = *p.scale;
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
+    // The 16 values of lane row i: G's, or the product's times scale.
+    auto values = [&](int i, float (&val)[TN][4]) {
       const int r = row0 + 16 * i;
-      if (r < m0 || r >= p.M) continue;
-      float lse = 0.f, weight = 0.f;
-      int tgt = -1;
       if constexpr (EPI == kGrad) {
-        const float2 info = p.row[r];
-        lse = info.x;
-        weight = info.y;
-        tgt = p.local_target[r] - p.v0;
-      }
-      uint16_t* const out = (uint16_t*)p.out + (int64_t)r * p.ldo;
+        const float2 info = p.row[min(r, p.M - 1)];
+        const int tgt = p.local_target[min(r, p.M - 1)] - p.v0;
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int n = col0 + 16 * j;
-        float val[4];
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          if constexpr (EPI == kGrad) {
-            float e = __builtin_amdgcn_exp2f((acc[i][j][v] - lse) * kLog2e);
-            if (n + v == tgt) e -= 1.f;
+          for (int v = 0; v < 4; ++v) {
+            float e = __builtin_amdgcn_exp2f((acc[i][j][v] - info.x) * kLog2e);
+            if (col0 + 16 * j + v == tgt) e -= 1.f;
             // a row of weight zero (an ignored target) has no gradient, whatever its logits
-            val[v] = weight == 0.f ? 0.f : e * weight;
-          } else {
-            val[v] = acc[i][j][v] * scale;
+            val[j][v] = info.y == 0.f ? 0.f : e * info.y;
           }
-        }
-        if (n >= n0 && n + 3 < p.N && (n & 3) == 0) {
-          *(uint2*)(out + n) = make_uint2(pack_bf16x2_rne(val[0], val[1]), pack_bf16x2_rne(val[2], val[3]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) val[j][v] = acc[i][j][v] * scale;
+      }
+    };
+    uint16_t* const out = (uint16_t*)p.out;
+    if (BM == 256 && (nl & 7) == 0) {
+      // Through LDS, so that every store writes whole lines (in the MFMA layout
+      // a row of a wave's columns would leave in pieces of 32 bytes): 64 rows of
+      // 512 bytes in each stage array, 16-byte chunk c of row r at c ^ (r & 15).
+      auto quarter = [&](int q) -> uint8_t* { return q == 0 ? sA0 : q == 1 ? sA1 : q == 2 ? sB0 : sB1; };
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        float val[TN][4];
+        values(i, val);
+        uint8_t* const rowp = quarter((wm0 + 16 * i) >> 6) + ((wm0 + 16 * i + frow) & 63) * 512;
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          *(uint2*)(rowp + 16 * (((wn0 >> 3) + 2 * j + (fq >> 1)) ^ frow) + 8 * (fq & 1)) =
+              make_uint2(pack_bf16x2_rne(val[j][0], val[j][1]), pack_bf16x2_rne(val[j][2], val[j][3]));
+      }
+      __syncthreads();
+      const uint8_t* const src = quarter(wave >> 1);
+      const int c = lane & 31, n = nl + 8 * c;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int rr = 32 * (wave & 1) + 2 * k + (lane >> 5);
+        const int r = ml + 64 * (wave >> 1) + rr;
+        const u32x4_t d = *(const u32x4_t*)(src + rr * 512 + 16 * (c ^ (rr & 15)));
+        if (r < m0 || r >= p.M || n + 7 < n0 || n >= p.N) continue;
+        uint16_t* const at = out + (int64_t)r * p.ldo + n;
+        if (n >= n0 && n + 7 < p.N) {
+          if constexpr (EPI == kOut) __builtin_nontemporal_store(d, (u32x4_t*)at);
+          else *(u32x4_t*)at = d;   // the next products read G
         } else {
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (n + v >= n0 && n + v < p.N) out[n + v] = (uint16_t)f32_to_bf16_rne(val[v]);
+          for (int e = 0; e < 8; ++e)
+            if (n + e >= n0 && n + e < p.N) at[e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int r = row0 + 16 * i;
+        float val[TN][4];
+        values(i, val);
+        if (r < m0 || r >= p.M) continue;
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const int n = col0 + 16 * j;
+          uint16_t* const at = out + (int64_t)r * p.ldo + n;
+          if (n >= n0 && n + 3 < p.N && (n & 3) == 0) {
+            *(uint2*)at = make_uint2(pack_bf16x2_rne(val[j][0], val[j][1]), pack_bf16x2_rne(val[j][2], val[j][3]));
+          } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (n + v >= n0 && n + v < p.N) at[v] = (uint16_t)f32_to_bf16_rne(val[j][v]);
+          }
         }
       }
     }
@@ -401,65 +550,29 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, const
   }
 }
 
-// out[c, r] = in[r, c] of bf16; rows past `rows` up to `rows_pad` come out as
-// zeros, so that a contraction over them is unchanged.  64 x 64 tiles through
-// LDS, 8-byte reads and writes.
-__global__ __launch_bounds__(256) void transpose_bf16_kernel(const uint16_t* __restrict__ in, int64_t ld_in,
-                                                             int rows, int rows_pad, int cols,
-                                                             uint16_t* __restrict__ out, int64_t ld_out) {
-  __shared__ uint16_t tile[64][68];
-  const int c0 = blockIdx.y * 64, r0 = blockIdx.x * 64;
-  const int x = (threadIdx.x & 15) * 4, y = threadIdx.x >> 4;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + y + 16 * i;
-    uint16_t e[4] = {0, 0, 0, 0};
-    if (r < rows) {
-      const uint16_t* const src = in + (int64_t)r * ld_in + c0 + x;
-      if (c0 + x + 3 < cols && ((uintptr_t)src & 7) == 0) {
-        const uint2 u = *(const uint2*)src;
-        e[0] = u.x & 0xFFFF; e[1] = u.x >> 16; e[2] = u.y & 0xFFFF; e[3] = u.y >> 16;
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (c0 + x + k < cols) e[k] = src[k];
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) tile[x + k][y + 16 * i] = e[k];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = c0 + y + 16 * i;
-    if (c < cols && r0 + x < rows_pad)   // rows_pad is a multiple of 64
-      *(uint2*)(out + (int64_t)c * ld_out + r0 + x) = *(const uint2*)&tile[y + 16 * i][x];
-  }
-}
-
-// Zeros in columns [c0, c1) of bf16 rows, one wave a row.
+// Zeros in columns [c0, c1) of bf16 rows: one row and 2048 columns a workgroup.
 __global__ __launch_bounds__(256) void zero_columns_kernel(uint16_t* out, int64_t ld, int64_t rows, int64_t c0,
                                                            int64_t c1) {
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (r >= rows) return;
-  for (int64_t c = c0 + (threadIdx.x & 63); c < c1; c += 64) out[r * ld + c] = 0;
+  const int64_t end = min(c1, c0 + ((int64_t)blockIdx.y + 1) * 2048);
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int64_t c = c0 + (int64_t)blockIdx.y * 2048 + threadIdx.x; c < end; c += 256) out[r * ld + c] = 0;
 }
 
 // dH = scale * sum over the splits of their fp32 shares, to bf16.
 __global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ acc, int splits, int64_t T,
                                                       int64_t K, const float* __restrict__ scale,
                                                       uint16_t* __restrict__ dh, int64_t ld_dh) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= T * K) return;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = 0; k < splits; ++k) {
-    const float4 e = *(const float4*)(acc + (int64_t)k * T * K + i);
-    s.x += e.x; s.y += e.y; s.z += e.z; s.w += e.w;
-  }
   const float f = *scale;
-  const int64_t t = i / K;
-  *(uint2*)(dh + t * ld_dh + (i - t * K)) =
-      make_uint2(pack_bf16x2_rne(s.x * f, s.y * f), pack_bf16x2_rne(s.z * f, s.w * f));
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < T * K; i += (int64_t)gridDim.x * 1024) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < splits; ++k) {
+      const float4 e = *(const float4*)(acc + (int64_t)k * T * K + i);
+      s.x += e.x; s.y += e.y; s.z += e.z; s.w += e.w;
+    }
+    const int64_t t = i / K;
+    *(uint2*)(dh + t * ld_dh + (i - t * K)) =
+        make_uint2(pack_bf16x2_rne(s.x * f, s.y * f), pack_bf16x2_rne(s.z * f, s.w * f));
+  }
 }
 
 constexpr int kCus = 256;
@@ -471,7 +584,7 @@ bool large_tiles(int64_t M, int64_t N, int64_t splits) {
   return M >= 256 && N >= 256 && ((M + 255) / 256) * ((N + 255) / 256) * splits >= kCus / 2;
 }
 
-template <int EPI>
+template <int EPI, bool AKM = false, bool BKM = false>
 hipError_t run_gemm(XentGemm p, int splits, hipStream_t stream) {
   const bool large = large_tiles(p.M, p.N, splits);
   const int bm = large ? 256 : 64;
@@ -479,23 +592,22 @@ hipError_t run_gemm(XentGemm p, int splits, hipStream_t stream) {
   p.tiles_n = (p.N + 255) / 256;
   p.kb_per_split = (p.kblocks + splits - 1) / splits;
   const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)splits);
-  if (large) hipLaunchKernelGGL((xent_gemm_kernel<256, 256, 2, 4, false, EPI>), grid, dim3(512), 0, stream, p);
-  else hipLaunchKernelGGL((xent_gemm_kernel<64, 256, 1, 4, true, EPI>), grid, dim3(256), 0, stream, p);
+  if (large) hipLaunchKernelGGL((xent_gemm_kernel<256, 256, 2, 4, false, EPI, AKM, BKM>), grid, dim3(512), 0, stream, p);
+  else hipLaunchKernelGGL((xent_gemm_kernel<64, 256, 1, 4, true, EPI, AKM, BKM>), grid, dim3(256), 0, stream, p);
   return hipGetLastError();
 }
 
 int64_t pad64(int64_t n) { return (n + 63) & ~(int64_t)63; }
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Vocabulary columns per piece: as many as keep G, its transpose and W's
-// transpose at 256 MB each (the memory-side cache's size), in whole tiles.
+// Vocabulary columns per piece: whole tiles, as many as keep G at 256 MB, the
+// memory-side cache's size.
 constexpr int64_t kPieceBytes = (int64_t)256 << 20;
 
 struct XentLayout {
-  int64_t tp, piece, vp;       // padded tokens, columns of a piece, padded
-  int64_t ld_ht, ld_g, ld_gt, ld_wt;
+  int64_t tp, piece, ld_g;     // tokens in whole slabs; columns of a piece; G's row
   int splits;                  // of dH's contraction over the piece
-  size_t part, logit, row, target, scale, ht, g, gt, wt, acc, total;
+  size_t part, logit, row, target, scale, g, acc, total;
 };
 
 XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
@@ -509,23 +621,22 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
     return L;
   }
   L.tp = pad64(T);
-  int64_t piece = kPieceBytes / 2 / (L.tp > K ? L.tp : K) / 256 * 256;
+  int64_t piece = kPieceBytes / 2 / L.tp / 256 * 256;
   if (piece < 256) piece = 256;
   if (piece > V) piece = V;
   const int64_t n = (V + piece - 1) / piece;
   if (n > 1) piece = ((V + n - 1) / n + 255) / 256 * 256;   // even pieces
   L.piece = piece;
-  L.vp = pad64(piece);
-  // an odd number of 128-byte lines a row: rows do not all start on one memory channel
-  L.ld_ht = L.ld_gt = (L.tp / 64 | 1) * 64;
-  L.ld_g = L.ld_wt = (L.vp / 64 | 1) * 64;
+  // Whole tiles, and an odd number of 128-byte lines a row, so that rows do not
+  // all start on one memory channel.
+  L.ld_g = (piece + 255) / 256 * 256 + 64;
   // dH's contraction is split until its tiles fill one round of the chip, at
   // least 8 slabs a split; large tiles if that many splits let them.  (1777 x
   // 2048 outputs over 50001 columns: 56 large tiles x 4 splits.)
   auto splits_of = [&](int64_t bm) {
     const int64_t tiles = ((T + bm - 1) / bm) * ((K + 255) / 256);
     int64_t s = kCus / tiles;
-    if (s > L.vp / 512) s = L.vp / 512;
+    if (s > piece / 512) s = piece / 512;
     return s < 1 ? (int64_t)1 : s;
   };
   const int64_t s_large = splits_of(256);
@@ -534,20 +645,15 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
   L.row = take((size_t)T * sizeof(float2));
   L.target = take((size_t)T * 4);
   L.scale = take(4);
-  L.ht = take((size_t)K * L.ld_ht * 2);
-  L.g = take((size_t)T * L.ld_g * 2);
-  L.gt = take((size_t)L.piece * L.ld_gt * 2);
-  L.wt = take((size_t)K * L.ld_wt * 2);
+  L.g = take((size_t)L.tp * L.ld_g * 2);
   L.acc = take((size_t)L.splits * T * K * 4);
   L.total = off;
   return L;
 }
 
-hipError_t transpose(const void* in, int64_t ld_in, int64_t rows, int64_t cols, void* out, int64_t ld_out,
-                     hipStream_t stream) {
-  const int64_t rp = pad64(rows);
-  hipLaunchKernelGGL(transpose_bf16_kernel, dim3((unsigned)(rp / 64), (unsigned)((cols + 63) / 64)), dim3(256), 0,
-                     stream, (const uint16_t*)in, ld_in, (int)rows, (int)rp, (int)cols, (uint16_t*)out, ld_out);
+hipError_t zero_columns(uint16_t* out, int64_t ld, int64_t rows, int64_t c0, int64_t c1, hipStream_t stream) {
+  hipLaunchKernelGGL(zero_columns_kernel, dim3((unsigned)(rows < 65536 ? rows : 65536), (unsigned)((c1 - c0 + 2047) / 2048)),
+                     dim3(256), 0, stream, out, ld, rows, c0, c1);
   return hipGetLastError();
 }
 
@@ -581,16 +687,17 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
   float2* const row = (float2*)(base + L.row);
   int* const target = (int*)(base + L.target);
   float* const scale = (float*)(base + L.scale);
-  uint16_t* const ht = (uint16_t*)(base + L.ht);
   uint16_t* const g = (uint16_t*)(base + L.g);
-  uint16_t* const gt = (uint16_t*)(base + L.gt);
-  uint16_t* const wt = (uint16_t*)(base + L.wt);
   float* const acc = (float*)(base + L.acc);
   hipLaunchKernelGGL(xent_rows_kernel, dim3(1), dim3(1024), 0, stream, (int)p.T, p.V, p.target,
                      p.ignore_index, p.dloss, p.lse, row, target, scale);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (p.dw && (e = transpose(p.h, p.ld_h, p.T, p.K, ht, L.ld_ht, stream)) != hipSuccess) return e;
+  auto zero = [&](uint16_t* at, int64_t rows, int64_t c0, int64_t c1) {
+    return zero_columns(at, L.ld_g, rows, c0, c1, stream);
+  };
+  // The tokens that fill dW's last slab have no gradient.
+  if (p.dw && L.tp > p.T && (e = zero(g + p.T * L.ld_g, L.tp - p.T, 0, L.ld_g)) != hipSuccess) return e;
   for (int64_t v0 = 0; v0 < p.V; v0 += L.piece) {
     const int64_t nv = p.V - v0 < L.piece ? p.V - v0 : L.piece;
     const uint16_t* const w = (const uint16_t*)p.w + v0 * p.ld_w;
@@ -602,39 +709,33 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
     z.out = g; z.ldo = L.ld_g;
     if ((e = run_gemm<kGrad>(z, 1, stream)) != hipSuccess) return e;
     if (p.dw) {
-      if ((e = transpose(g, L.ld_g, p.T, nv, gt, L.ld_gt, stream)) != hipSuccess) return e;
-      XentGemm d = {};
-      d.a = (const uint8_t*)gt; d.lda = L.ld_gt * 2;
-      d.b = (const uint8_t*)ht; d.ldb = L.ld_ht * 2;
+      XentGemm d = {};   // dW[v, k] = sum_t G[t, v] H[t, k]
+      d.a = (const uint8_t*)g; d.lda = L.ld_g * 2; d.a_rows = (int)L.tp;
+      d.b = (const uint8_t*)p.h; d.ldb = p.ld_h * 2; d.b_rows = (int)p.T;
       d.M = (int)nv; d.N = (int)p.K; d.kblocks = (int)(L.tp / 64);
       d.out = (uint16_t*)p.dw + v0 * p.ld_dw; d.ldo = p.ld_dw; d.scale = scale;
-      if ((e = run_gemm<kOut>(d, 1, stream)) != hipSuccess) return e;
+      if ((e = run_gemm<kOut, true, true>(d, 1, stream)) != hipSuccess) return e;
     }
     if (p.dh) {
-      if (nv % 64) {
-        hipLaunchKernelGGL(zero_columns_kernel, dim3((unsigned)((p.T + 3) / 4)), dim3(256), 0, stream, g,
-                           L.ld_g, p.T, nv, pad64(nv));
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-      }
-      if ((e = transpose(w, p.ld_w, nv, p.K, wt, L.ld_wt, stream)) != hipSuccess) return e;
-      XentGemm d = {};
+      // The columns that fill dH's last slab have no gradient.
+      if (nv % 64 && (e = zero(g, p.T, nv, pad64(nv))) != hipSuccess) return e;
+      XentGemm d = {};   // dH[t, k] += sum_v G[t, v] W[v, k]
       d.a = (const uint8_t*)g; d.lda = L.ld_g * 2;
-      d.b = (const uint8_t*)wt; d.ldb = L.ld_wt * 2;
+      d.b = (const uint8_t*)w; d.ldb = p.ld_w * 2; d.b_rows = (int)nv;
       d.M = (int)p.T; d.N = (int)p.K; d.kblocks = (int)(pad64(nv) / 64);
       d.acc = acc; d.add = v0 > 0;
-      if ((e = run_gemm<kAcc>(d, L.splits, stream)) != hipSuccess) return e;
+      if ((e = run_gemm<kAcc, false, true>(d, L.splits, stream)) != hipSuccess) return e;
     }
   }
   if (!p.dh) return hipSuccess;
-  hipLaunchKernelGGL(xent_dh_kernel, dim3((unsigned)((p.T * p.K / 4 + 255) / 256)), dim3(256), 0, stream, acc,
+  const int64_t groups = (p.T * p.K / 4 + 255) / 256;
+  hipLaunchKernelGGL(xent_dh_kernel, dim3((unsigned)(groups < (1 << 20) ? groups : (1 << 20))), dim3(256), 0, stream, acc,
                      L.splits, p.T, p.K, scale, (uint16_t*)p.dh, p.ld_dh);
   return hipGetLastError();
 }
 
 hipError_t launch_zero_rows_bf16(void* out, int64_t rows, int64_t cols, int64_t ld, hipStream_t stream) {
-  hipLaunchKernelGGL(zero_columns_kernel, dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, stream, (uint16_t*)out,
-                     ld, rows, (int64_t)0, cols);
-  return hipGetLastError();
+  return zero_columns((uint16_t*)out, ld, rows, 0, cols, stream);
 }
 
 }  // namespace fp8bw

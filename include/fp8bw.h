@@ -418,8 +418,8 @@ int fp8_linear_bwd(const void* dy, const void* w, const void* saved, size_t save
  *                (ld_q) with recip[r*rs_row + kb*rs_kb]; qt E4M3 [cols, rows]
  *                (ld_qt) with recip_t[c*rst_row + mb*rst_kb].  The codes
  *                follow the quantizers' recipe on the fp32 v (not on y).
- *   Requires cols % 16 == 0, cols <= 16384, and rows % 16 == 0 with qt (one
- *   more launch, which reads s again).  eps >= 0.
+ *   Requires cols % 16 == 0, cols <= 16384, rows < 2^22, and rows % 16 == 0
+ *   with qt (one more launch, which reads s again).  eps >= 0.
  */
 int fp8bw_rms_norm_fwd(const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
                        const void* weight, int weight_dtype, float eps, int64_t rows, int64_t cols,
@@ -471,7 +471,7 @@ int fp8bw_rms_norm_bwd(const void* dy, int64_t ld_dy, const void* s, int64_t ld_
  *            aligned (backward: 0 or 1).
  *   Requires K % 64 == 0, 64 <= K <= 2^20, V <= 2^28, T <= 2^24, leading
  *   dimensions a multiple of 8 and at most 2^22 - K / 128, and
- *   ceil(T / 64) * ceil(V / 256) < 2^31.  With V == 0 every call with T > 0 is
+ *   ceil(T / 256) * ceil(max(V, K) / 256) < 2^23.  With V == 0 every call with T > 0 is
  *   rejected (an empty sum has no logarithm); with T == 0 dw is set to zero.
  */
 size_t fp8bw_linear_xent_ws_bytes(int64_t T, int64_t V, int64_t K, int backward);
@@ -510,7 +510,7 @@ int fp8bw_linear_xent_bwd(const float* dloss, const void* h, int64_t ld_h, const
  *            `tensors`, element).  Equal arguments give equal results; use
  *            another seed each step.  Zero: to nearest.
  *   step     counts from 1.  lr, weight_decay and eps >= 0; 0 <= beta1, beta2 < 1.
- * One launch per 40 tensors.
+ * One launch per 40 tensors.  numel < 2^35.
  */
 typedef enum { FP8BW_STATE_F32 = 0, FP8BW_STATE_E4M3 = 1 } fp8bw_state;
 typedef struct {
