@@ -1,5 +1,6 @@
 """blockwise_scaled_fp8_amd: blockwise- and tensorwise-scaled FP8 (OCP E4M3)
-quantization and GEMM for AMD MI355X (gfx950).
+quantization and GEMM for AMD MI355X (gfx950), and the operators around an FP8
+linear in a training step (RMS norm, vocabulary cross entropy, AdamW).
 
 The computation lives in libfp8bw.so (hand-written HIP for gfx950 behind the
 C ABI in include/fp8bw.h); this package is its ctypes binding.  PyTorch is
@@ -35,4 +36,10 @@ from .ops import (  # noqa: F401
     rms_norm_fwd,
     scale_grid,
 )
-from .torch_ops import Float8BlockwiseLinear  # noqa: E402,F401  (registers torch.ops.fp8bw.*)
+from .torch_ops import (  # noqa: E402,F401  (registers torch.ops.fp8bw.*)
+    AdamW,
+    Float8BlockwiseLinear,
+    RMSNorm,
+    RMSNormLinear,
+    linear_cross_entropy,
+)

@@ -285,11 +285,12 @@ FP8BW_API int fp8bw_adamw_step(const fp8bw_adamw_tensor* tensors, int count, int
   if (!tensors) return fail(FP8BW_ERR_NULL, "tensors must be non-null");
   if (!aligned(grad_scale, 4)) return fail(FP8BW_ERR_ALIGN, "grad_scale must be 4-byte aligned");
   const bool eight = state == FP8BW_STATE_E4M3;
-  int64_t total = 0;
+  constexpr int64_t kManyElements = (int64_t)1 << 23;
+  int64_t total = 0;   // up to kManyElements
   for (int i = 0; i < count; ++i) {
     const int st = check_adamw_tensor(tensors[i], i, eight);
     if (st != FP8BW_OK) return st;
-    total += tensors[i].numel;
+    if (total < kManyElements) total += tensors[i].numel;
   }
   fp8bw::AdamwLaunch L = {};
   L.grad_scale = grad_scale;
@@ -304,7 +305,7 @@ FP8BW_API int fp8bw_adamw_step(const fp8bw_adamw_tensor* tensors, int count, int
   // Runs of 2048 elements per workgroup: four once that still leaves the chip
   // several workgroups per compute unit, so that the search for the tensor and
   // the first loads' latency are paid once for them.
-  L.iters = total >= ((int64_t)1 << 23) ? 4 : 1;
+  L.iters = total >= kManyElements ? 4 : 1;
   const int64_t chunk = (int64_t)2048 * L.iters;
   int64_t groups = 0;
   auto flush = [&]() -> hipError_t {

@@ -21,7 +21,11 @@ add bench script", Summary).  Here that is:
     above;
   * ``Float8BlockwiseLinear``, a module with ``nn.Linear``'s interface
     (bias-free) that flattens leading dimensions into the token axis and
-    trains through the fused-quantization ops.
+    trains through the fused-quantization ops;
+  * around it, what the rest of a training step needs: ``RMSNorm`` (with the
+    residual's addition), ``RMSNormLinear`` (the norm writes the linear's
+    operand codes itself), ``linear_cross_entropy`` (a head and its loss
+    without the logits) and ``AdamW`` (fp32 or 8-bit states).
 
 Shapes follow the ABI's rules: in_features and out_features multiples of
 128 (they are contraction axes in fwd and dgrad) and a token count that is a
@@ -30,6 +34,7 @@ Everything is bf16.  There is no fallback: without libfp8bw.so the ops raise.
 """
 
 import math
+from typing import Optional
 
 import torch
 
@@ -225,3 +230,325 @@ class Float8BlockwiseLinear(torch.nn.Module):
 
     def extra_repr(self):
         return f"in_features={self.in_features}, out_features={self.out_features}, bias=False"
+
+
+# ---------------------------------------------------------------------------
+# RMS norm.
+
+
+def _empty(like, dtype=None):
+    return like.new_empty((0,), dtype=dtype)
+
+
+@torch.library.custom_op("fp8bw::rms_norm_fwd", mutates_args=())
+def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor],
+                 eps: float) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(y, s, rstd) of ops.rms_norm_fwd; s comes back empty without a
+    residual (it is x)."""
+    o = ops.rms_norm_fwd(x, weight, residual=residual, eps=eps)
+    return o.y, (_empty(x) if residual is None else o.s), o.rstd
+
+
+@rms_norm_fwd.register_fake
+def _rms_norm_fwd_fake(x, weight, residual, eps):
+    _check_2d_bf16(x)
+    rows, cols = x.shape
+    return (x.new_empty((rows, cols)), _empty(x) if residual is None else x.new_empty((rows, cols)),
+            x.new_empty((rows,), dtype=torch.float32))
+
+
+@torch.library.custom_op("fp8bw::rms_norm_bwd", mutates_args=())
+def rms_norm_bwd(dy: torch.Tensor, s: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
+                 dres: Optional[torch.Tensor]) -> tuple[torch.Tensor, torch.Tensor]:
+    """(dx, dweight) of ops.rms_norm_bwd."""
+    return ops.rms_norm_bwd(dy, s, rstd, weight, dres)
+
+
+@rms_norm_bwd.register_fake
+def _rms_norm_bwd_fake(dy, s, rstd, weight, dres):
+    return torch.empty_like(dy), torch.empty_like(weight)
+
+
+class _RMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, eps):
+        y, s, rstd = torch.ops.fp8bw.rms_norm_fwd(x, weight, residual, eps)
+        ctx.has_residual = residual is not None
+        ctx.set_materialize_grads(False)   # an unused sum costs no reading of zeros
+        ctx.save_for_backward(x if residual is None else s, rstd, weight)
+        return y, s
+
+    @staticmethod
+    def backward(ctx, dy, ds):
+        s, rstd, weight = ctx.saved_tensors
+        dres = ds.contiguous() if ctx.has_residual and ds is not None else None
+        if dy is None:
+            return dres, dres, None, None
+        dx, dweight = torch.ops.fp8bw.rms_norm_bwd(dy.contiguous(), s, rstd, weight, dres)
+        return dx, (dx if ctx.has_residual else None), dweight, None
+
+
+class RMSNorm(torch.nn.Module):
+    """Root-mean-square norm of [..., features] bf16 with a learned weight.
+    ``norm(x)`` returns y; ``norm(x, residual)`` returns (y, x + residual), the
+    sum in bf16 being the next residual."""
+
+    def __init__(self, features, eps=1e-6, device=None, dtype=torch.bfloat16):
+        super().__init__()
+        if features % 16:
+            raise ValueError("features must be a multiple of 16")
+        self.features, self.eps = features, eps
+        self.weight = torch.nn.Parameter(torch.ones(features, device=device, dtype=dtype))
+
+    def forward(self, x, residual=None):
+        shape = x.shape
+        x2 = x.reshape(-1, self.features)
+        r2 = None if residual is None else residual.reshape(-1, self.features)
+        y, s = _RMSNorm.apply(x2, r2, self.weight, self.eps)
+        return y.reshape(shape) if residual is None else (y.reshape(shape), s.reshape(shape))
+
+    def extra_repr(self):
+        return f"{self.features}, eps={self.eps}"
+
+
+# ---------------------------------------------------------------------------
+# RMS norm and FP8 linear in one: the norm writes the E4M3 codes of the GEMM's
+# operand (and, training, of its transpose), so the bf16 normed activation
+# never exists.
+
+@torch.library.custom_op("fp8bw::norm_linear_fwd", mutates_args=())
+def norm_linear_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], norm_weight: torch.Tensor,
+                    w: torch.Tensor, eps: float, train: bool
+                    ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(Y, s, rstd, qt, recip_t): Y = norm(x + residual) . W^T; s empty without
+    a residual, qt and recip_t empty unless train."""
+    _check_2d_bf16(x, w)
+    o = ops.rms_norm_fwd(x, norm_weight, residual=residual, eps=eps, y=False, q=True, qt=train)
+    wq, wr = ops.fp8_blockwise_quant(w.contiguous(), "128x128")
+    out = ops.fp8_scaled_gemm_blockwise(o.q, o.recip, wq, wr)
+    return (out, _empty(x) if residual is None else o.s, o.rstd,
+            o.qt if train else _empty(x, torch.uint8),
+            o.recip_t if train else _empty(x, torch.float32))
+
+
+@norm_linear_fwd.register_fake
+def _norm_linear_fwd_fake(x, residual, norm_weight, w, eps, train):
+    _check_2d_bf16(x, w)
+    M, K = x.shape
+    return (x.new_empty((M, w.shape[0])), _empty(x) if residual is None else x.new_empty((M, K)),
+            x.new_empty((M,), dtype=torch.float32),
+            x.new_empty((K, M), dtype=torch.uint8) if train else _empty(x, torch.uint8),
+            x.new_empty(((M + 127) // 128, K), dtype=torch.float32).t() if train
+            else _empty(x, torch.float32))
+
+
+@torch.library.custom_op("fp8bw::norm_linear_bwd", mutates_args=())
+def norm_linear_bwd(dy: torch.Tensor, ds: Optional[torch.Tensor], s: torch.Tensor,
+                    rstd: torch.Tensor, norm_weight: torch.Tensor, w: torch.Tensor,
+                    qt: torch.Tensor, recip_t: torch.Tensor
+                    ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dx, dnorm_weight, dW): dgrad and wgrad GEMMs on the linear's recipe,
+    then the norm's backward on the dgrad."""
+    dyq, dyr, dytq, dytr = ops.fp8_blockwise_quant_dual(dy.contiguous(), "1x128")
+    wtq, wtr = ops.fp8_blockwise_quant(w.contiguous(), "128x128", transpose=True)
+    dv = ops.fp8_scaled_gemm_blockwise(dyq, dyr, wtq, wtr)
+    dw = ops.fp8_scaled_gemm_blockwise(dytq, dytr, qt, recip_t, b_block="1x128")
+    dx, dnorm = ops.rms_norm_bwd(dv, s, rstd, norm_weight, ds)
+    return dx, dnorm, dw
+
+
+@norm_linear_bwd.register_fake
+def _norm_linear_bwd_fake(dy, ds, s, rstd, norm_weight, w, qt, recip_t):
+    return torch.empty_like(s), torch.empty_like(norm_weight), torch.empty_like(w)
+
+
+class _RMSNormLinear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, norm_weight, w, eps):
+        y, s, rstd, qt, recip_t = torch.ops.fp8bw.norm_linear_fwd(x, residual, norm_weight, w, eps, True)
+        ctx.has_residual = residual is not None
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(x if residual is None else s, rstd, norm_weight, w, qt, recip_t)
+        return y, s
+
+    @staticmethod
+    def backward(ctx, dy, ds):
+        s, rstd, norm_weight, w, qt, recip_t = ctx.saved_tensors
+        dres = ds.contiguous() if ctx.has_residual and ds is not None else None
+        if dy is None:
+            return dres, dres, None, None, None
+        dx, dnorm, dw = torch.ops.fp8bw.norm_linear_bwd(dy.contiguous(), dres, s, rstd, norm_weight,
+                                                        w, qt, recip_t)
+        return dx, (dx if ctx.has_residual else None), dnorm, dw, None
+
+
+class RMSNormLinear(torch.nn.Module):
+    """``Float8BlockwiseLinear(RMSNorm(x))`` with the norm writing the linear's
+    FP8 operand.  ``m(x)`` returns y; ``m(x, residual)`` returns (y, x +
+    residual).  Training needs a token count that is a multiple of 128."""
+
+    def __init__(self, in_features, out_features, eps=1e-6, device=None):
+        super().__init__()
+        self.norm = RMSNorm(in_features, eps, device=device)
+        self.linear = Float8BlockwiseLinear(in_features, out_features, device=device)
+
+    def forward(self, x, residual=None):
+        lin = self.linear
+        x2 = x.reshape(-1, lin.in_features)
+        r2 = None if residual is None else residual.reshape(-1, lin.in_features)
+        args = (x2, r2, self.norm.weight, lin.weight)
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in args):
+            if x2.shape[0] % 128:
+                raise ValueError(f"training needs the token count ({x2.shape[0]}) to be a multiple of "
+                                 "128: the weight gradient contracts over tokens in blocks of 128")
+            y, s = _RMSNormLinear.apply(*args, self.norm.eps)
+        else:
+            y, s = torch.ops.fp8bw.norm_linear_fwd(*args, self.norm.eps, False)[:2]
+        y = y.reshape(*x.shape[:-1], lin.out_features)
+        return y if residual is None else (y, s.reshape(x.shape))
+
+
+# ---------------------------------------------------------------------------
+# Cross entropy of a linear head.
+
+@torch.library.custom_op("fp8bw::linear_xent_fwd", mutates_args=())
+def linear_xent_fwd(h: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
+                    ignore_index: int) -> tuple[torch.Tensor, torch.Tensor]:
+    """(loss, lse) per token of ops.linear_xent_fwd."""
+    return ops.linear_xent_fwd(h, w, target, ignore_index)
+
+
+@linear_xent_fwd.register_fake
+def _linear_xent_fwd_fake(h, w, target, ignore_index):
+    _check_2d_bf16(h, w)
+    return tuple(h.new_empty((h.shape[0],), dtype=torch.float32) for _ in range(2))
+
+
+@torch.library.custom_op("fp8bw::linear_xent_bwd", mutates_args=())
+def linear_xent_bwd(dloss: torch.Tensor, h: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
+                    lse: torch.Tensor, ignore_index: int, need_dh: bool,
+                    need_dw: bool) -> tuple[torch.Tensor, torch.Tensor]:
+    """(dh, dw) of ops.linear_xent_bwd; one not asked for comes back empty."""
+    dh, dw = ops.linear_xent_bwd(dloss, h, w, target, lse, ignore_index, need_dh, need_dw)
+    return (_empty(h) if dh is None else dh), (_empty(w) if dw is None else dw)
+
+
+@linear_xent_bwd.register_fake
+def _linear_xent_bwd_fake(dloss, h, w, target, lse, ignore_index, need_dh, need_dw):
+    return (h.new_empty(h.shape) if need_dh else _empty(h),
+            w.new_empty(w.shape) if need_dw else _empty(w))
+
+
+class _LinearXent(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, w, target, ignore_index):
+        loss, lse = torch.ops.fp8bw.linear_xent_fwd(h, w, target, ignore_index)
+        ctx.ignore_index = ignore_index
+        ctx.save_for_backward(h, w, target, lse)
+        return loss
+
+    @staticmethod
+    def backward(ctx, dloss):
+        h, w, target, lse = ctx.saved_tensors
+        need = ctx.needs_input_grad[:2]
+        dh, dw = torch.ops.fp8bw.linear_xent_bwd(dloss.contiguous(), h, w, target, lse,
+                                                 ctx.ignore_index, *need)
+        return (dh if need[0] else None), (dw if need[1] else None), None, None
+
+
+def linear_cross_entropy(h, w, target, ignore_index=-100, reduction="mean"):
+    """Cross entropy of logits h . w^T (never kept) against target: h bf16
+    [..., K], w bf16 [V, K], target int64 [...].  reduction as in
+    ``F.cross_entropy``: "mean" over the tokens that count (NaN if none
+    does), "sum" or "none"."""
+    if reduction not in ("mean", "sum", "none"):
+        raise ValueError(f"unknown reduction {reduction!r}")
+    flat = target.reshape(-1).contiguous()
+    loss = _LinearXent.apply(h.reshape(-1, h.shape[-1]), w, flat, ignore_index)
+    if reduction == "none":
+        return loss.reshape(target.shape)
+    if reduction == "sum":
+        return loss.sum()
+    return loss.sum() / (flat != ignore_index).sum()
+
+
+# ---------------------------------------------------------------------------
+# Optimizer.
+
+class AdamW(torch.optim.Optimizer):
+    """AdamW whose step is one call of ``fp8bw_adamw_step`` per group.
+
+    state_bits: 32, or 8 for E4M3 codes with a scale per 128 elements (2.06
+    bytes of state per parameter instead of 8).  master_weights: fp32 copies
+    behind bf16 parameters.  stochastic: round codes, and bf16 parameters
+    without a master, up or down at random by a hash of (seed, step, tensor,
+    element); default: wherever something is so held.  ``step(grad_scale=t)``
+    multiplies every gradient by the one-element fp32 tensor t."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, state_bits=32,
+                 master_weights=False, stochastic=True, seed=0):
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        if lr < 0 or eps < 0 or weight_decay < 0 or not all(0 <= b < 1 for b in betas):
+            raise ValueError("lr, eps and weight_decay must be >= 0 and betas in [0, 1)")
+        self.state_bits, self.master_weights = state_bits, master_weights
+        self.stochastic, self.seed = stochastic, seed
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay))
+
+    def _new_state(self, p):
+        st = {"step": 0}
+        n = ops.adamw_scales(p.numel())
+        if self.state_bits == 8:
+            for k in ("exp_avg", "exp_avg_root"):
+                st[k] = torch.zeros(p.numel(), dtype=torch.uint8, device=p.device)
+                st[k + "_scale"] = torch.ones(n, dtype=torch.float32, device=p.device)
+        else:
+            st["exp_avg"] = torch.zeros_like(p, dtype=torch.float32, memory_format=torch.contiguous_format)
+            st["exp_avg_sq"] = torch.zeros_like(st["exp_avg"])
+        if self.master_weights and p.dtype == torch.bfloat16:
+            st["master"] = p.detach().float().contiguous()
+        return st
+
+    @torch.no_grad()
+    def step(self, closure=None, grad_scale=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            by_step = {}
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                if not self.state[p]:
+                    self.state[p].update(self._new_state(p))
+                st = self.state[p]
+                st["step"] += 1
+                by_step.setdefault((p.device, st["step"]), []).append((p, st))
+            for (_, step), tensors in by_step.items():
+                self._step_group(group, step, tensors, grad_scale)
+        return loss
+
+    def _step_group(self, group, step, tensors, grad_scale):
+        states = [st for _, st in tensors]
+        eight = self.state_bits == 8
+        second = "exp_avg_root" if eight else "exp_avg_sq"
+        ops.adamw_step([p for p, _ in tensors], [p.grad.contiguous() for p, _ in tensors],
+                       [st["exp_avg"] for st in states], [st[second] for st in states], step=step,
+                       lr=group["lr"], beta1=group["betas"][0], beta2=group["betas"][1],
+                       eps=group["eps"], weight_decay=group["weight_decay"],
+                       exp_avg_scales=[st["exp_avg_scale"] for st in states] if eight else None,
+                       root_scales=[st["exp_avg_root_scale"] for st in states] if eight else None,
+                       masters=[st.get("master") for st in states], grad_scale=grad_scale,
+                       seed=(self.seed + 0x9E3779B97F4A7C15 * step) & 0xFFFFFFFFFFFFFFFF
+                       if self.stochastic else None)
+
+    def load_state_dict(self, state_dict):
+        """As torch's, but states keep their types (torch casts floating
+        parameters' states to the parameter's type, which codes do not survive)."""
+        super().load_state_dict(state_dict)
+        saved = [i for g in state_dict["param_groups"] for i in g["params"]]
+        mine = [p for g in self.param_groups for p in g["params"]]
+        for i, p in zip(saved, mine):
+            for k, v in state_dict["state"].get(i, {}).items():
+                self.state[p][k] = v.detach().clone().to(p.device) if isinstance(v, torch.Tensor) else v
