@@ -25,6 +25,8 @@
 // epilogues multiply back in fp32: with the usual equal weights of a mean
 // loss nothing but G's own rounding remains.
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "launch.h"
 
@@ -36,6 +38,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
+constexpr int kCus = 256;   // compute units of an MI355X
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // What a product's epilogue does with its tile.
@@ -54,7 +57,8 @@ struct XentGemm {
   int a_rows, b_rows;
   int M, N;
   int kblocks;                     // of 64 elements (128 bytes)
-  int kb_per_split;
+  int kb_per_split, splits;
+  int rounds;                      // tiles per workgroup (large tiles)
   int tiles_m, tiles_n;
   // kStats
   float2* part;                    // [tiles_n][M] (max, sum of exp(z - max))
@@ -135,8 +139,8 @@ template <int C, bool KM, bool CLAMP>
 struct SlabLoader {
   static constexpr int N = C / 16;                 // loads a wave
   static constexpr int RPL = KM ? 512 / C : 8;     // rows a load covers
-  uint32_t off[KM ? 2 : CLAMP ? N : 1];
-  uint32_t col[2];                                 // KM: a lane's column bytes, by the swizzle's top bit
+  uint32_t off[CLAMP && !KM ? N : 1];
+  uint32_t col0, col1;                             // KM: a lane's column bytes, by the swizzle's top bit
   const uint8_t* base;
   int64_t ld;
   int rows, lrow, wave;
@@ -153,15 +157,15 @@ struct SlabLoader {
       base = p + 2 * (int64_t)first;
       lrow = lane / (64 / RPL);
       const int chunk = lane % (64 / RPL);
-#pragma unroll
-      for (int top = 0; top < 2; ++top) {
-        // row = RPL (wave + 2 i) + lrow; its bit 4 comes from i alone
-        const int swz = km_swz<C>((RPL * wave + lrow) & 15) | top << (C == 256 ? 2 : 1);
-        int c = 16 * ((chunk >> 1) ^ swz) + 8 * (chunk & 1);
-        if (CLAMP) c = min(c, limit - first - 8);   // past the last column: any of them
-        col[top] = 2 * c;
-        off[top] = (uint32_t)((RPL * wave + lrow) * (int)ld) + col[top];
-      }
+      // row = RPL (wave + 2 i) + lrow; its bit 4 comes from i alone
+      const int swz = km_swz<C>((RPL * wave + lrow) & 15);
+      auto column = [&](int top) {
+        const int c = 16 * ((chunk >> 1) ^ (swz | top << (C == 256 ? 2 : 1))) + 8 * (chunk & 1);
+        return (uint32_t)(2 * (CLAMP ? min(c, limit - first - 8) : c));   // past the last column: any of them
+      };
+      col0 = column(0);
+      col1 = column(1);
+      off[0] = (uint32_t)((RPL * wave + lrow) * (int)ld);
     } else {
       base = p + (int64_t)first * ld;
       rsrc = rsrc_of(base, (int64_t)C * ld);
@@ -176,29 +180,43 @@ struct SlabLoader {
   }
   __device__ __forceinline__ void issue(int kb, uint8_t* lds) const {
 #if defined(__HIP_DEVICE_COMPILE__)
+    // The scalar offset and the LDS address step from load to load; opaque, or
+    // the compiler keeps all N values of each in scalar registers and spills.
+    int to = __builtin_amdgcn_readfirstlane(wave * 1024);
     if constexpr (!KM) {
+      const int step = CLAMP ? 0 : __builtin_amdgcn_readfirstlane(16 * (int)ld);
+      int so = kb * 128;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + (wave + 2 * i) * 1024), 16,
-                                                 off[CLAMP ? i : 0],
-                                                 kb * 128 + (CLAMP ? 0 : 16 * i * (int)ld), 0, 0);
+      for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + to), 16, off[CLAMP ? i : 0], so, 0, 0);
+        so += step;
+        to += 2048;
+        asm volatile("" : "+s"(so), "+s"(to));
+      }
     } else {
       // A descriptor of its own per slab: offsets stay within 64 rows.
       const __amdgpu_buffer_rsrc_t rs = rsrc_of(base + (int64_t)kb * 64 * ld, 64 * ld);
       const int left = rows - kb * 64;
       if (left >= 64) {
+        const int step = __builtin_amdgcn_readfirstlane(2 * RPL * (int)ld);
+        int so = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + (wave + 2 * i) * 1024), 16,
-                                                   off[(2 * RPL * i >> 4) & 1], 2 * RPL * i * (int)ld, 0, 0);
+        for (int i = 0; i < N; ++i) {
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + to), 16,
+                                                   off[0] + ((2 * RPL * i >> 4) & 1 ? col1 : col0), so, 0, 0);
+          so += step;
+          to += 2048;
+          asm volatile("" : "+s"(so), "+s"(to));
+        }
       } else {
         // Rows past the last read that one: the other operand is zero there.
 #pragma unroll
         for (int i = 0; i < N; ++i)
           __builtin_amdgcn_raw_ptr_buffer_load_lds(
               rs, (lds_void*)(lds + (wave + 2 * i) * 1024), 16,
-              (uint32_t)(min(RPL * (wave + 2 * i) + lrow, left - 1) * (int)ld) + col[(2 * RPL * i >> 4) & 1], 0, 0,
-              0);
+              (uint32_t)(min(RPL * (wave + 2 * i) + lrow, left - 1) * (int)ld) +
+                  ((2 * RPL * i >> 4) & 1 ? col1 : col0),
+              0, 0, 0);
       }
     }
 #endif
@@ -238,6 +256,12 @@ struct FragReader {
   }
 };
 
+// One output tile: its own rows [m0, ..) and columns [n0, ..), the window that
+// its loads cover, and its slabs.
+struct Tile {
+  int m0, n0, ml, nl, tn, split, kb0, kb1;
+};
+
 // C[m, n] = sum_k A[m, k] B[n, k] on BM x BN tiles of WGM x WGN waves.  Two
 // stages of 64 contraction elements in LDS, filled by direct buffer -> LDS
 // loads from waves 0 and 1 (a direct load keeps the issuing wave for about 16
@@ -245,245 +269,312 @@ struct FragReader {
 // variable of its own and the stage loop is unrolled, so that the compiler
 // sees that reads of one stage do not depend on loads into the other.
 //
-// Edges: with CLAMP every lane's row is clamped to the last one (any M, N);
-// without, M >= BM and N >= BN, and an edge tile's window moves back to end
-// at the last row, so no load needs a register of its own for its row.  A
-// KM operand A needs neither: its rows are at least tiles_m BM columns long.
-// Either way a tile's epilogue handles only its own rows and columns.
-template <int BM, int BN, int WGM, int WGN, bool CLAMP, int EPI, bool AKM, bool BKM>
+// A workgroup of the 256 x 256 kernel runs `rounds` tiles, a chip's worth of
+// workgroups apart, and starts the next tile's first slab before it works off
+// this one's epilogue, which uses LDS beside the stages; its results are stored
+// by the waves that load nothing, so that no load waits for them.
+//
+// Edges: the 64-row kernel (SMALL) clamps every lane's row to the last one
+// (any M, N); the large one has M >= BM and N >= BN, and an edge tile's window
+// moves back to end at the last row, so no load needs a register of its own
+// for its row.  A KM operand A needs neither: its rows are at least tiles_m BM
+// columns long.  Either way a tile's epilogue handles only its own rows and
+// columns.
+template <int BM, int BN, int WGM, int WGN, int EPI, bool AKM, bool BKM>
 __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGemm p) {
+  constexpr bool SMALL = BM == 64;
   constexpr int NW = WGM * WGN;
   constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16;
+  constexpr bool ROWS = EPI == kStats || EPI == kGrad;       // the epilogue needs its rows' targets
+  constexpr bool STAGED = !SMALL && (EPI == kGrad || EPI == kOut);
   __shared__ __attribute__((aligned(1024))) uint8_t sA0[BM * 128], sA1[BM * 128];
   __shared__ __attribute__((aligned(1024))) uint8_t sB0[BN * 128], sB1[BN * 128];
+  // The epilogue's own: 64 rows of bf16 results, or each wave's row statistics.
+  // (The small kernel, two workgroups a CU, uses a stage for the latter.)
+  __shared__ __attribute__((aligned(16))) uint8_t sE[STAGED ? 64 * 512 : !SMALL && EPI == kStats ? WGN * BM * 8 : 16];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm0 = (wave / WGN) * WM, wn0 = (wave % WGN) * WN;
   const int frow = lane & 15, fq = lane >> 4;
+  const int tiles = p.tiles_m * p.tiles_n, total = tiles * p.splits;
   // (split, tile), split-major, contiguous per XCD
-  const int id = xcd_order(blockIdx.y * gridDim.x + blockIdx.x, gridDim.x * gridDim.y);
-  const int split = id / gridDim.x;
-  int tm, tn;
-  tile_order(id - split * gridDim.x, p.tiles_m, p.tiles_n, &tm, &tn);
-  const int m0 = tm * BM, n0 = tn * BN;
-  const int ml = CLAMP || AKM ? m0 : min(m0, p.M - BM), nl = CLAMP ? n0 : min(n0, p.N - BN);
-  const int kb0 = split * p.kb_per_split, kb1 = min(p.kblocks, kb0 + p.kb_per_split);
-
-  SlabLoader<BM, AKM, CLAMP && !AKM> la;
-  SlabLoader<BN, BKM, CLAMP> lb;
-  la.init(p.a, p.lda, ml, p.M, p.a_rows, wave, lane);
-  lb.init(p.b, p.ldb, nl, p.N, p.b_rows, wave, lane);
-  auto issue = [&](int kb, uint8_t* sa, uint8_t* sb) {
+  auto locate = [&](int n) __attribute__((always_inline)) -> Tile {
+    const int id = xcd_order(n, total);
+    Tile t;
+    t.split = id / tiles;
+    int tm;
+    tile_order(id - t.split * tiles, p.tiles_m, p.tiles_n, &tm, &t.tn);
+    t.m0 = tm * BM;
+    t.n0 = t.tn * BN;
+    t.ml = SMALL || AKM ? t.m0 : min(t.m0, p.M - BM);
+    t.nl = SMALL ? t.n0 : min(t.n0, p.N - BN);
+    t.kb0 = t.split * p.kb_per_split;
+    t.kb1 = min(p.kblocks, t.kb0 + p.kb_per_split);
+    return t;
+  };
+  SlabLoader<BM, AKM, SMALL && !AKM> la;
+  SlabLoader<BN, BKM, SMALL> lb;
+  auto issue = [&](int kb, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
     if (wave < 2) {
       la.issue(kb, sa);
       lb.issue(kb, sb);
     }
   };
+  auto begin = [&](const Tile& t) __attribute__((always_inline)) {
+    la.init(p.a, p.lda, t.ml, p.M, p.a_rows, wave, lane);
+    lb.init(p.b, p.ldb, t.nl, p.N, p.b_rows, wave, lane);
+    if (t.kb0 < t.kb1) issue(t.kb0, sA0, sB0);
+  };
+  float scale = 1.f;
+  if constexpr (EPI == kOut) scale = *p.scale;
 
-  v4f acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-
-  if (kb0 < kb1) issue(kb0, sA0, sB0);
-  ring_sync();
-  for (int it = kb0; it < kb1; it += 2) {
-#pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      const int kb = it + st;
-      if (kb >= kb1) break;
-      // past the end the last slab is loaded again, into a stage nobody reads
-      issue(min(kb + 1, kb1 - 1), st ? sA0 : sA1, st ? sB0 : sB1);
-      const uint8_t* const ta = st ? sA1 : sA0;
-      const uint8_t* const tb = st ? sB1 : sB0;
-      FragReader<BM, AKM> ra;
-      FragReader<BN, BKM> rb;
-      ra.init(wm0, lane);
-      rb.init(wn0, lane);
-      bf16x8 bl[TN], bh[TN], al[2], ah[2];
-      bl[0] = rb.low(tb, 0);
-      al[0] = ra.low(ta, 0);
-#pragma unroll
-      for (int j = 1; j < TN; ++j) bl[j] = rb.low(tb, j);
-      ah[0] = ra.high(ta, 0);
-#pragma unroll
-      for (int j = 0; j < TN; ++j) bh[j] = rb.high(tb, j);
-      __builtin_amdgcn_sched_barrier(0);
+  // Workgroups 0 .. kCus - 1 start with tiles 0 .. kCus - 1, the next kCus
+  // after all of theirs.
+  int number = SMALL ? blockIdx.x : blockIdx.x / kCus * (kCus * p.rounds) + blockIdx.x % kCus;
+  if (number >= total) return;
+  const int last = SMALL ? total : min(total, (int)(blockIdx.x / kCus + 1) * kCus * p.rounds);
+  Tile t = locate(number);
+  begin(t);
+  for (;;) {
+    // The epilogue's rows, read before the slabs so that nothing waits for
+    // them: target column in this wave's, lse and weight.
+    int tgt[ROWS ? TM : 1];
+    float2 info[EPI == kGrad ? TM : 1];
+    if constexpr (ROWS) {
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        if (i + 1 < TM) {
-          al[(i + 1) & 1] = ra.low(ta, i + 1);
-          ah[(i + 1) & 1] = ra.high(ta, i + 1);
-          __builtin_amdgcn_sched_barrier(0);   // keep the next row's reads ahead of this row's MFMAs
-        }
-        // B first: lane l then holds row 16 i + l % 16, columns 16 j + 4 (l / 16) + 0..3
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bl[j], al[i & 1], acc[i][j], 0, 0, 0);
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bh[j], ah[i & 1], acc[i][j], 0, 0, 0);
+        const int r = min(t.ml + wm0 + 16 * i + frow, p.M - 1);
+        const int64_t y = (EPI == kGrad ? (int64_t)p.local_target[r] - p.v0 : p.target[r]) - (t.nl + wn0);
+        tgt[i] = y >= 0 && y < WN ? (int)y : -1;
+        if constexpr (EPI == kGrad) info[i] = p.row[r];
       }
-      ring_sync();
     }
-  }
-  __syncthreads();   // every wave's reads and loads are done: the stages are free
+    v4f acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  const int row0 = ml + wm0 + frow;            // + 16 i
-  const int col0 = nl + wn0 + 4 * fq;          // + 16 j + v
-  if constexpr (EPI == kStats) {
-    // Maximum and sum of exponentials of each row over this wave's columns
-    // (a row's columns lie in lanes frow + 16 q), then over the waves.
-    float2* const red = (float2*)sA0;          // [WGN][BM]
+    ring_sync();
+    for (int it = t.kb0; it < t.kb1; it += 2) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int r = row0 + 16 * i;
-      const bool mine = r >= m0 && r < p.M;
-      const int64_t tgt = mine ? p.target[r] : -1;
-      float m = -INFINITY;
+      for (int st = 0; st < 2; ++st) {
+        const int kb = it + st;
+        if (kb >= t.kb1) break;
+        // past the end the last slab is loaded again, into a stage nobody reads
+        issue(min(kb + 1, t.kb1 - 1), st ? sA0 : sA1, st ? sB0 : sB1);
+        const uint8_t* const ta = st ? sA1 : sA0;
+        const uint8_t* const tb = st ? sB1 : sB0;
+        FragReader<BM, AKM> ra;
+        FragReader<BN, BKM> rb;
+        ra.init(wm0, lane);
+        rb.init(wn0, lane);
+        bf16x8 bl[TN], bh[TN], al[2], ah[2];
+        bl[0] = rb.low(tb, 0);
+        al[0] = ra.low(ta, 0);
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
+        for (int j = 1; j < TN; ++j) bl[j] = rb.low(tb, j);
+        ah[0] = ra.high(ta, 0);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int n = col0 + 16 * j + v;
-          const bool in = n >= n0 && n < p.N;
-          if (in && (int64_t)n == tgt) p.target_logit[r] = acc[i][j][v];
-          // A NaN logit has to reach the sum: fmaxf drops it, the sum does not.
-          if (in) m = fmaxf(m, acc[i][j][v]);
-        }
-      m = fmaxf(m, __shfl_xor(m, 16));
-      m = fmaxf(m, __shfl_xor(m, 32));
-      const float base = m == -INFINITY ? 0.f : m;   // no column, or all at -inf
-      float s = 0.f;
+        for (int j = 0; j < TN; ++j) bh[j] = rb.high(tb, j);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int n = col0 + 16 * j + v;
-          if (n >= n0 && n < p.N) s += __builtin_amdgcn_exp2f((acc[i][j][v] - base) * kLog2e);
-        }
-      s += __shfl_xor(s, 16);
-      s += __shfl_xor(s, 32);
-      if (fq == 0) red[(wave % WGN) * BM + wm0 + 16 * i + frow] = make_float2(m, s);
-    }
-    __syncthreads();
-    for (int r = threadIdx.x; r < BM; r += 64 * NW) {
-      float m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < WGN; ++w) m = fmaxf(m, red[w * BM + r].x);
-      float s = 0.f;
-#pragma unroll
-      for (int w = 0; w < WGN; ++w) {
-        const float2 e = red[w * BM + r];
-        if (e.x != -INFINITY) s += e.y * __builtin_amdgcn_exp2f((e.x - m) * kLog2e);
-        else s += e.y;     // 0, or NaN
-      }
-      const int row = ml + r;
-      if (row >= m0 && row < p.M) p.part[(int64_t)tn * p.M + row] = make_float2(m, s);
-    }
-  } else if constexpr (EPI == kAcc) {
-    float* const base = p.acc + (int64_t)split * p.M * p.N;
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      const int r = row0 + 16 * i;
-      if (r < m0 || r >= p.M) continue;
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        // N is a multiple of 64 and a window starts on a multiple of 64, so
-        // four columns are all this tile's or none is
-        const int n = col0 + 16 * j;
-        if (n < n0 || n >= p.N) continue;
-        float4* const at = (float4*)(base + (int64_t)r * p.N + n);
-        float4 o = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
-        if (p.add) {
-          const float4 e = *at;
-          o.x += e.x; o.y += e.y; o.z += e.z; o.w += e.w;
-        }
-        *at = o;
-      }
-    }
-  } else {
-    float scale = 1.f;
-    if constexpr (EPI == kOut) scale = *p.scale;
-    // The 16 values of lane row i: G's, or the product's times scale.
-    auto values = [&](int i, float (&val)[TN][4]) {
-      const int r = row0 + 16 * i;
-      if constexpr (EPI == kGrad) {
-        const float2 info = p.row[min(r, p.M - 1)];
-        const int tgt = p.local_target[min(r, p.M - 1)] - p.v0;
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            float e = __builtin_amdgcn_exp2f((acc[i][j][v] - info.x) * kLog2e);
-            if (col0 + 16 * j + v == tgt) e -= 1.f;
-            // a row of weight zero (an ignored target) has no gradient, whatever its logits
-            val[j][v] = info.y == 0.f ? 0.f : e * info.y;
+        for (int i = 0; i < TM; ++i) {
+          if (i + 1 < TM) {
+            al[(i + 1) & 1] = ra.low(ta, i + 1);
+            ah[(i + 1) & 1] = ra.high(ta, i + 1);
+            __builtin_amdgcn_sched_barrier(0);   // keep the next row's reads ahead of this row's MFMAs
           }
-      } else {
+          // B first: lane l then holds row 16 i + l % 16, columns 16 j + 4 (l / 16) + 0..3
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+          for (int j = 0; j < TN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bl[j], al[i & 1], acc[i][j], 0, 0, 0);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) val[j][v] = acc[i][j][v] * scale;
-      }
-    };
-    uint16_t* const out = (uint16_t*)p.out;
-    if (BM == 256 && (nl & 7) == 0) {
-      // Through LDS, so that every store writes whole lines (in the MFMA layout
-      // a row of a wave's columns would leave in pieces of 32 bytes): 64 rows of
-      // 512 bytes in each stage array, 16-byte chunk c of row r at c ^ (r & 15).
-      auto quarter = [&](int q) -> uint8_t* { return q == 0 ? sA0 : q == 1 ? sA1 : q == 2 ? sB0 : sB1; };
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        float val[TN][4];
-        values(i, val);
-        uint8_t* const rowp = quarter((wm0 + 16 * i) >> 6) + ((wm0 + 16 * i + frow) & 63) * 512;
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          *(uint2*)(rowp + 16 * (((wn0 >> 3) + 2 * j + (fq >> 1)) ^ frow) + 8 * (fq & 1)) =
-              make_uint2(pack_bf16x2_rne(val[j][0], val[j][1]), pack_bf16x2_rne(val[j][2], val[j][3]));
-      }
-      __syncthreads();
-      const uint8_t* const src = quarter(wave >> 1);
-      const int c = lane & 31, n = nl + 8 * c;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int rr = 32 * (wave & 1) + 2 * k + (lane >> 5);
-        const int r = ml + 64 * (wave >> 1) + rr;
-        const u32x4_t d = *(const u32x4_t*)(src + rr * 512 + 16 * (c ^ (rr & 15)));
-        if (r < m0 || r >= p.M || n + 7 < n0 || n >= p.N) continue;
-        uint16_t* const at = out + (int64_t)r * p.ldo + n;
-        if (n >= n0 && n + 7 < p.N) {
-          if constexpr (EPI == kOut) __builtin_nontemporal_store(d, (u32x4_t*)at);
-          else *(u32x4_t*)at = d;   // the next products read G
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (n + e >= n0 && n + e < p.N) at[e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
+          for (int j = 0; j < TN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bh[j], ah[i & 1], acc[i][j], 0, 0, 0);
         }
+        ring_sync();
       }
-    } else {
+    }
+    __syncthreads();   // every wave's reads and loads are done: the stages are free
+    const Tile d = t;
+    number += kCus;
+    const bool more = !SMALL && number < last;
+    if (more) {
+      t = locate(number);
+      begin(t);
+    }
+
+    const int row0 = d.ml + wm0 + frow;            // + 16 i
+    const int col0 = d.nl + wn0 + 4 * fq;          // + 16 j + v
+    // Whether every column of this wave's is the tile's own.
+    const bool whole = d.nl + wn0 >= d.n0 && d.nl + wn0 + WN <= p.N;
+    if constexpr (EPI == kStats) {
+      // Maximum and sum of exponentials of each row over this wave's columns
+      // (a row's columns lie in lanes frow + 16 q), then over the waves.
+      float2* const red = (float2*)(SMALL ? sA0 : sE);          // [WGN][BM]
+      auto statistics = [&](auto check) __attribute__((always_inline)) {
+        constexpr bool kCheck = decltype(check)::value;
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const int r = row0 + 16 * i;
+          if (__builtin_amdgcn_ballot_w64(tgt[i] >= 0)) {       // a target among these columns: rarely
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                if (16 * j + 4 * fq + v == tgt[i] && r >= d.m0 && r < p.M && col0 + 16 * j + v >= d.n0)
+                  p.target_logit[r] = acc[i][j][v];
+          }
+          float m = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              if constexpr (kCheck) {
+                const int n = col0 + 16 * j + v;
+                if (n < d.n0 || n >= p.N) acc[i][j][v] = -INFINITY;
+              }
+              m = fmaxf(m, acc[i][j][v]);   // drops a NaN; the sum below does not
+            }
+          m = fmaxf(m, __shfl_xor(m, 16));
+          m = fmaxf(m, __shfl_xor(m, 32));
+          const float base = m == -INFINITY ? 0.f : m;   // no column, or all at -inf
+          float s = 0.f;
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) s += __builtin_amdgcn_exp2f((acc[i][j][v] - base) * kLog2e);
+          s += __shfl_xor(s, 16);
+          s += __shfl_xor(s, 32);
+          if (fq == 0) red[(wave % WGN) * BM + wm0 + 16 * i + frow] = make_float2(m, s);
+        }
+      };
+      if (whole) statistics(std::false_type{});
+      else statistics(std::true_type{});
+      __syncthreads();
+      for (int r = threadIdx.x; r < BM; r += 64 * NW) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WGN; ++w) m = fmaxf(m, red[w * BM + r].x);
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < WGN; ++w) {
+          const float2 e = red[w * BM + r];
+          if (e.x != -INFINITY) s += e.y * __builtin_amdgcn_exp2f((e.x - m) * kLog2e);
+          else s += e.y;     // 0, or NaN
+        }
+        const int row = d.ml + r;
+        if (row >= d.m0 && row < p.M) p.part[(int64_t)d.tn * p.M + row] = make_float2(m, s);
+      }
+    } else if constexpr (EPI == kAcc) {
+      float* const base = p.acc + (int64_t)d.split * p.M * p.N;
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         const int r = row0 + 16 * i;
-        float val[TN][4];
-        values(i, val);
-        if (r < m0 || r >= p.M) continue;
+        if (r < d.m0 || r >= p.M) continue;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
+          // N is a multiple of 64 and a window starts on a multiple of 64, so
+          // four columns are all this tile's or none is
           const int n = col0 + 16 * j;
-          uint16_t* const at = out + (int64_t)r * p.ldo + n;
-          if (n >= n0 && n + 3 < p.N && (n & 3) == 0) {
-            *(uint2*)at = make_uint2(pack_bf16x2_rne(val[j][0], val[j][1]), pack_bf16x2_rne(val[j][2], val[j][3]));
-          } else {
+          if (n < d.n0 || n >= p.N) continue;
+          float4* const at = (float4*)(base + (int64_t)r * p.N + n);
+          float4 o = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+          if (p.add) {
+            const float4 e = *at;
+            o.x += e.x; o.y += e.y; o.z += e.z; o.w += e.w;
+          }
+          *at = o;
+        }
+      }
+    } else {
+      uint16_t* const out = (uint16_t*)p.out;
+      // Lane row i's columns as bf16: G's, or the product times scale.
+      auto results = [&](int i, uint2 (&w)[TN]) __attribute__((always_inline)) {
+        if constexpr (EPI == kGrad) {
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-              if (n + v >= n0 && n + v < p.N) at[v] = (uint16_t)f32_to_bf16_rne(val[j][v]);
+              acc[i][j][v] = __builtin_amdgcn_exp2f((acc[i][j][v] - info[i].x) * kLog2e);
+          if (__builtin_amdgcn_ballot_w64(tgt[i] >= 0)) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                if (16 * j + 4 * fq + v == tgt[i]) acc[i][j][v] -= 1.f;
+          }
+        }
+        const float f = EPI == kGrad ? info[i].y : scale;
+        // a row of weight zero (an ignored target) has no gradient, whatever its logits
+        const uint32_t keep = EPI == kGrad && f == 0.f ? 0u : ~0u;
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+          w[j] = make_uint2(pack_bf16x2_rne(acc[i][j][0] * f, acc[i][j][1] * f) & keep,
+                            pack_bf16x2_rne(acc[i][j][2] * f, acc[i][j][3] * f) & keep);
+      };
+      if (STAGED && (d.nl & 7) == 0) {
+        // Through LDS, so that every store writes whole lines (in the MFMA
+        // layout a row of a wave's columns would leave in pieces of 32 bytes):
+        // 64 rows of 512 bytes at a time, 16-byte chunk c of row r at
+        // c ^ (r & 15).
+#pragma unroll
+        for (int q = 0; q < BM / 64; ++q) {
+          if (wm0 / 128 == q / 2) {
+#pragma unroll
+            for (int ii = 0; ii < 4; ++ii) {
+              uint2 w[TN];
+              results((4 * q + ii) % TM, w);
+              uint8_t* const rowp = sE + (16 * ii + frow) * 512;
+#pragma unroll
+              for (int j = 0; j < TN; ++j)
+                *(uint2*)(rowp + 16 * (((wn0 >> 3) + 2 * j + (fq >> 1)) ^ frow) + 8 * (fq & 1)) = w[j];
+            }
+          }
+          __syncthreads();
+          const int c = lane & 31, n = d.nl + 8 * c;
+          if (wave >= 2) {
+            for (int pr = wave - 2; pr < 32; pr += NW - 2) {
+              const int rr = 2 * pr + (lane >> 5), r = d.ml + 64 * q + rr;
+              const u32x4_t v = *(const u32x4_t*)(sE + rr * 512 + 16 * (c ^ (rr & 15)));
+              if (r < d.m0 || r >= p.M || n + 7 < d.n0 || n >= p.N) continue;
+              uint16_t* const at = out + (int64_t)r * p.ldo + n;
+              if (n >= d.n0 && n + 7 < p.N) {
+                if constexpr (EPI == kOut) __builtin_nontemporal_store(v, (u32x4_t*)at);
+                else *(u32x4_t*)at = v;   // the next products read G
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (n + e >= d.n0 && n + e < p.N) at[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+              }
+            }
+          }
+          __syncthreads();
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          const int r = row0 + 16 * i;
+          uint2 w[TN];
+          results(i, w);
+          if (r < d.m0 || r >= p.M) continue;
+#pragma unroll
+          for (int j = 0; j < TN; ++j) {
+            const int n = col0 + 16 * j;
+            uint16_t* const at = out + (int64_t)r * p.ldo + n;
+            if (n >= d.n0 && n + 3 < p.N && (n & 3) == 0) {
+              *(uint2*)at = w[j];
+            } else {
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                if (n + v >= d.n0 && n + v < p.N) at[v] = (uint16_t)((v < 2 ? w[j].x : w[j].y) >> (16 * (v & 1)));
+            }
           }
         }
       }
     }
+    if (!more) return;
   }
 }
 
@@ -575,7 +666,6 @@ __global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ 
   }
 }
 
-constexpr int kCus = 256;
 
 // Large tiles once they (times the splits of the contraction) fill half the
 // chip's compute units; below that 64-row tiles give four times the workgroups
@@ -584,16 +674,27 @@ bool large_tiles(int64_t M, int64_t N, int64_t splits) {
   return M >= 256 && N >= 256 && ((M + 255) / 256) * ((N + 255) / 256) * splits >= kCus / 2;
 }
 
+// Tiles a workgroup: more hide more epilogues, but workgroups drift apart
+// within a launch and then share fewer operand slices in the L2.
+constexpr int kRounds = 4;
+
 template <int EPI, bool AKM = false, bool BKM = false>
 hipError_t run_gemm(XentGemm p, int splits, hipStream_t stream) {
   const bool large = large_tiles(p.M, p.N, splits);
   const int bm = large ? 256 : 64;
   p.tiles_m = (p.M + bm - 1) / bm;
   p.tiles_n = (p.N + 255) / 256;
+  p.splits = splits;
   p.kb_per_split = (p.kblocks + splits - 1) / splits;
-  const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)splits);
-  if (large) hipLaunchKernelGGL((xent_gemm_kernel<256, 256, 2, 4, false, EPI, AKM, BKM>), grid, dim3(512), 0, stream, p);
-  else hipLaunchKernelGGL((xent_gemm_kernel<64, 256, 1, 4, true, EPI, AKM, BKM>), grid, dim3(256), 0, stream, p);
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * splits;
+  if (large) {
+    p.rounds = kRounds;
+    const int64_t groups = (tiles + kCus * p.rounds - 1) / (kCus * p.rounds) * kCus;
+    hipLaunchKernelGGL((xent_gemm_kernel<256, 256, 2, 4, EPI, AKM, BKM>), dim3((unsigned)groups), dim3(512), 0, stream,
+                       p);
+  } else {
+    hipLaunchKernelGGL((xent_gemm_kernel<64, 256, 1, 4, EPI, AKM, BKM>), dim3((unsigned)tiles), dim3(256), 0, stream, p);
+  }
   return hipGetLastError();
 }
 
