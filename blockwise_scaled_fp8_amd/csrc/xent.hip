@@ -80,10 +80,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int6
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)n, 0x00020000);
 }
 
-// Waits of the two-stage ring (gfx9 s_waitcnt encoding): this wave's direct
-// loads have landed and its LDS reads returned, then the barrier.
+// Wait of the slab ring (gfx9 s_waitcnt encoding): at most N of this wave's
+// direct loads are still on their way (those of later slabs), its LDS reads
+// have returned, then the barrier.
+template <int N>
 __device__ __forceinline__ void ring_sync() {
-  __builtin_amdgcn_s_waitcnt(0x7 << 4);
+  static_assert(N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | (N >> 4) << 14 | 0x7 << 4);
   __builtin_amdgcn_s_barrier();
 }
 
@@ -118,9 +121,11 @@ __device__ __forceinline__ bf16x8 frag(const uint8_t* tile, uint32_t off) {
 // 16-lane group is element i % 4 of the 8 bytes that lane 4 e + i / 4
 // addresses), so half a wave reads rows {0-3, 16-19} (+ a constant) of one
 // unit column: the swizzle spreads these 8 pieces of 32 bytes over all banks.
+// (Rows of 128 bytes, C = 64, alternate between two halves of the banks: two
+// bits then do, from the rows of one half.)
 template <int C>
 __device__ __forceinline__ int km_swz(int row) {
-  return C == 256 ? (row & 3) | ((row >> 4) & 1) << 2 : ((row >> 1) & 1) | ((row >> 4) & 1) << 1;
+  return C >= 128 ? (row & 3) | ((row >> 4) & 1) << 2 : ((row >> 1) & 1) | ((row >> 4) & 1) << 1;
 }
 template <int C>
 __device__ __forceinline__ bf16x8 frag_km(const uint8_t* tile, uint32_t off) {
@@ -134,20 +139,22 @@ __device__ __forceinline__ bf16x8 frag_km(const uint8_t* tile, uint32_t off) {
 }
 
 // One operand's slab by direct loads from waves 0 and 1: C rows of 128 bytes,
-// or with KM 64 rows of 2 C bytes; 1 KB an instruction either way.
-template <int C, bool KM, bool CLAMP>
+// or with KM 64 rows of 2 C bytes; 1 KB an instruction either way.  Nothing
+// past the operand is read: rows (KM: columns) past its end are replaced by
+// ones before it, which reach only results that nobody stores.
+template <int C, bool KM>
 struct SlabLoader {
   static constexpr int N = C / 16;                 // loads a wave
   static constexpr int RPL = KM ? 512 / C : 8;     // rows a load covers
-  uint32_t off[CLAMP && !KM ? N : 1];
-  uint32_t col0, col1;                             // KM: a lane's column bytes, by the swizzle's top bit
+  uint32_t off, off_edge;       // a lane's offset in a load's rows; in the load that holds the last row
+  uint32_t col0, col1;          // KM: a lane's column bytes, by the swizzle's top bit
   const uint8_t* base;
   int64_t ld;
-  int rows, lrow, wave;
+  int rows, lrow, wave, edge;   // KM: contraction rows; else the load number that holds the last row, -1: all exist
   __amdgpu_buffer_rsrc_t rsrc;
 
-  // first: first row (KM: column) of the tile's window; limit: rows (columns)
-  // of the operand; k_rows: its contraction rows (KM).
+  // first: first row (KM: column) of the tile; limit: the operand's; k_rows:
+  // its contraction rows (KM).
   __device__ __forceinline__ void init(const uint8_t* p, int64_t ld_, int first, int limit, int k_rows,
                                        int wave_, int lane) {
     ld = ld_;
@@ -160,38 +167,49 @@ struct SlabLoader {
       // row = RPL (wave + 2 i) + lrow; its bit 4 comes from i alone
       const int swz = km_swz<C>((RPL * wave + lrow) & 15);
       auto column = [&](int top) {
-        const int c = 16 * ((chunk >> 1) ^ (swz | top << (C == 256 ? 2 : 1))) + 8 * (chunk & 1);
-        return (uint32_t)(2 * (CLAMP ? min(c, limit - first - 8) : c));   // past the last column: any of them
+        const int c = 16 * ((chunk >> 1) ^ (swz | top << (C >= 128 ? 2 : 1))) + 8 * (chunk & 1);
+        return (uint32_t)(2 * min(c, limit - first - 8));
       };
       col0 = column(0);
       col1 = column(1);
-      off[0] = (uint32_t)((RPL * wave + lrow) * (int)ld);
+      off = (uint32_t)((RPL * wave + lrow) * (int)ld);
     } else {
       base = p + (int64_t)first * ld;
       rsrc = rsrc_of(base, (int64_t)C * ld);
       lrow = lane >> 3;
       const int chunk = (lane & 7) ^ ((4 * (wave & 1) + (lrow >> 1)) & 5);
-#pragma unroll
-      for (int i = 0; i < (CLAMP ? N : 1); ++i) {
-        const int r = 8 * (wave + 2 * i) + lrow;
-        off[i] = (uint32_t)((CLAMP ? min(r, limit - 1 - first) : r) * (int)ld + chunk * 16);
-      }
+      const int last = min(limit - first, C) - 1;
+      edge = last + 1 == C ? -1 : last >> 3;
+      off = (uint32_t)(lrow * (int)ld + chunk * 16);
+      off_edge = (uint32_t)(min(lrow, last & 7) * (int)ld + chunk * 16);
     }
   }
   __device__ __forceinline__ void issue(int kb, uint8_t* lds) const {
 #if defined(__HIP_DEVICE_COMPILE__)
-    // The scalar offset and the LDS address step from load to load; opaque, or
-    // the compiler keeps all N values of each in scalar registers and spills.
+    // Load numbers and LDS addresses step from load to load; opaque, or the
+    // compiler keeps all N values of each in scalar registers and spills them.
     int to = __builtin_amdgcn_readfirstlane(wave * 1024);
     if constexpr (!KM) {
-      const int step = CLAMP ? 0 : __builtin_amdgcn_readfirstlane(16 * (int)ld);
-      int so = kb * 128;
+      const int step = __builtin_amdgcn_readfirstlane(8 * (int)ld);
+      if (edge < 0) {   // every row exists
+        int so = kb * 128 + __builtin_amdgcn_readfirstlane(wave) * step;
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + to), 16, off[CLAMP ? i : 0], so, 0, 0);
-        so += step;
-        to += 2048;
-        asm volatile("" : "+s"(so), "+s"(to));
+        for (int i = 0; i < N; ++i) {
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + to), 16, off, so, 0, 0);
+          so += 2 * step;
+          to += 2048;
+          asm volatile("" : "+s"(so), "+s"(to));
+        }
+      } else {
+        int o = __builtin_amdgcn_readfirstlane(wave);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + to), 16, o < edge ? off : off_edge,
+                                                   kb * 128 + min(o, edge) * step, 0, 0);
+          o += 2;
+          to += 2048;
+          asm volatile("" : "+s"(o), "+s"(to));
+        }
       }
     } else {
       // A descriptor of its own per slab: offsets stay within 64 rows.
@@ -203,7 +221,7 @@ struct SlabLoader {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + to), 16,
-                                                   off[0] + ((2 * RPL * i >> 4) & 1 ? col1 : col0), so, 0, 0);
+                                                   off + ((2 * RPL * i >> 4) & 1 ? col1 : col0), so, 0, 0);
           so += step;
           to += 2048;
           asm volatile("" : "+s"(so), "+s"(to));
@@ -256,39 +274,41 @@ struct FragReader {
   }
 };
 
-// One output tile: its own rows [m0, ..) and columns [n0, ..), the window that
-// its loads cover, and its slabs.
+// One output tile and its slabs.
 struct Tile {
-  int m0, n0, ml, nl, tn, split, kb0, kb1;
+  int m0, n0, tn, split, kb0, kb1;
 };
 
-// C[m, n] = sum_k A[m, k] B[n, k] on BM x BN tiles of WGM x WGN waves.  Two
-// stages of 64 contraction elements in LDS, filled by direct buffer -> LDS
+// C[m, n] = sum_k A[m, k] B[n, k] on BM x BN tiles of WGM x WGN waves.  A ring
+// of stages of 64 contraction elements in LDS, filled by direct buffer -> LDS
 // loads from waves 0 and 1 (a direct load keeps the issuing wave for about 16
 // cycles; the others go straight to their MFMAs).  Each stage is an LDS
 // variable of its own and the stage loop is unrolled, so that the compiler
-// sees that reads of one stage do not depend on loads into the other.
+// sees that reads of one stage do not depend on loads into another.
+//
+// 256 x 256 tiles (8 waves, two stages, all of a CU's LDS) read the fewest
+// operand bytes per product.  64-row tiles (4 waves, two workgroups a CU) serve
+// few tokens or columns: 64 x 256 with two stages where W streams by, 64 x 128
+// with three where a tile takes what the wait for its slabs takes.
 //
 // A workgroup of the 256 x 256 kernel runs `rounds` tiles, a chip's worth of
 // workgroups apart, and starts the next tile's first slab before it works off
 // this one's epilogue, which uses LDS beside the stages; its results are stored
 // by the waves that load nothing, so that no load waits for them.
-//
-// Edges: the 64-row kernel (SMALL) clamps every lane's row to the last one
-// (any M, N); the large one has M >= BM and N >= BN, and an edge tile's window
-// moves back to end at the last row, so no load needs a register of its own
-// for its row.  A KM operand A needs neither: its rows are at least tiles_m BM
-// columns long.  Either way a tile's epilogue handles only its own rows and
-// columns.
+// Any M and N: a tile past an edge loads rows again and stores only its own.
 template <int BM, int BN, int WGM, int WGN, int EPI, bool AKM, bool BKM>
 __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGemm p) {
   constexpr bool SMALL = BM == 64;
+  constexpr int STAGES = BN == 128 ? 3 : 2;
+  constexpr int LATER = STAGES == 3 ? (BM + BN) / 16 : 0;         // a loading wave's loads of one later slab
   constexpr int NW = WGM * WGN;
   constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16;
   constexpr bool ROWS = EPI == kStats || EPI == kGrad;       // the epilogue needs its rows' targets
   constexpr bool STAGED = !SMALL && (EPI == kGrad || EPI == kOut);
-  __shared__ __attribute__((aligned(1024))) uint8_t sA0[BM * 128], sA1[BM * 128];
-  __shared__ __attribute__((aligned(1024))) uint8_t sB0[BN * 128], sB1[BN * 128];
+  __shared__ __attribute__((aligned(1024))) uint8_t sA0[BM * 128], sA1[BM * 128], sA2[STAGES == 3 ? BM * 128 : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t sB0[BN * 128], sB1[BN * 128], sB2[STAGES == 3 ? BN * 128 : 16];
+  uint8_t* const sA[3] = {sA0, sA1, sA2};
+  uint8_t* const sB[3] = {sB0, sB1, sB2};
   // The epilogue's own: 64 rows of bf16 results, or each wave's row statistics.
   // (The small kernel, two workgroups a CU, uses a stage for the latter.)
   __shared__ __attribute__((aligned(16))) uint8_t sE[STAGED ? 64 * 512 : !SMALL && EPI == kStats ? WGN * BM * 8 : 16];
@@ -306,14 +326,12 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
     tile_order(id - t.split * tiles, p.tiles_m, p.tiles_n, &tm, &t.tn);
     t.m0 = tm * BM;
     t.n0 = t.tn * BN;
-    t.ml = SMALL || AKM ? t.m0 : min(t.m0, p.M - BM);
-    t.nl = SMALL ? t.n0 : min(t.n0, p.N - BN);
     t.kb0 = t.split * p.kb_per_split;
     t.kb1 = min(p.kblocks, t.kb0 + p.kb_per_split);
     return t;
   };
-  SlabLoader<BM, AKM, SMALL && !AKM> la;
-  SlabLoader<BN, BKM, SMALL> lb;
+  SlabLoader<BM, AKM> la;
+  SlabLoader<BN, BKM> lb;
   auto issue = [&](int kb, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
     if (wave < 2) {
       la.issue(kb, sa);
@@ -321,9 +339,12 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
     }
   };
   auto begin = [&](const Tile& t) __attribute__((always_inline)) {
-    la.init(p.a, p.lda, t.ml, p.M, p.a_rows, wave, lane);
-    lb.init(p.b, p.ldb, t.nl, p.N, p.b_rows, wave, lane);
-    if (t.kb0 < t.kb1) issue(t.kb0, sA0, sB0);
+    la.init(p.a, p.lda, t.m0, AKM ? p.tiles_m * BM : p.M, p.a_rows, wave, lane);
+    lb.init(p.b, p.ldb, t.n0, p.N, p.b_rows, wave, lane);
+    if (t.kb0 < t.kb1) {
+      issue(t.kb0, sA0, sB0);
+      if constexpr (STAGES == 3) issue(min(t.kb0 + 1, t.kb1 - 1), sA1, sB1);
+    }
   };
   float scale = 1.f;
   if constexpr (EPI == kOut) scale = *p.scale;
@@ -343,8 +364,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
     if constexpr (ROWS) {
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        const int r = min(t.ml + wm0 + 16 * i + frow, p.M - 1);
-        const int64_t y = (EPI == kGrad ? (int64_t)p.local_target[r] - p.v0 : p.target[r]) - (t.nl + wn0);
+        const int r = min(t.m0 + wm0 + 16 * i + frow, p.M - 1);
+        const int64_t y = (EPI == kGrad ? (int64_t)p.local_target[r] - p.v0 : p.target[r]) - (t.n0 + wn0);
         tgt[i] = y >= 0 && y < WN ? (int)y : -1;
         if constexpr (EPI == kGrad) info[i] = p.row[r];
       }
@@ -355,16 +376,16 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    ring_sync();
-    for (int it = t.kb0; it < t.kb1; it += 2) {
+    ring_sync<LATER>();
+    for (int it = t.kb0; it < t.kb1; it += STAGES) {
 #pragma unroll
-      for (int st = 0; st < 2; ++st) {
+      for (int st = 0; st < STAGES; ++st) {
         const int kb = it + st;
         if (kb >= t.kb1) break;
         // past the end the last slab is loaded again, into a stage nobody reads
-        issue(min(kb + 1, t.kb1 - 1), st ? sA0 : sA1, st ? sB0 : sB1);
-        const uint8_t* const ta = st ? sA1 : sA0;
-        const uint8_t* const tb = st ? sB1 : sB0;
+        issue(min(kb + STAGES - 1, t.kb1 - 1), sA[(st + STAGES - 1) % STAGES], sB[(st + STAGES - 1) % STAGES]);
+        const uint8_t* const ta = sA[st];
+        const uint8_t* const tb = sB[st];
         FragReader<BM, AKM> ra;
         FragReader<BN, BKM> rb;
         ra.init(wm0, lane);
@@ -393,9 +414,10 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
           for (int j = 0; j < TN; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bh[j], ah[i & 1], acc[i][j], 0, 0, 0);
         }
-        ring_sync();
+        ring_sync<LATER>();
       }
     }
+    ring_sync<0>();
     __syncthreads();   // every wave's reads and loads are done: the stages are free
     const Tile d = t;
     number += kCus;
@@ -405,10 +427,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
       begin(t);
     }
 
-    const int row0 = d.ml + wm0 + frow;            // + 16 i
-    const int col0 = d.nl + wn0 + 4 * fq;          // + 16 j + v
-    // Whether every column of this wave's is the tile's own.
-    const bool whole = d.nl + wn0 >= d.n0 && d.nl + wn0 + WN <= p.N;
+    const int row0 = d.m0 + wm0 + frow;            // + 16 i
+    const int col0 = d.n0 + wn0 + 4 * fq;          // + 16 j + v
+    const bool whole = d.n0 + wn0 + WN <= p.N;     // every column of this wave's exists
     if constexpr (EPI == kStats) {
       // Maximum and sum of exponentials of each row over this wave's columns
       // (a row's columns lie in lanes frow + 16 q), then over the waves.
@@ -423,7 +444,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
             for (int j = 0; j < TN; ++j)
 #pragma unroll
               for (int v = 0; v < 4; ++v)
-                if (16 * j + 4 * fq + v == tgt[i] && r >= d.m0 && r < p.M && col0 + 16 * j + v >= d.n0)
+                if (16 * j + 4 * fq + v == tgt[i] && r < p.M)
                   p.target_logit[r] = acc[i][j][v];
           }
           float m = -INFINITY;
@@ -432,8 +453,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
               if constexpr (kCheck) {
-                const int n = col0 + 16 * j + v;
-                if (n < d.n0 || n >= p.N) acc[i][j][v] = -INFINITY;
+                if (col0 + 16 * j + v >= p.N) acc[i][j][v] = -INFINITY;
               }
               m = fmaxf(m, acc[i][j][v]);   // drops a NaN; the sum below does not
             }
@@ -464,21 +484,19 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
           if (e.x != -INFINITY) s += e.y * __builtin_amdgcn_exp2f((e.x - m) * kLog2e);
           else s += e.y;     // 0, or NaN
         }
-        const int row = d.ml + r;
-        if (row >= d.m0 && row < p.M) p.part[(int64_t)d.tn * p.M + row] = make_float2(m, s);
+        const int row = d.m0 + r;
+        if (row < p.M) p.part[(int64_t)d.tn * p.M + row] = make_float2(m, s);
       }
     } else if constexpr (EPI == kAcc) {
       float* const base = p.acc + (int64_t)d.split * p.M * p.N;
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         const int r = row0 + 16 * i;
-        if (r < d.m0 || r >= p.M) continue;
+        if (r >= p.M) continue;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-          // N is a multiple of 64 and a window starts on a multiple of 64, so
-          // four columns are all this tile's or none is
           const int n = col0 + 16 * j;
-          if (n < d.n0 || n >= p.N) continue;
+          if (n >= p.N) continue;   // N is a multiple of 64: all four columns exist or none
           float4* const at = (float4*)(base + (int64_t)r * p.N + n);
           float4 o = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
           if (p.add) {
@@ -514,7 +532,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
           w[j] = make_uint2(pack_bf16x2_rne(acc[i][j][0] * f, acc[i][j][1] * f) & keep,
                             pack_bf16x2_rne(acc[i][j][2] * f, acc[i][j][3] * f) & keep);
       };
-      if (STAGED && (d.nl & 7) == 0) {
+      if constexpr (STAGED) {
         // Through LDS, so that every store writes whole lines (in the MFMA
         // layout a row of a wave's columns would leave in pieces of 32 bytes):
         // 64 rows of 512 bytes at a time, 16-byte chunk c of row r at
@@ -533,20 +551,20 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
             }
           }
           __syncthreads();
-          const int c = lane & 31, n = d.nl + 8 * c;
+          const int c = lane & 31, n = d.n0 + 8 * c;
           if (wave >= 2) {
             for (int pr = wave - 2; pr < 32; pr += NW - 2) {
-              const int rr = 2 * pr + (lane >> 5), r = d.ml + 64 * q + rr;
+              const int rr = 2 * pr + (lane >> 5), r = d.m0 + 64 * q + rr;
               const u32x4_t v = *(const u32x4_t*)(sE + rr * 512 + 16 * (c ^ (rr & 15)));
-              if (r < d.m0 || r >= p.M || n + 7 < d.n0 || n >= p.N) continue;
+              if (r >= p.M || n >= p.N) continue;
               uint16_t* const at = out + (int64_t)r * p.ldo + n;
-              if (n >= d.n0 && n + 7 < p.N) {
+              if (n + 7 < p.N) {
                 if constexpr (EPI == kOut) __builtin_nontemporal_store(v, (u32x4_t*)at);
                 else *(u32x4_t*)at = v;   // the next products read G
               } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                  if (n + e >= d.n0 && n + e < p.N) at[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+                  if (n + e < p.N) at[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
               }
             }
           }
@@ -558,17 +576,17 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
           const int r = row0 + 16 * i;
           uint2 w[TN];
           results(i, w);
-          if (r < d.m0 || r >= p.M) continue;
+          if (r >= p.M) continue;
 #pragma unroll
           for (int j = 0; j < TN; ++j) {
             const int n = col0 + 16 * j;
             uint16_t* const at = out + (int64_t)r * p.ldo + n;
-            if (n >= d.n0 && n + 3 < p.N && (n & 3) == 0) {
+            if (n + 3 < p.N) {
               *(uint2*)at = w[j];
             } else {
 #pragma unroll
               for (int v = 0; v < 4; ++v)
-                if (n + v >= d.n0 && n + v < p.N) at[v] = (uint16_t)((v < 2 ? w[j].x : w[j].y) >> (16 * (v & 1)));
+                if (n + v < p.N) at[v] = (uint16_t)((v < 2 ? w[j].x : w[j].y) >> (16 * (v & 1)));
             }
           }
         }
@@ -667,11 +685,18 @@ __global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ 
 }
 
 
-// Large tiles once they (times the splits of the contraction) fill half the
-// chip's compute units; below that 64-row tiles give four times the workgroups
-// (and take any M and N).
+// Large tiles for more than 128 rows, once they (times the splits of the
+// contraction) fill half the chip's compute units; else 64-row tiles.
+// (131072 x 5120, forward: 100 tokens 337 us on 64-row tiles, 356 us on large
+// ones; 131072 x 4096: 255 tokens 402 us and 311 us.)
 bool large_tiles(int64_t M, int64_t N, int64_t splits) {
-  return M >= 256 && N >= 256 && ((M + 255) / 256) * ((N + 255) / 256) * splits >= kCus / 2;
+  return M > 128 && ((M + 255) / 256) * ((N + 255) / 256) * splits >= kCus / 2;
+}
+// Columns of the logits' 64-row tiles: 256 once these fill the chip twice.
+// (33 tokens, 131072 x 5120: 238 us, with 128 columns 246 us; a step of 128
+// tokens, 2048 x 512: 44 us with 128, 52 us with 256.)
+int64_t logit_columns(int64_t T, int64_t V) {
+  return large_tiles(T, V, 1) || ((T + 63) / 64) * ((V + 255) / 256) >= 2 * kCus ? 256 : 128;
 }
 
 // Tiles a workgroup: more hide more epilogues, but workgroups drift apart
@@ -681,9 +706,10 @@ constexpr int kRounds = 4;
 template <int EPI, bool AKM = false, bool BKM = false>
 hipError_t run_gemm(XentGemm p, int splits, hipStream_t stream) {
   const bool large = large_tiles(p.M, p.N, splits);
-  const int bm = large ? 256 : 64;
+  constexpr bool LOGITS = EPI == kStats || EPI == kGrad;
+  const int bm = large ? 256 : 64, bn = large ? 256 : LOGITS ? (int)logit_columns(p.M, p.N) : 128;
   p.tiles_m = (p.M + bm - 1) / bm;
-  p.tiles_n = (p.N + 255) / 256;
+  p.tiles_n = (p.N + bn - 1) / bn;
   p.splits = splits;
   p.kb_per_split = (p.kblocks + splits - 1) / splits;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * splits;
@@ -692,8 +718,11 @@ hipError_t run_gemm(XentGemm p, int splits, hipStream_t stream) {
     const int64_t groups = (tiles + kCus * p.rounds - 1) / (kCus * p.rounds) * kCus;
     hipLaunchKernelGGL((xent_gemm_kernel<256, 256, 2, 4, EPI, AKM, BKM>), dim3((unsigned)groups), dim3(512), 0, stream,
                        p);
+  } else if (LOGITS && bn == 256) {
+    if constexpr (LOGITS)
+      hipLaunchKernelGGL((xent_gemm_kernel<64, 256, 1, 4, EPI, AKM, BKM>), dim3((unsigned)tiles), dim3(256), 0, stream, p);
   } else {
-    hipLaunchKernelGGL((xent_gemm_kernel<64, 256, 1, 4, EPI, AKM, BKM>), dim3((unsigned)tiles), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((xent_gemm_kernel<64, 128, 1, 4, EPI, AKM, BKM>), dim3((unsigned)tiles), dim3(256), 0, stream, p);
   }
   return hipGetLastError();
 }
@@ -706,6 +735,7 @@ size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr int64_t kPieceBytes = (int64_t)256 << 20;
 
 struct XentLayout {
+  int64_t part_tiles;          // vocabulary tiles of the statistics
   int64_t tp, piece, ld_g;     // tokens in whole slabs; columns of a piece; G's row
   int splits;                  // of dH's contraction over the piece
   size_t part, logit, row, target, scale, g, acc, total;
@@ -716,7 +746,8 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t at = off; off += pad256(bytes); return at; };
   if (!backward) {
-    L.part = take((size_t)((V + 255) / 256) * T * sizeof(float2));
+    L.part_tiles = (V + logit_columns(T, V) - 1) / logit_columns(T, V);
+    L.part = take((size_t)L.part_tiles * T * sizeof(float2));
     L.logit = take((size_t)T * 4);
     L.total = off;
     return L;
@@ -734,15 +765,15 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
   // dH's contraction is split until its tiles fill one round of the chip, at
   // least 8 slabs a split; large tiles if that many splits let them.  (1777 x
   // 2048 outputs over 50001 columns: 56 large tiles x 4 splits.)
-  auto splits_of = [&](int64_t bm) {
-    const int64_t tiles = ((T + bm - 1) / bm) * ((K + 255) / 256);
+  auto splits_of = [&](int64_t bm, int64_t bn) {
+    const int64_t tiles = ((T + bm - 1) / bm) * ((K + bn - 1) / bn);
     int64_t s = kCus / tiles;
     if (s > piece / 512) s = piece / 512;
     return s < 1 ? (int64_t)1 : s;
   };
-  const int64_t s_large = splits_of(256);
-  L.splits = (int)(large_tiles(T, K, s_large) ? s_large : splits_of(64));
-  // (splits_of(64) <= s_large, so run_gemm takes the same decision.)
+  const int64_t s_large = splits_of(256, 256);
+  L.splits = (int)(large_tiles(T, K, s_large) ? s_large : splits_of(64, 128));
+  // (splits_of(64, 128) <= s_large, so run_gemm takes the same decision.)
   L.row = take((size_t)T * sizeof(float2));
   L.target = take((size_t)T * 4);
   L.scale = take(4);
@@ -777,7 +808,7 @@ hipError_t launch_xent_fwd(const XentArgs& p, void* ws, hipStream_t stream) {
   hipError_t e = run_gemm<kStats>(g, 1, stream);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(xent_join_kernel, dim3((unsigned)((p.T + 15) / 16)), dim3(1024), 0, stream, g.part,
-                     (int)((p.V + 255) / 256), (int)p.T, p.V, g.target_logit, p.target, p.ignore_index,
+                     (int)L.part_tiles, (int)p.T, p.V, g.target_logit, p.target, p.ignore_index,
                      p.loss, p.lse);
   return hipGetLastError();
 }
