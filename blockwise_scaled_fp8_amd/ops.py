@@ -4,6 +4,7 @@ outputs with torch (device memory is plumbing), passes raw pointers, sizes and
 the current HIP stream, and raises FP8BWError on a non-OK status.  Every step
 of the computation runs in the HIP kernels of libfp8bw.so."""
 
+import array
 import functools
 from typing import NamedTuple, Optional
 
@@ -564,9 +565,12 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-6, y=True, q=False, qt=False, 
     rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     ty = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if y else None
     tq = torch.empty((rows, cols), dtype=torch.uint8, device=dev) if q else None
-    tr = colmajor_empty(rows, _cdiv(cols, 128), dev) if q else None
+    # column-major scales in one allocation call (no view to build)
+    tr = torch.empty_strided((rows, _cdiv(cols, 128)), (1, max(rows, 1)), dtype=torch.float32,
+                             device=dev) if q else None
     tqt = torch.empty((cols, rows), dtype=torch.uint8, device=dev) if qt else None
-    trt = colmajor_empty(cols, _cdiv(rows, 128), dev) if qt else None
+    trt = torch.empty_strided((cols, _cdiv(rows, 128)), (1, max(cols, 1)), dtype=torch.float32,
+                              device=dev) if qt else None
     check(lib.fp8bw_rms_norm_fwd(
         x.data_ptr(), x.stride(0), _ptr(residual), _ld(residual), weight.data_ptr(),
         OUT_DTYPES[weight.dtype], float(eps), rows, cols, _ptr(s), _ld(s), rstd.data_ptr(),
@@ -686,42 +690,63 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, beta1=0.9, bet
                      (masters, "masters")):
         if ts is not None:
             _adamw_list(ts, n, name)
+    # Checks and addresses list by list, one attribute at a time, and the C
+    # array's words in one go: about 1 us a tensor, a small model's whole cost.
     device = params[0].device
-    arr = (AdamwTensor * n)()
-    none = [None] * n
+    index = device.index if device.type == "cuda" else -1
+    numels = [t.numel() for t in params]
     state_dtypes = CODE_DTYPES if eight else (torch.float32,)
-    for d, p, g, m, v, ms, rs, w in zip(arr, params, grads, exp_avgs, exp_avg_sqs,
-                                        exp_avg_scales or none, root_scales or none,
-                                        masters or none):
-        numel = p.numel()
-        for t in (p, g, m, v):
-            if t.device != device or not t.is_cuda:
-                raise ValueError("fp8bw ops take CUDA (HIP) tensors on one device")
-            if not t.is_contiguous() or t.numel() != numel:
-                raise ValueError("params, grads and states must be contiguous and of equal size")
-        if m.dtype not in state_dtypes or v.dtype not in state_dtypes:
-            raise ValueError("states must all be float32, or all be E4M3 codes")
-        if p.dtype not in OUT_DTYPES or g.dtype not in OUT_DTYPES:
-            raise ValueError("params and grads must be bfloat16 or float32")
-        if eight:
-            for t in (ms, rs):
-                if t.device != device:
-                    raise ValueError("fp8bw ops take CUDA (HIP) tensors on one device")
-                _vector(t, _cdiv(numel, 128), torch.float32, "scales")
-            d.exp_avg_scale, d.root_scale = ms.data_ptr(), rs.data_ptr()
-        if w is not None:
-            if w.device != device or w.dtype != torch.float32 or not w.is_contiguous() or w.numel() != numel:
+    here, yes = {index}, {True}
+    kinds = []
+    for ts, dtypes, name in ((params, OUT_DTYPES, "params"), (grads, OUT_DTYPES, "grads"),
+                             (exp_avgs, state_dtypes, "exp_avgs"),
+                             (exp_avg_sqs, state_dtypes, "exp_avg_sqs")):
+        if index < 0 or {t.get_device() for t in ts} != here:
+            raise ValueError("fp8bw ops take CUDA (HIP) tensors on one device")
+        if [t.numel() for t in ts] != numels or {t.is_contiguous() for t in ts} != yes:
+            raise ValueError("params, grads and states must be contiguous and of equal size")
+        kinds.append({t.dtype for t in ts})
+        if not kinds[-1] <= set(dtypes):
+            raise ValueError(f"{name} must be of {' or '.join(str(d) for d in dtypes)}")
+    zeros = [0] * n
+    scales = []
+    for ts in (exp_avg_scales, root_scales):
+        if ts is None:
+            scales.append(zeros)
+            continue
+        if any([t.get_device() != index for t in ts]):
+            raise ValueError("fp8bw ops take CUDA (HIP) tensors on one device")
+        for t, m in zip(ts, numels):
+            _vector(t, _cdiv(m, 128), torch.float32, "scales")
+        scales.append([t.data_ptr() for t in ts])
+    if masters is None:
+        master_ptrs = zeros
+    else:
+        for t, m in zip(masters, numels):
+            if t is not None and (t.get_device() != index or t.dtype != torch.float32
+                                  or not t.is_contiguous() or t.numel() != m):
                 raise ValueError("masters must be contiguous float32 tensors like params")
-            d.master = w.data_ptr()
-        d.param, d.grad, d.exp_avg, d.exp_avg_sq = p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr()
-        d.numel = numel
-        d.param_dtype, d.grad_dtype = OUT_DTYPES[p.dtype], OUT_DTYPES[g.dtype]
+        master_ptrs = [0 if t is None else t.data_ptr() for t in masters]
+    # AdamwTensor's fields in order, its two int types in one word
+    if len(kinds[0]) == len(kinds[1]) == 1:
+        types = [OUT_DTYPES[params[0].dtype] | OUT_DTYPES[grads[0].dtype] << 32] * n
+    else:
+        types = [OUT_DTYPES[p.dtype] | OUT_DTYPES[g.dtype] << 32 for p, g in zip(params, grads)]
+    fields = ([t.data_ptr() for t in params], [t.data_ptr() for t in grads],
+              [t.data_ptr() for t in exp_avgs], [t.data_ptr() for t in exp_avg_sqs],
+              *scales, master_ptrs, numels, types)
+    words = [0] * (9 * n)
+    for k, column in enumerate(fields):
+        words[k::9] = column
+    arr = (AdamwTensor * n).from_buffer(array.array("q", words))
     if grad_scale is not None and (grad_scale.device != device or grad_scale.dtype != torch.float32
                                    or grad_scale.numel() != 1):
         raise ValueError("grad_scale must be a one-element float32 tensor on the params' device")
-    with torch.cuda.device(device):
-        check(lib.fp8bw_adamw_step(arr, n, int(eight), int(step), float(lr), float(beta1),
-                                   float(beta2), float(eps), float(weight_decay), _ptr(grad_scale),
-                                   int(seed is not None),
-                                   0 if seed is None else int(seed) & 0xFFFFFFFFFFFFFFFF,
-                                   _stream(params[0])))
+    args = (arr, n, int(eight), int(step), float(lr), float(beta1), float(beta2), float(eps),
+            float(weight_decay), _ptr(grad_scale), int(seed is not None),
+            0 if seed is None else int(seed) & 0xFFFFFFFFFFFFFFFF, _stream(params[0]))
+    if index == torch._C._cuda_getDevice():
+        check(lib.fp8bw_adamw_step(*args))
+    else:
+        with torch.cuda.device(device):
+            check(lib.fp8bw_adamw_step(*args))
