@@ -1,6 +1,7 @@
 /*
  * fp8bw.h -- C ABI of libfp8bw.so: blockwise- and tensorwise-scaled FP8
- * (OCP E4M3) quantization and GEMM for AMD MI355X (gfx950).
+ * (OCP E4M3) quantization and GEMM for AMD MI355X (gfx950), and the operators
+ * around an FP8 linear in a training step.
  *
  * Sources, cited by page title and section:
  *   [REPRO]   pytorch/ao PR "add repro for blockwise _scaled_mm
