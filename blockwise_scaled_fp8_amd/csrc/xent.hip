@@ -254,14 +254,15 @@ struct FragReader {
       swz = km_swz<C>(row);
       unit = first >> 4;
       lo = row * 2 * C + 8 * (frow & 3);
-      hi = lo + 8 * 2 * C;
+      hi = 0;
     } else {
       lo = (first + frow) * 128 + (((2 * fq) ^ chunk_swz(first + frow)) << 4);
       hi = (first + frow) * 128 + (((2 * fq + 1) ^ chunk_swz(first + frow)) << 4);
     }
     // Opaque, so that the compiler keeps these and adds constants, instead of
     // one address per fragment and stage.
-    asm volatile("" : "+v"(lo), "+v"(hi));
+    asm volatile("" : "+v"(lo));
+    if constexpr (!KM) asm volatile("" : "+v"(hi));
   }
   // k = 16 fq + 0 .. 7 (low) and 16 fq + 8 .. 15 (high) of sub-tile i
   __device__ __forceinline__ bf16x8 low(const uint8_t* tile, int i) const {
@@ -269,7 +270,7 @@ struct FragReader {
     else return frag(tile, lo + 2048 * i);
   }
   __device__ __forceinline__ bf16x8 high(const uint8_t* tile, int i) const {
-    if constexpr (KM) return frag_km<C>(tile, hi + (((unit + i) ^ swz) << 5));
+    if constexpr (KM) return frag_km<C>(tile, lo + (((unit + i) ^ swz) << 5) + 8 * 2 * C);
     else return frag(tile, hi + 2048 * i);
   }
 };
@@ -293,7 +294,7 @@ struct Tile {
 //
 // A workgroup of the 256 x 256 kernel runs `rounds` tiles, a chip's worth of
 // workgroups apart, and starts the next tile's first slab before it works off
-// this one's epilogue, which uses LDS beside the stages; its results are stored
+// this one's epilogue, which uses LDS beside that stage; its results are stored
 // by the waves that load nothing, so that no load waits for them.
 // Any M and N: a tile past an edge loads rows again and stores only its own.
 template <int BM, int BN, int WGM, int WGN, int EPI, bool AKM, bool BKM>
@@ -309,9 +310,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
   __shared__ __attribute__((aligned(1024))) uint8_t sB0[BN * 128], sB1[BN * 128], sB2[STAGES == 3 ? BN * 128 : 16];
   uint8_t* const sA[3] = {sA0, sA1, sA2};
   uint8_t* const sB[3] = {sB0, sB1, sB2};
-  // The epilogue's own: 64 rows of bf16 results, or each wave's row statistics.
-  // (The small kernel, two workgroups a CU, uses a stage for the latter.)
-  __shared__ __attribute__((aligned(16))) uint8_t sE[STAGED ? 64 * 512 : !SMALL && EPI == kStats ? WGN * BM * 8 : 16];
+  // Each wave's row statistics.  (The small kernel uses a stage for them.)
+  __shared__ __attribute__((aligned(16))) uint8_t sE[!SMALL && EPI == kStats ? WGN * BM * 8 : 16];
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm0 = (wave / WGN) * WM, wn0 = (wave % WGN) * WN;
@@ -535,27 +535,26 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
       if constexpr (STAGED) {
         // Through LDS, so that every store writes whole lines (in the MFMA
         // layout a row of a wave's columns would leave in pieces of 32 bytes):
-        // 64 rows of 512 bytes at a time, 16-byte chunk c of row r at
-        // c ^ (r & 15).
+        // half of each wave's rows at a time, 128 rows of 512 bytes in the
+        // second stage, which the next tile's first slab leaves alone; 16-byte
+        // chunk c of row r at c ^ (r & 15).
 #pragma unroll
-        for (int q = 0; q < BM / 64; ++q) {
-          if (wm0 / 128 == q / 2) {
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int ii = 0; ii < 4; ++ii) {
-              uint2 w[TN];
-              results((4 * q + ii) % TM, w);
-              uint8_t* const rowp = sE + (16 * ii + frow) * 512;
+          for (int ii = 0; ii < TM / 2; ++ii) {
+            uint2 w[TN];
+            results(TM / 2 * h + ii, w);
+            uint8_t* const rowp = (wm0 ? sB1 : sA1) + (16 * ii + frow) * 512;
 #pragma unroll
-              for (int j = 0; j < TN; ++j)
-                *(uint2*)(rowp + 16 * (((wn0 >> 3) + 2 * j + (fq >> 1)) ^ frow) + 8 * (fq & 1)) = w[j];
-            }
+            for (int j = 0; j < TN; ++j)
+              *(uint2*)(rowp + 16 * (((wn0 >> 3) + 2 * j + (fq >> 1)) ^ frow) + 8 * (fq & 1)) = w[j];
           }
           __syncthreads();
           const int c = lane & 31, n = d.n0 + 8 * c;
           if (wave >= 2) {
-            for (int pr = wave - 2; pr < 32; pr += NW - 2) {
-              const int rr = 2 * pr + (lane >> 5), r = d.m0 + 64 * q + rr;
-              const u32x4_t v = *(const u32x4_t*)(sE + rr * 512 + 16 * (c ^ (rr & 15)));
+            for (int pr = wave - 2; pr < 64; pr += NW - 2) {
+              const int rr = 2 * (pr & 31) + (lane >> 5), r = d.m0 + 128 * (pr >> 5) + 64 * h + rr;
+              const u32x4_t v = *(const u32x4_t*)((pr >> 5 ? sB1 : sA1) + rr * 512 + 16 * (c ^ (rr & 15)));
               if (r >= p.M || n >= p.N) continue;
               uint16_t* const at = out + (int64_t)r * p.ldo + n;
               if (n + 7 < p.N) {
