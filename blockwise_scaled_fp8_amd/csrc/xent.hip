@@ -288,11 +288,12 @@ struct Tile {
 // sees that reads of one stage do not depend on loads into another.
 //
 // 256 x 256 tiles (8 waves, two stages, all of a CU's LDS) read the fewest
-// operand bytes per product.  64-row tiles (4 waves, two workgroups a CU) serve
-// few tokens or columns: 64 x 256 with two stages where W streams by, 64 x 128
-// with three where a tile takes what the wait for its slabs takes.
+// operand bytes per product; 128 x 256 tiles (8 waves, three stages) do for 65
+// to 128 tokens.  64-row tiles (4 waves, two workgroups a CU) serve few tokens
+// or columns: 64 x 256 with two stages where W streams by, 64 x 128 with three
+// where a tile takes what the wait for its slabs takes.
 //
-// A workgroup of the 256 x 256 kernel runs `rounds` tiles, a chip's worth of
+// A workgroup of the 8-wave kernels runs `rounds` tiles, a chip's worth of
 // workgroups apart, and starts the next tile's first slab before it works off
 // this one's epilogue, which uses LDS beside that stage; its results are stored
 // by the waves that load nothing, so that no load waits for them.
@@ -300,7 +301,7 @@ struct Tile {
 template <int BM, int BN, int WGM, int WGN, int EPI, bool AKM, bool BKM>
 __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGemm p) {
   constexpr bool SMALL = BM == 64;
-  constexpr int STAGES = BN == 128 ? 3 : 2;
+  constexpr int STAGES = BN == 128 || BM == 128 ? 3 : 2;
   constexpr int LATER = STAGES == 3 ? (BM + BN) / 16 : 0;         // a loading wave's loads of one later slab
   constexpr int NW = WGM * WGN;
   constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16;
@@ -535,16 +536,16 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
       if constexpr (STAGED) {
         // Through LDS, so that every store writes whole lines (in the MFMA
         // layout a row of a wave's columns would leave in pieces of 32 bytes):
-        // half of each wave's rows at a time, 128 rows of 512 bytes in the
-        // second stage, which the next tile's first slab leaves alone; 16-byte
-        // chunk c of row r at c ^ (r & 15).
+        // half of each wave's rows at a time, rows of 512 bytes in the last
+        // stage, which the next tile's first slabs leave alone; 16-byte chunk c
+        // of row r at c ^ (r & 15).
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int ii = 0; ii < TM / 2; ++ii) {
             uint2 w[TN];
             results(TM / 2 * h + ii, w);
-            uint8_t* const rowp = (wm0 ? sB1 : sA1) + (16 * ii + frow) * 512;
+            uint8_t* const rowp = (wm0 ? sB : sA)[STAGES - 1] + (16 * ii + frow) * 512;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
               *(uint2*)(rowp + 16 * (((wn0 >> 3) + 2 * j + (fq >> 1)) ^ frow) + 8 * (fq & 1)) = w[j];
@@ -552,9 +553,11 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
           __syncthreads();
           const int c = lane & 31, n = d.n0 + 8 * c;
           if (wave >= 2) {
-            for (int pr = wave - 2; pr < 64; pr += NW - 2) {
-              const int rr = 2 * (pr & 31) + (lane >> 5), r = d.m0 + 128 * (pr >> 5) + 64 * h + rr;
-              const u32x4_t v = *(const u32x4_t*)((pr >> 5 ? sB1 : sA1) + rr * 512 + 16 * (c ^ (rr & 15)));
+            constexpr int PAIRS = WM / 4;   // of rows, in half of a wave's
+            for (int pr = wave - 2; pr < 2 * PAIRS; pr += NW - 2) {
+              const int rr = 2 * (pr % PAIRS) + (lane >> 5), r = d.m0 + WM * (pr / PAIRS) + WM / 2 * h + rr;
+              const u32x4_t v =
+                  *(const u32x4_t*)((pr / PAIRS ? sB : sA)[STAGES - 1] + rr * 512 + 16 * (c ^ (rr & 15)));
               if (r >= p.M || n >= p.N) continue;
               uint16_t* const at = out + (int64_t)r * p.ldo + n;
               if (n + 7 < p.N) {
@@ -691,11 +694,19 @@ __global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ 
 bool large_tiles(int64_t M, int64_t N, int64_t splits) {
   return M > 128 && ((M + 255) / 256) * ((N + 255) / 256) * splits >= kCus / 2;
 }
-// Columns of the logits' 64-row tiles: 256 once these fill the chip twice.
-// (33 tokens, 131072 x 5120: 238 us, with 128 columns 246 us; a step of 128
-// tokens, 2048 x 512: 44 us with 128, 52 us with 256.)
-int64_t logit_columns(int64_t T, int64_t V) {
-  return large_tiles(T, V, 1) || ((T + 63) / 64) * ((V + 255) / 256) >= 2 * kCus ? 256 : 128;
+// Tiles of the logits: rows and columns.  Below the large ones, 128 rows for 65
+// to 128 tokens once the columns fill half the chip; else 64, with 256 columns
+// once these tiles fill the chip twice.  (100 tokens, 131072 x 5120: @A us on
+// 128 rows, 331 us on 64.  33 tokens: 231 us with 256 columns, 246 us with 128;
+// a step of 128 tokens, 2048 x 512: 43 us with 128, 52 us with 256.)
+struct TileShape {
+  int rows, cols;
+};
+TileShape logit_tiles(int64_t T, int64_t V) {
+  if (large_tiles(T, V, 1)) return {256, 256};
+  const int64_t wide = (V + 255) / 256;
+  if (T > 64 && T <= 128 && wide >= kCus / 2) return {128, 256};
+  return {64, (T + 63) / 64 * wide >= 2 * kCus ? 256 : 128};
 }
 
 // Tiles a workgroup: more hide more epilogues, but workgroups drift apart
@@ -704,24 +715,25 @@ constexpr int kRounds = 4;
 
 template <int EPI, bool AKM = false, bool BKM = false>
 hipError_t run_gemm(XentGemm p, int splits, hipStream_t stream) {
-  const bool large = large_tiles(p.M, p.N, splits);
   constexpr bool LOGITS = EPI == kStats || EPI == kGrad;
-  const int bm = large ? 256 : 64, bn = large ? 256 : LOGITS ? (int)logit_columns(p.M, p.N) : 128;
-  p.tiles_m = (p.M + bm - 1) / bm;
-  p.tiles_n = (p.N + bn - 1) / bn;
+  const TileShape tile = LOGITS ? logit_tiles(p.M, p.N)
+                                : large_tiles(p.M, p.N, splits) ? TileShape{256, 256} : TileShape{64, 128};
+  p.tiles_m = (p.M + tile.rows - 1) / tile.rows;
+  p.tiles_n = (p.N + tile.cols - 1) / tile.cols;
   p.splits = splits;
   p.kb_per_split = (p.kblocks + splits - 1) / splits;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * splits;
-  if (large) {
-    p.rounds = kRounds;
-    const int64_t groups = (tiles + kCus * p.rounds - 1) / (kCus * p.rounds) * kCus;
-    hipLaunchKernelGGL((xent_gemm_kernel<256, 256, 2, 4, EPI, AKM, BKM>), dim3((unsigned)groups), dim3(512), 0, stream,
-                       p);
-  } else if (LOGITS && bn == 256) {
-    if constexpr (LOGITS)
-      hipLaunchKernelGGL((xent_gemm_kernel<64, 256, 1, 4, EPI, AKM, BKM>), dim3((unsigned)tiles), dim3(256), 0, stream, p);
-  } else {
-    hipLaunchKernelGGL((xent_gemm_kernel<64, 128, 1, 4, EPI, AKM, BKM>), dim3((unsigned)tiles), dim3(256), 0, stream, p);
+  p.rounds = kRounds;
+  const dim3 few((unsigned)tiles), many((unsigned)((tiles + kCus * kRounds - 1) / (kCus * kRounds) * kCus));
+  if (tile.rows == 256)
+    hipLaunchKernelGGL((xent_gemm_kernel<256, 256, 2, 4, EPI, AKM, BKM>), many, dim3(512), 0, stream, p);
+  else if (tile.cols == 128)
+    hipLaunchKernelGGL((xent_gemm_kernel<64, 128, 1, 4, EPI, AKM, BKM>), few, dim3(256), 0, stream, p);
+  else if constexpr (LOGITS) {
+    if (tile.rows == 128)
+      hipLaunchKernelGGL((xent_gemm_kernel<128, 256, 2, 4, EPI, AKM, BKM>), many, dim3(512), 0, stream, p);
+    else
+      hipLaunchKernelGGL((xent_gemm_kernel<64, 256, 1, 4, EPI, AKM, BKM>), few, dim3(256), 0, stream, p);
   }
   return hipGetLastError();
 }
@@ -745,7 +757,8 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t at = off; off += pad256(bytes); return at; };
   if (!backward) {
-    L.part_tiles = (V + logit_columns(T, V) - 1) / logit_columns(T, V);
+    const int cols = logit_tiles(T, V).cols;
+    L.part_tiles = (V + cols - 1) / cols;
     L.part = take((size_t)L.part_tiles * T * sizeof(float2));
     L.logit = take((size_t)T * 4);
     L.total = off;
