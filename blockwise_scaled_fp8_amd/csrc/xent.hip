@@ -18,7 +18,9 @@
 // the logits, G in dH) or across it (W in dH; G and H in dW): the latter are
 // turned by transposing LDS reads, so nothing is ever transposed in memory.
 // The products are bound by the matrix cores from a few hundred tokens on, by
-// the reading of W below.
+// the reading of W below: 8192 tokens, 131072 x 4096, statistics 6.1 ms (1.45
+// PFLOP/s, matrix cores busy 72% of the cycles at the 1.87 GHz they are given),
+// G 6.7, dW 6.7 and dH 6.6 ms; 33 tokens, 131072 x 5120, forward 225 us (6 TB/s).
 //
 // Rounding: G is held as bf16, the accuracy of the matrix cores' operands.
 // It is formed with dloss divided by its largest magnitude, which the
@@ -50,8 +52,9 @@ enum XentEpilogue {
 };
 
 struct XentGemm {
-  // Operands by rows of ld bytes: [M or N][contraction], or, for the product
-  // kernels' *_KM operands, [contraction][M or N] with a_rows / b_rows rows.
+  // Operands by rows of ld bytes: [M or N][contraction], or, for the kernel's
+  // KM operands, [contraction][M or N].  a_rows, b_rows: the rows that exist;
+  // kGrad's results past them, up to M and N, are zeros.
   const uint8_t* a; int64_t lda;
   const uint8_t* b; int64_t ldb;
   int a_rows, b_rows;
@@ -178,7 +181,7 @@ struct SlabLoader {
       rsrc = rsrc_of(base, (int64_t)C * ld);
       lrow = lane >> 3;
       const int chunk = (lane & 7) ^ ((4 * (wave & 1) + (lrow >> 1)) & 5);
-      const int last = min(limit - first, C) - 1;
+      const int last = min(limit - first, C) - 1;   // the tile's first row exists
       edge = last + 1 == C ? -1 : last >> 3;
       off = (uint32_t)(lrow * (int)ld + chunk * 16);
       off_edge = (uint32_t)(min(lrow, last & 7) * (int)ld + chunk * 16);
@@ -340,8 +343,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
     }
   };
   auto begin = [&](const Tile& t) __attribute__((always_inline)) {
-    la.init(p.a, p.lda, t.m0, AKM ? p.tiles_m * BM : p.M, p.a_rows, wave, lane);
-    lb.init(p.b, p.ldb, t.n0, p.N, p.b_rows, wave, lane);
+    la.init(p.a, p.lda, t.m0, AKM ? p.tiles_m * BM : p.a_rows, p.a_rows, wave, lane);
+    lb.init(p.b, p.ldb, t.n0, BKM ? p.N : p.b_rows, p.b_rows, wave, lane);
     if (t.kb0 < t.kb1) {
       issue(t.kb0, sA0, sB0);
       if constexpr (STAGES == 3) issue(min(t.kb0 + 1, t.kb1 - 1), sA1, sB1);
@@ -365,10 +368,13 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
     if constexpr (ROWS) {
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        const int r = min(t.m0 + wm0 + 16 * i + frow, p.M - 1);
+        const int r = min(t.m0 + wm0 + 16 * i + frow, p.a_rows - 1);
         const int64_t y = (EPI == kGrad ? (int64_t)p.local_target[r] - p.v0 : p.target[r]) - (t.n0 + wn0);
         tgt[i] = y >= 0 && y < WN ? (int)y : -1;
-        if constexpr (EPI == kGrad) info[i] = p.row[r];
+        if constexpr (EPI == kGrad) {
+          info[i] = p.row[r];
+          if (t.m0 + wm0 + 16 * i + frow >= p.a_rows) info[i].y = 0.f;
+        }
       }
     }
     v4f acc[TM][TN];
@@ -528,6 +534,13 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
         const float f = EPI == kGrad ? info[i].y : scale;
         // a row of weight zero (an ignored target) has no gradient, whatever its logits
         const uint32_t keep = EPI == kGrad && f == 0.f ? 0u : ~0u;
+        if (EPI == kGrad && d.n0 + wn0 + WN > p.b_rows) {
+#pragma unroll
+          for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (col0 + 16 * j + v >= p.b_rows) acc[i][j][v] = 0.f;
+        }
 #pragma unroll
         for (int j = 0; j < TN; ++j)
           w[j] = make_uint2(pack_bf16x2_rne(acc[i][j][0] * f, acc[i][j][1] * f) & keep,
@@ -696,7 +709,7 @@ bool large_tiles(int64_t M, int64_t N, int64_t splits) {
 }
 // Tiles of the logits: rows and columns.  Below the large ones, 128 rows for 65
 // to 128 tokens once the columns fill half the chip; else 64, with 256 columns
-// once these tiles fill the chip twice.  (100 tokens, 131072 x 5120: @A us on
+// once these tiles fill the chip twice.  (100 tokens, 131072 x 5120: 261 us on
 // 128 rows, 331 us on 64.  33 tokens: 231 us with 256 columns, 246 us with 128;
 // a step of 128 tokens, 2048 x 512: 43 us with 128, 52 us with 256.)
 struct TileShape {
@@ -709,6 +722,14 @@ TileShape logit_tiles(int64_t T, int64_t V) {
   return {64, (T + 63) / 64 * wide >= 2 * kCus ? 256 : 128};
 }
 
+// Tiles of the gradients' products; `splits` of the contraction (dH).  (dH of
+// 100 tokens, 131072 x 4096: 177 us on 128 rows, 354 us on 64.)
+TileShape gradient_tiles(int64_t M, int64_t N, int64_t splits) {
+  if (large_tiles(M, N, splits)) return {256, 256};
+  if (splits > 1 && M > 64 && M <= 128 && (N + 255) / 256 * splits >= kCus / 2) return {128, 256};
+  return {64, 128};
+}
+
 // Tiles a workgroup: more hide more epilogues, but workgroups drift apart
 // within a launch and then share fewer operand slices in the L2.
 constexpr int kRounds = 4;
@@ -716,8 +737,7 @@ constexpr int kRounds = 4;
 template <int EPI, bool AKM = false, bool BKM = false>
 hipError_t run_gemm(XentGemm p, int splits, hipStream_t stream) {
   constexpr bool LOGITS = EPI == kStats || EPI == kGrad;
-  const TileShape tile = LOGITS ? logit_tiles(p.M, p.N)
-                                : large_tiles(p.M, p.N, splits) ? TileShape{256, 256} : TileShape{64, 128};
+  const TileShape tile = LOGITS ? logit_tiles(p.M, p.N) : gradient_tiles(p.M, p.N, splits);
   p.tiles_m = (p.M + tile.rows - 1) / tile.rows;
   p.tiles_n = (p.N + tile.cols - 1) / tile.cols;
   p.splits = splits;
@@ -729,10 +749,10 @@ hipError_t run_gemm(XentGemm p, int splits, hipStream_t stream) {
     hipLaunchKernelGGL((xent_gemm_kernel<256, 256, 2, 4, EPI, AKM, BKM>), many, dim3(512), 0, stream, p);
   else if (tile.cols == 128)
     hipLaunchKernelGGL((xent_gemm_kernel<64, 128, 1, 4, EPI, AKM, BKM>), few, dim3(256), 0, stream, p);
-  else if constexpr (LOGITS) {
+  else if constexpr (EPI != kOut) {   // dW has no shape of few rows and many columns
     if (tile.rows == 128)
       hipLaunchKernelGGL((xent_gemm_kernel<128, 256, 2, 4, EPI, AKM, BKM>), many, dim3(512), 0, stream, p);
-    else
+    else if constexpr (LOGITS)
       hipLaunchKernelGGL((xent_gemm_kernel<64, 256, 1, 4, EPI, AKM, BKM>), few, dim3(256), 0, stream, p);
   }
   return hipGetLastError();
@@ -783,9 +803,11 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
     if (s > piece / 512) s = piece / 512;
     return s < 1 ? (int64_t)1 : s;
   };
-  const int64_t s_large = splits_of(256, 256);
-  L.splits = (int)(large_tiles(T, K, s_large) ? s_large : splits_of(64, 128));
-  // (splits_of(64, 128) <= s_large, so run_gemm takes the same decision.)
+  for (const TileShape t : {TileShape{256, 256}, TileShape{128, 256}, TileShape{64, 128}}) {
+    const int64_t n_splits = splits_of(t.rows, t.cols);
+    L.splits = (int)n_splits;
+    if (gradient_tiles(T, K, n_splits).rows == t.rows) break;   // as run_gemm will choose
+  }
   L.row = take((size_t)T * sizeof(float2));
   L.target = take((size_t)T * 4);
   L.scale = take(4);
@@ -813,7 +835,7 @@ hipError_t launch_xent_fwd(const XentArgs& p, void* ws, hipStream_t stream) {
   XentGemm g = {};
   g.a = (const uint8_t*)p.h; g.lda = p.ld_h * 2;
   g.b = (const uint8_t*)p.w; g.ldb = p.ld_w * 2;
-  g.M = (int)p.T; g.N = (int)p.V; g.kblocks = (int)(p.K / 64);
+  g.M = g.a_rows = (int)p.T; g.N = g.b_rows = (int)p.V; g.kblocks = (int)(p.K / 64);
   g.part = (float2*)(base + L.part);
   g.target = p.target;
   g.target_logit = (float*)(base + L.logit);
@@ -837,18 +859,16 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
                      p.ignore_index, p.dloss, p.lse, row, target, scale);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  auto zero = [&](uint16_t* at, int64_t rows, int64_t c0, int64_t c1) {
-    return zero_columns(at, L.ld_g, rows, c0, c1, stream);
-  };
-  // The tokens that fill dW's last slab have no gradient.
-  if (p.dw && L.tp > p.T && (e = zero(g + p.T * L.ld_g, L.tp - p.T, 0, L.ld_g)) != hipSuccess) return e;
   for (int64_t v0 = 0; v0 < p.V; v0 += L.piece) {
     const int64_t nv = p.V - v0 < L.piece ? p.V - v0 : L.piece;
     const uint16_t* const w = (const uint16_t*)p.w + v0 * p.ld_w;
     XentGemm z = {};
     z.a = (const uint8_t*)p.h; z.lda = p.ld_h * 2;
     z.b = (const uint8_t*)w; z.ldb = p.ld_w * 2;
-    z.M = (int)p.T; z.N = (int)nv; z.kblocks = (int)(p.K / 64);
+    // The tokens and columns that fill the last slabs of the next products have
+    // no gradient: zeros.
+    z.M = (int)L.tp; z.N = (int)pad64(nv); z.kblocks = (int)(p.K / 64);
+    z.a_rows = (int)p.T; z.b_rows = (int)nv;
     z.row = row; z.local_target = target; z.v0 = (int)v0;
     z.out = g; z.ldo = L.ld_g;
     if ((e = run_gemm<kGrad>(z, 1, stream)) != hipSuccess) return e;
@@ -861,10 +881,8 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
       if ((e = run_gemm<kOut, true, true>(d, 1, stream)) != hipSuccess) return e;
     }
     if (p.dh) {
-      // The columns that fill dH's last slab have no gradient.
-      if (nv % 64 && (e = zero(g, p.T, nv, pad64(nv))) != hipSuccess) return e;
       XentGemm d = {};   // dH[t, k] += sum_v G[t, v] W[v, k]
-      d.a = (const uint8_t*)g; d.lda = L.ld_g * 2;
+      d.a = (const uint8_t*)g; d.lda = L.ld_g * 2; d.a_rows = (int)p.T;
       d.b = (const uint8_t*)w; d.ldb = p.ld_w * 2; d.b_rows = (int)nv;
       d.M = (int)p.T; d.N = (int)p.K; d.kblocks = (int)(pad64(nv) / 64);
       d.acc = acc; d.add = v0 > 0;
