@@ -203,29 +203,46 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamwLaunch L) {
       load8_f32((const float*)T.v + at, n, v);
     }
     uint32_t rnd[8];
+    float am = 0.f, av = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float gj = g[j] * gs;
       m[j] = m[j] * L.beta1 + gj * L.one_minus_beta1;
       v[j] = v[j] * L.beta2 + gj * gj * L.one_minus_beta2;
-      // Hardware square root and reciprocal, each within 1 ulp (9.2e-8 and
-      // 9.0e-8 measured): the step they form is far smaller than p, and with
-      // IEEE forms the 8-bit kernel was bound by its arithmetic.
-      root[j] = __builtin_amdgcn_sqrtf(v[j]);
-      p[j] = p[j] * L.decay - m[j] * __builtin_amdgcn_rcpf(root[j] * L.root_factor + L.eps) * L.step_size;
       rnd[j] = RANDOM ? mix32(T.key + (uint32_t)i + j) : 0u;
+      if (EIGHT && j < n) {
+        am = fmaxf(am, fabsf(m[j]));
+        av = fmaxf(av, v[j]);
+      }
     }
     if constexpr (EIGHT) {
-      float am = 0.f, av = 0.f;
+      am = row16_max(am);
+      av = row16_max(av);
+      // Hardware square root and reciprocal, each within 1 ulp (9.2e-8 and
+      // 9.0e-8 measured): codes keep 4 bits and the step is far smaller than
+      // p, while the IEEE forms bind this kernel by its arithmetic (723
+      // against 655 us for 336M elements).  They do not take subnormals: a
+      // block of them gets the IEEE root.
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (j < n) {
-          am = fmaxf(am, fabsf(m[j]));
-          av = fmaxf(av, v[j]);
-        }
+      for (int j = 0; j < 8; ++j) root[j] = __builtin_amdgcn_sqrtf(v[j]);
+      if (__builtin_amdgcn_ballot_w64(av > 0.f && av < 0x1p-100f)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) root[j] = __builtin_sqrtf(v[j]);
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        p[j] = p[j] * L.decay - m[j] * __builtin_amdgcn_rcpf(root[j] * L.root_factor + L.eps) * L.step_size;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        p[j] = p[j] * L.decay - m[j] / (__builtin_sqrtf(v[j]) * L.root_factor + L.eps) * L.step_size;
+    }
+    if constexpr (EIGHT) {
       // The root's scale comes from the correctly rounded root of the largest v.
-      const int em = scale_exponent(row16_max(am)), er = scale_exponent(__builtin_sqrtf(row16_max(av)));
+      const int em = scale_exponent(am), er = scale_exponent(__builtin_sqrtf(av));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (v[j] > 0.f) root[j] = fmaxf(root[j], 0x1p-75f);   // above zero whatever the hardware made of it
       store8_codes((uint8_t*)T.m + at, n, encode8<RANDOM, false>(m, em, rnd, 0));
       store8_codes((uint8_t*)T.v + at, n, encode8<RANDOM, true>(root, er, rnd, 16));
       if ((threadIdx.x & 15) == 0) {

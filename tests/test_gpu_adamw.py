@@ -247,3 +247,21 @@ def test_equal_arguments_give_equal_bits(gpu):
     for a, b, c in zip(ds, twin, other):
         assert all(torch.equal(a[k], b[k]) for k in a)
         assert not torch.equal(a["m"], c["m"])
+
+
+def test_subnormal_second_moments(gpu):
+    """Gradients of 1e-20, whose squares are subnormal: the root still comes
+    out, within half a code (2^-4) and the subnormal's own rounding (2^-11)."""
+    n = 300
+    z = dict(dtype=torch.uint8, device=gpu)
+    d = {"param": torch.zeros(n, device=gpu), "grad": torch.full((n,), 1e-20, device=gpu), "m": torch.zeros(n, **z),
+         "root": torch.zeros(n, **z), "m_scale": torch.ones(3, device=gpu), "root_scale": torch.ones(3, device=gpu)}
+    d["grad"][256:] = 1.0
+    d["grad"][257] = 1e-20          # next to a large one: the smallest code
+    say("adamw subnormal moments")
+    _call([d], 8, None)
+    root = e4m3.decode(d["root"].cpu().numpy()) * np.repeat(_f64(d["root_scale"]), 128)[:n]
+    want = np.sqrt((1 - HYPER["beta2"]) * _f64(d["grad"]) ** 2)
+    sure = np.arange(n) != 257
+    assert np.all(np.abs(root - want)[sure] <= (2.0 ** -4 + 2.0 ** -11) * want[sure])
+    assert int(d["root"][257]) == 1 and bool(d["param"].isfinite().all())
