@@ -154,7 +154,8 @@ constexpr int64_t kXentMaxT = (int64_t)1 << 24, kXentMaxV = (int64_t)1 << 28, kX
 
 bool xent_dims_ok(int64_t T, int64_t V, int64_t K) {
   return T >= 0 && V >= 0 && T <= kXentMaxT && V <= kXentMaxV && K >= 64 && K <= kXentMaxK && K % 64 == 0 &&
-         cdiv(T, 256) * cdiv(V, 256) < kXentMaxTiles && cdiv(T, 256) * cdiv(K, 256) < kXentMaxTiles;
+         cdiv(T, 256) * cdiv(V, 256) < kXentMaxTiles && cdiv(T, 256) * cdiv(K, 256) < kXentMaxTiles &&
+         cdiv(V, 256) * cdiv(K, 256) < kXentMaxTiles;
 }
 
 // The products address a tile of 256 rows with 32-bit byte offsets.
@@ -171,7 +172,7 @@ int check_xent(const void* h, int64_t ld_h, const void* w, int64_t ld_w, const i
   if (!xent_dims_ok(T, V, K))
     return fail(FP8BW_ERR_SHAPE,
                 "T=%lld V=%lld K=%lld: K must be a multiple of 64 in [64, 2^20], V <= 2^28, T <= 2^24, "
-                "ceil(T / 256) ceil(max(V, K) / 256) < 2^23",
+                "ceil(a / 256) ceil(b / 256) < 2^23 for any two of them",
                 (long long)T, (long long)V, (long long)K);
   if (T == 0) return FP8BW_OK;
   if (V == 0) return fail(FP8BW_ERR_SHAPE, "an empty vocabulary has no cross entropy");

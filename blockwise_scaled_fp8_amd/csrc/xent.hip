@@ -40,6 +40,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void;
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
+constexpr int kMaxStages = 3;   // of 64 contraction elements, in LDS
 constexpr int kCus = 256;   // compute units of an MI355X
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -61,7 +62,7 @@ struct XentGemm {
   int M, N;
   int kblocks;                     // of 64 elements (128 bytes)
   int kb_per_split, splits;
-  int rounds;                      // tiles per workgroup (large tiles)
+  int rounds;                      // tiles per workgroup (8-wave kernels)
   int tiles_m, tiles_n;
   // kStats
   float2* part;                    // [tiles_n][M] (max, sum of exp(z - max))
@@ -301,22 +302,15 @@ struct Tile {
 // this one's epilogue, which uses LDS beside that stage; its results are stored
 // by the waves that load nothing, so that no load waits for them.
 // Any M and N: a tile past an edge loads rows again and stores only its own.
-template <int BM, int BN, int WGM, int WGN, int EPI, bool AKM, bool BKM>
-__global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGemm p) {
+template <int BM, int BN, int WGM, int WGN, int STAGES, int EPI, bool AKM, bool BKM>
+__device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t* const (&sA)[kMaxStages],
+                                           uint8_t* const (&sB)[kMaxStages], uint8_t* sE) {
   constexpr bool SMALL = BM == 64;
-  constexpr int STAGES = BN == 128 || BM == 128 ? 3 : 2;
-  constexpr int LATER = STAGES == 3 ? (BM + BN) / 16 : 0;         // a loading wave's loads of one later slab
+  constexpr int LATER = (STAGES - 2) * (BM + BN) / 16;         // a loading wave's loads of the later slabs
   constexpr int NW = WGM * WGN;
   constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16;
   constexpr bool ROWS = EPI == kStats || EPI == kGrad;       // the epilogue needs its rows' targets
   constexpr bool STAGED = !SMALL && (EPI == kGrad || EPI == kOut);
-  __shared__ __attribute__((aligned(1024))) uint8_t sA0[BM * 128], sA1[BM * 128], sA2[STAGES == 3 ? BM * 128 : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t sB0[BN * 128], sB1[BN * 128], sB2[STAGES == 3 ? BN * 128 : 16];
-  uint8_t* const sA[3] = {sA0, sA1, sA2};
-  uint8_t* const sB[3] = {sB0, sB1, sB2};
-  // Each wave's row statistics.  (The small kernel uses a stage for them.)
-  __shared__ __attribute__((aligned(16))) uint8_t sE[!SMALL && EPI == kStats ? WGN * BM * 8 : 16];
-
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm0 = (wave / WGN) * WM, wn0 = (wave % WGN) * WN;
   const int frow = lane & 15, fq = lane >> 4;
@@ -346,8 +340,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
     la.init(p.a, p.lda, t.m0, AKM ? p.tiles_m * BM : p.a_rows, p.a_rows, wave, lane);
     lb.init(p.b, p.ldb, t.n0, BKM ? p.N : p.b_rows, p.b_rows, wave, lane);
     if (t.kb0 < t.kb1) {
-      issue(t.kb0, sA0, sB0);
-      if constexpr (STAGES == 3) issue(min(t.kb0 + 1, t.kb1 - 1), sA1, sB1);
+#pragma unroll
+      for (int st = 0; st < STAGES - 1; ++st) issue(min(t.kb0 + st, t.kb1 - 1), sA[st], sB[st]);
     }
   };
   float scale = 1.f;
@@ -355,9 +349,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
 
   // Workgroups 0 .. kCus - 1 start with tiles 0 .. kCus - 1, the next kCus
   // after all of theirs.
-  int number = SMALL ? blockIdx.x : blockIdx.x / kCus * (kCus * p.rounds) + blockIdx.x % kCus;
+  int number = SMALL ? block : block / kCus * (kCus * p.rounds) + block % kCus;
   if (number >= total) return;
-  const int last = SMALL ? total : min(total, (int)(blockIdx.x / kCus + 1) * kCus * p.rounds);
+  const int last = SMALL ? total : min(total, (block / kCus + 1) * kCus * p.rounds);
   Tile t = locate(number);
   begin(t);
   for (;;) {
@@ -440,7 +434,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
     if constexpr (EPI == kStats) {
       // Maximum and sum of exponentials of each row over this wave's columns
       // (a row's columns lie in lanes frow + 16 q), then over the waves.
-      float2* const red = (float2*)(SMALL ? sA0 : sE);          // [WGN][BM]
+      float2* const red = (float2*)sE;          // [WGN][BM]
       auto statistics = [&](auto check) __attribute__((always_inline)) {
         constexpr bool kCheck = decltype(check)::value;
 #pragma unroll
@@ -611,6 +605,42 @@ __global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGem
   }
 }
 
+// A kernel's stages, and its waves' row statistics (64-row kernels: in a stage).
+#define XENT_LDS(BM, BN, WGN, STAGES, EPI)                                                            \
+  __shared__ __attribute__((aligned(1024))) uint8_t sA0[BM * 128], sA1[BM * 128];                     \
+  __shared__ __attribute__((aligned(1024))) uint8_t sB0[BN * 128], sB1[BN * 128];                     \
+  __shared__ __attribute__((aligned(1024))) uint8_t sA2[STAGES > 2 ? BM * 128 : 16];                  \
+  __shared__ __attribute__((aligned(1024))) uint8_t sB2[STAGES > 2 ? BN * 128 : 16];                  \
+  __shared__ __attribute__((aligned(16))) uint8_t sums[BM > 64 && EPI == kStats ? WGN * BM * 8 : 16]; \
+  uint8_t* const sA[kMaxStages] = {sA0, sA1, sA2};                                                    \
+  uint8_t* const sB[kMaxStages] = {sB0, sB1, sB2};                                                    \
+  uint8_t* const sE = BM > 64 ? sums : sA0
+
+template <int BM, int BN, int WGM, int WGN, int STAGES, int EPI, bool AKM, bool BKM>
+__global__ __launch_bounds__(64 * WGM * WGN) void xent_gemm_kernel(const XentGemm p) {
+  XENT_LDS(BM, BN, WGN, STAGES, EPI);
+  xent_tiles<BM, BN, WGM, WGN, STAGES, EPI, AKM, BKM>(p, blockIdx.x, sA, sB, sE);
+}
+
+// dH's and dW's products in one launch: the first workgroups dH's, which are
+// the longer, then dW's, which fill what they leave.
+template <int BM, int BN, int WGM, int WGN, int STAGES>
+__global__ __launch_bounds__(64 * WGM * WGN) void xent_pair_kernel(const XentGemm h, const XentGemm w, int h_blocks) {
+  XENT_LDS(BM, BN, WGN, STAGES, kOut);
+  if ((int)blockIdx.x < h_blocks)
+    xent_tiles<BM, BN, WGM, WGN, STAGES, kAcc, false, true>(h, blockIdx.x, sA, sB, sE);
+  else
+    xent_tiles<BM, BN, WGM, WGN, STAGES, kOut, true, true>(w, blockIdx.x - h_blocks, sA, sB, sE);
+}
+
+// (m, s) and (m2, s2): sums of exponentials s, s2 beside their maxima.
+__device__ __forceinline__ void join_sums(float& m, float& s, float m2, float s2) {
+  const float top = fmaxf(m, m2);
+  const float base = top == -INFINITY ? 0.f : top;
+  s = s * __builtin_amdgcn_exp2f((m - base) * kLog2e) + s2 * __builtin_amdgcn_exp2f((m2 - base) * kLog2e);
+  m = top;
+}
+
 // Joins the tiles' (max, sum) of 16 tokens: 64 threads a token over the
 // tiles, then over the threads in a fixed order.
 __global__ __launch_bounds__(1024) void xent_join_kernel(const float2* __restrict__ part, int tiles,
@@ -619,26 +649,25 @@ __global__ __launch_bounds__(1024) void xent_join_kernel(const float2* __restric
                                                          const int64_t* __restrict__ target,
                                                          int64_t ignore_index, float* __restrict__ loss,
                                                          float* __restrict__ lse) {
-  __shared__ float2 red[64][17];
+  __shared__ float2 red[16][17];
   const int c = threadIdx.x & 15, g = threadIdx.x >> 4;
   const int t = blockIdx.x * 16 + c;
   float m = -INFINITY, s = 0.f;
   if (t < T) {
+#pragma unroll 4
     for (int i = g; i < tiles; i += 64) {
       const float2 e = part[(int64_t)i * T + t];
-      const float top = fmaxf(m, e.x);
-      const float base = top == -INFINITY ? 0.f : top;
-      s = s * __builtin_amdgcn_exp2f((m - base) * kLog2e) + e.y * __builtin_amdgcn_exp2f((e.x - base) * kLog2e);
-      m = top;
+      join_sums(m, s, e.x, e.y);
     }
   }
-  red[g][c] = make_float2(m, s);
+#pragma unroll
+  for (int x = 16; x < 64; x *= 2) join_sums(m, s, __shfl_xor(m, x), __shfl_xor(s, x));
+  if (threadIdx.x % 64 < 16) red[threadIdx.x >> 6][c] = make_float2(m, s);
   __syncthreads();
   if (g == 0 && t < T) {
-    for (int i = 0; i < 64; ++i) m = fmaxf(m, red[i][c].x);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) join_sums(m, s, red[i][c].x, red[i][c].y);
     const float base = m == -INFINITY ? 0.f : m;
-    s = 0.f;
-    for (int i = 0; i < 64; ++i) s += red[i][c].y * __builtin_amdgcn_exp2f((red[i][c].x - base) * kLog2e);
     const float l = base + __logf(s);
     lse[t] = l;
     const int64_t y = target[t];
@@ -734,27 +763,53 @@ TileShape gradient_tiles(int64_t M, int64_t N, int64_t splits) {
 // within a launch and then share fewer operand slices in the L2.
 constexpr int kRounds = 4;
 
+// A product's tiles; the workgroups that run them.
+int64_t lay_out(XentGemm* p, TileShape tile, int splits, int rounds) {
+  p->tiles_m = (p->M + tile.rows - 1) / tile.rows;
+  p->tiles_n = (p->N + tile.cols - 1) / tile.cols;
+  p->splits = splits;
+  p->kb_per_split = (p->kblocks + splits - 1) / splits;
+  p->rounds = rounds;
+  const int64_t tiles = (int64_t)p->tiles_m * p->tiles_n * splits;
+  return tile.rows == 64 ? tiles : (tiles + kCus * rounds - 1) / (kCus * rounds) * kCus;
+}
+
 template <int EPI, bool AKM = false, bool BKM = false>
 hipError_t run_gemm(XentGemm p, int splits, hipStream_t stream) {
   constexpr bool LOGITS = EPI == kStats || EPI == kGrad;
   const TileShape tile = LOGITS ? logit_tiles(p.M, p.N) : gradient_tiles(p.M, p.N, splits);
-  p.tiles_m = (p.M + tile.rows - 1) / tile.rows;
-  p.tiles_n = (p.N + tile.cols - 1) / tile.cols;
-  p.splits = splits;
-  p.kb_per_split = (p.kblocks + splits - 1) / splits;
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * splits;
-  p.rounds = kRounds;
-  const dim3 few((unsigned)tiles), many((unsigned)((tiles + kCus * kRounds - 1) / (kCus * kRounds) * kCus));
+  const dim3 grid((unsigned)lay_out(&p, tile, splits, kRounds));
   if (tile.rows == 256)
-    hipLaunchKernelGGL((xent_gemm_kernel<256, 256, 2, 4, EPI, AKM, BKM>), many, dim3(512), 0, stream, p);
+    hipLaunchKernelGGL((xent_gemm_kernel<256, 256, 2, 4, 2, EPI, AKM, BKM>), grid, dim3(512), 0, stream, p);
   else if (tile.cols == 128)
-    hipLaunchKernelGGL((xent_gemm_kernel<64, 128, 1, 4, EPI, AKM, BKM>), few, dim3(256), 0, stream, p);
+    hipLaunchKernelGGL((xent_gemm_kernel<64, 128, 1, 4, 3, EPI, AKM, BKM>), grid, dim3(256), 0, stream, p);
   else if constexpr (EPI != kOut) {   // dW has no shape of few rows and many columns
     if (tile.rows == 128)
-      hipLaunchKernelGGL((xent_gemm_kernel<128, 256, 2, 4, EPI, AKM, BKM>), many, dim3(512), 0, stream, p);
+      hipLaunchKernelGGL((xent_gemm_kernel<128, 256, 2, 4, 3, EPI, AKM, BKM>), grid, dim3(512), 0, stream, p);
     else if constexpr (LOGITS)
-      hipLaunchKernelGGL((xent_gemm_kernel<64, 256, 1, 4, EPI, AKM, BKM>), few, dim3(256), 0, stream, p);
+      hipLaunchKernelGGL((xent_gemm_kernel<64, 256, 1, 4, 2, EPI, AKM, BKM>), grid, dim3(256), 0, stream, p);
   }
+  return hipGetLastError();
+}
+
+// dH's share of a piece and the piece's dW, in one launch where both take the
+// same tiles: one launch fewer (128 tokens, 2048 x 512: 42.6 to 38 us a step),
+// and dW's tiles fill the compute units that dH's leave (1777 tokens, 50001 x
+// 2048: 1287 to 1258 us).  dW's workgroups then run one tile each, as the rest
+// of dH's round is of any length; four: 1276 us.
+hipError_t run_pair(XentGemm h, int splits, XentGemm w, hipStream_t stream) {
+  const TileShape th = gradient_tiles(h.M, h.N, splits), tw = gradient_tiles(w.M, w.N, 1);
+  if (th.rows != tw.rows) {
+    const hipError_t e = run_gemm<kAcc, false, true>(h, splits, stream);
+    return e != hipSuccess ? e : run_gemm<kOut, true, true>(w, 1, stream);
+  }
+  // whole turns of the XCDs, so that dW's workgroups start on the first
+  const int64_t nh = (lay_out(&h, th, splits, kRounds) + 7) / 8 * 8;
+  const dim3 grid((unsigned)(nh + lay_out(&w, tw, 1, 1)));
+  if (th.rows == 256)
+    hipLaunchKernelGGL((xent_pair_kernel<256, 256, 2, 4, 2>), grid, dim3(512), 0, stream, h, w, (int)nh);
+  else
+    hipLaunchKernelGGL((xent_pair_kernel<64, 128, 1, 4, 3>), grid, dim3(256), 0, stream, h, w, (int)nh);
   return hipGetLastError();
 }
 
@@ -872,22 +927,20 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
     z.row = row; z.local_target = target; z.v0 = (int)v0;
     z.out = g; z.ldo = L.ld_g;
     if ((e = run_gemm<kGrad>(z, 1, stream)) != hipSuccess) return e;
-    if (p.dw) {
-      XentGemm d = {};   // dW[v, k] = sum_t G[t, v] H[t, k]
-      d.a = (const uint8_t*)g; d.lda = L.ld_g * 2; d.a_rows = (int)L.tp;
-      d.b = (const uint8_t*)p.h; d.ldb = p.ld_h * 2; d.b_rows = (int)p.T;
-      d.M = (int)nv; d.N = (int)p.K; d.kblocks = (int)(L.tp / 64);
-      d.out = (uint16_t*)p.dw + v0 * p.ld_dw; d.ldo = p.ld_dw; d.scale = scale;
-      if ((e = run_gemm<kOut, true, true>(d, 1, stream)) != hipSuccess) return e;
-    }
-    if (p.dh) {
-      XentGemm d = {};   // dH[t, k] += sum_v G[t, v] W[v, k]
-      d.a = (const uint8_t*)g; d.lda = L.ld_g * 2; d.a_rows = (int)p.T;
-      d.b = (const uint8_t*)w; d.ldb = p.ld_w * 2; d.b_rows = (int)nv;
-      d.M = (int)p.T; d.N = (int)p.K; d.kblocks = (int)(pad64(nv) / 64);
-      d.acc = acc; d.add = v0 > 0;
-      if ((e = run_gemm<kAcc, false, true>(d, L.splits, stream)) != hipSuccess) return e;
-    }
+    XentGemm dw = {};   // dW[v, k] = sum_t G[t, v] H[t, k]
+    dw.a = (const uint8_t*)g; dw.lda = L.ld_g * 2; dw.a_rows = (int)L.tp;
+    dw.b = (const uint8_t*)p.h; dw.ldb = p.ld_h * 2; dw.b_rows = (int)p.T;
+    dw.M = (int)nv; dw.N = (int)p.K; dw.kblocks = (int)(L.tp / 64);
+    dw.out = p.dw ? (uint16_t*)p.dw + v0 * p.ld_dw : nullptr; dw.ldo = p.ld_dw; dw.scale = scale;
+    XentGemm dh = {};   // dH[t, k] += sum_v G[t, v] W[v, k]
+    dh.a = (const uint8_t*)g; dh.lda = L.ld_g * 2; dh.a_rows = (int)p.T;
+    dh.b = (const uint8_t*)w; dh.ldb = p.ld_w * 2; dh.b_rows = (int)nv;
+    dh.M = (int)p.T; dh.N = (int)p.K; dh.kblocks = (int)(pad64(nv) / 64);
+    dh.acc = acc; dh.add = v0 > 0;
+    if (p.dh && p.dw) e = run_pair(dh, L.splits, dw, stream);
+    else if (p.dw) e = run_gemm<kOut, true, true>(dw, 1, stream);
+    else if (p.dh) e = run_gemm<kAcc, false, true>(dh, L.splits, stream);
+    if (e != hipSuccess) return e;
   }
   if (!p.dh) return hipSuccess;
   const int64_t groups = (p.T * p.K / 4 + 255) / 256;

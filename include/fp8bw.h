@@ -472,8 +472,9 @@ int fp8bw_rms_norm_bwd(const void* dy, int64_t ld_dy, const void* s, int64_t ld_
  *            aligned (backward: 0 or 1).
  *   Requires K % 64 == 0, 64 <= K <= 2^20, V <= 2^28, T <= 2^24, leading
  *   dimensions a multiple of 8 and at most 2^22 - K / 128, and
- *   ceil(T / 256) * ceil(max(V, K) / 256) < 2^23.  With V == 0 every call with T > 0 is
- *   rejected (an empty sum has no logarithm); with T == 0 dw is set to zero.
+ *   ceil(a / 256) * ceil(b / 256) < 2^23 for any two of T, V, K.  With V == 0 every
+ *   call with T > 0 is rejected (an empty sum has no logarithm); with T == 0 dw is set
+ *   to zero.
  */
 size_t fp8bw_linear_xent_ws_bytes(int64_t T, int64_t V, int64_t K, int backward);
 int fp8bw_linear_xent_fwd(const void* h, int64_t ld_h, const void* w, int64_t ld_w,

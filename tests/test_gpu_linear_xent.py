@@ -103,6 +103,18 @@ def test_strided_operands_and_single_gradients(gpu):
     assert fp8.linear_xent_bwd(dd, hd, wd, td, lse, need_dh=False, need_dw=False) == (None, None)
 
 
+@pytest.mark.parametrize("shape", [(40, 700, 256), (100, 20000, 512), (700, 9000, 1024), (2049, 4097, 192)])
+def test_gradients_together_and_alone(gpu, shape):
+    """Both gradients in one launch, or in two where their tiles differ, have
+    the bits of each by itself."""
+    h, w, target, dloss = (t.to(gpu) for t in _case(*shape, seed=sum(shape)))
+    say(f"linear_xent gradients {shape}")
+    _, lse = fp8.linear_xent_fwd(h, w, target)
+    dh, dw = fp8.linear_xent_bwd(dloss, h, w, target, lse)
+    assert torch.equal(dh, fp8.linear_xent_bwd(dloss, h, w, target, lse, need_dw=False)[0])
+    assert torch.equal(dw, fp8.linear_xent_bwd(dloss, h, w, target, lse, need_dh=False)[1])
+
+
 def test_targets_that_do_not_count(gpu):
     """Ignored tokens (another ignore_index, in the vocabulary too), targets
     outside it, and weights of zero: no gradient, whatever the token holds."""
