@@ -816,9 +816,14 @@ hipError_t run_pair(XentGemm h, int splits, XentGemm w, hipStream_t stream) {
 int64_t pad64(int64_t n) { return (n + 63) & ~(int64_t)63; }
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Vocabulary columns per piece: whole tiles, as many as keep G at 256 MB, the
-// memory-side cache's size.
-constexpr int64_t kPieceBytes = (int64_t)256 << 20;
+// Vocabulary columns per piece: whole tiles, as many as keep G at 128 MB, so
+// that the products after it find it in the memory-side cache (8192 tokens,
+// 131072 x 4096: 26.05 ms a step; 256 MB 26.55, 64 MB 26.70, 1 GB 26.28).  But
+// for many tokens 8192 columns, as dH's sums are read and written once a piece
+// (32768 x 4096: 16640 tokens 14.30 ms with 8192 columns, 14.79 with 4032; 65536
+// tokens 53.9 and 79.8 ms with 8192 and 1024).
+constexpr int64_t kPieceBytes = (int64_t)128 << 20;
+constexpr int64_t kPieceMinCols = 8192;
 
 struct XentLayout {
   int64_t part_tiles;          // vocabulary tiles of the statistics
@@ -841,7 +846,7 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
   }
   L.tp = pad64(T);
   int64_t piece = kPieceBytes / 2 / L.tp / 256 * 256;
-  if (piece < 256) piece = 256;
+  if (piece < kPieceMinCols) piece = kPieceMinCols;
   if (piece > V) piece = V;
   const int64_t n = (V + piece - 1) / piece;
   if (n > 1) piece = ((V + n - 1) / n + 255) / 256 * 256;   // even pieces
