@@ -221,11 +221,15 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamwLaunch L) {
       // Hardware square root and reciprocal, each within 1 ulp (9.2e-8 and
       // 9.0e-8 measured): codes keep 4 bits and the step is far smaller than
       // p, while the IEEE forms bind this kernel by its arithmetic (723
-      // against 655 us for 336M elements).  They do not take subnormals: a
-      // block of them gets the IEEE root.
+      // against 655 us for 336M elements).  They do not take subnormals:
+      // where a wave has some, it takes the IEEE root.
+      bool tiny = false;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) root[j] = __builtin_amdgcn_sqrtf(v[j]);
-      if (__builtin_amdgcn_ballot_w64(av > 0.f && av < 0x1p-100f)) {
+      for (int j = 0; j < 8; ++j) {
+        root[j] = __builtin_amdgcn_sqrtf(v[j]);
+        tiny |= __builtin_amdgcn_classf(v[j], 1 << 7);   // positive subnormal
+      }
+      if (__builtin_amdgcn_ballot_w64(tiny)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) root[j] = __builtin_sqrtf(v[j]);
       }
@@ -240,9 +244,6 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamwLaunch L) {
     if constexpr (EIGHT) {
       // The root's scale comes from the correctly rounded root of the largest v.
       const int em = scale_exponent(am), er = scale_exponent(__builtin_sqrtf(av));
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (v[j] > 0.f) root[j] = fmaxf(root[j], 0x1p-75f);   // above zero whatever the hardware made of it
       store8_codes((uint8_t*)T.m + at, n, encode8<RANDOM, false>(m, em, rnd, 0));
       store8_codes((uint8_t*)T.v + at, n, encode8<RANDOM, true>(root, er, rnd, 16));
       if ((threadIdx.x & 15) == 0) {
