@@ -23,9 +23,9 @@
 // block's scale takes does not hang on how an expression was compiled.
 //
 // Every element is read and written once; the kernel is bound by HBM: 336M bf16
-// parameters with 8-bit states 650 us (5.2 TB/s; 885 us with IEEE square root and
+// parameters with 8-bit states 660 us (5.2 TB/s; 885 us with IEEE square root and
 // division and the rounding in integer arithmetic), with fp32 states and
-// masters 1814 us (5.2 TB/s).
+// masters 1810 us (5.2 TB/s).
 
 #include "device_common.h"
 #include "launch.h"

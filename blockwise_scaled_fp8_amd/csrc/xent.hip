@@ -18,9 +18,9 @@
 // the logits, G in dH) or across it (W in dH; G and H in dW): the latter are
 // turned by transposing LDS reads, so nothing is ever transposed in memory.
 // The products are bound by the matrix cores from a few hundred tokens on, by
-// the reading of W below: 8192 tokens, 131072 x 4096, statistics 6.1 ms (1.45
-// PFLOP/s, matrix cores busy 72% of the cycles at the 1.87 GHz they are given),
-// G 6.7, dW 6.7 and dH 6.6 ms; 33 tokens, 131072 x 5120, forward 225 us (6 TB/s).
+// the reading of W below: 8192 tokens, 131072 x 4096, statistics 6.1 ms (1.44
+// PFLOP/s, matrix cores busy 72% of the cycles at the 1.9 GHz they are given),
+// G 6.5, dH and dW 13.0 ms; 33 tokens, 131072 x 5120, forward 223 us (6 TB/s).
 //
 // Rounding: G is held as bf16, the accuracy of the matrix cores' operands.
 // It is formed with dloss divided by its largest magnitude, which the
