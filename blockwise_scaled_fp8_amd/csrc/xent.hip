@@ -38,6 +38,7 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) void global_void;
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kMaxStages = 3;   // of 64 contraction elements, in LDS
@@ -50,6 +51,14 @@ enum XentEpilogue {
   kGrad = 1,     // G in bf16
   kOut = 2,      // bf16, times *scale
   kAcc = 3       // fp32 partial [split][M][N], written or added to
+};
+
+// What the tokens of a backward have in common.
+struct XentTokens {
+  float scale;                     // largest |dloss| of those that count
+  int masked;                      // one that has no gradient holds an infinity or NaN
+  int pad[2];
+  float zeros[4];
 };
 
 struct XentGemm {
@@ -69,12 +78,12 @@ struct XentGemm {
   const int64_t* target;
   float* target_logit;             // [M]
   // kGrad
-  const float2* row;               // [M] (lse, dloss / scale)
+  const float2* row;               // [M], kOut [contraction]: (lse, dloss / scale)
   const int* local_target;         // [M] target column of the whole vocabulary, or -1
   int v0;                          // first vocabulary column of this piece
   // outputs
   void* out; int64_t ldo;          // kGrad, kOut: bf16 elements
-  const float* scale;
+  const XentTokens* tokens;        // kOut
   float* acc;                      // kAcc
   int add;
 };
@@ -146,7 +155,9 @@ __device__ __forceinline__ bf16x8 frag_km(const uint8_t* tile, uint32_t off) {
 // or with KM 64 rows of 2 C bytes; 1 KB an instruction either way.  Nothing
 // past the operand is read: rows (KM: columns) past its end are replaced by
 // ones before it, which reach only results that nobody stores.
-template <int C, bool KM>
+// MASK (H in dW, KM): once some token without a gradient holds an infinity or
+// NaN, the rows of such tokens are loaded as zeros, as 0 times those is no 0.
+template <int C, bool KM, bool MASK>
 struct SlabLoader {
   static constexpr int N = C / 16;                 // loads a wave
   static constexpr int RPL = KM ? 512 / C : 8;     // rows a load covers
@@ -156,6 +167,9 @@ struct SlabLoader {
   int64_t ld;
   int rows, lrow, wave, edge;   // KM: contraction rows; else the load number that holds the last row, -1: all exist
   __amdgpu_buffer_rsrc_t rsrc;
+  const XentTokens* tokens;     // MASK
+  const float2* row;
+  bool masked;
 
   // first: first row (KM: column) of the tile; limit: the operand's; k_rows:
   // its contraction rows (KM).
@@ -214,6 +228,16 @@ struct SlabLoader {
           to += 2048;
           asm volatile("" : "+s"(o), "+s"(to));
         }
+      }
+    } else if (MASK && masked) {
+#pragma unroll 1
+      for (int i = 0; i < N; ++i) {
+        const int t = kb * 64 + RPL * (wave + 2 * i) + lrow;
+        const bool live = t < rows && row[min(t, rows - 1)].y != 0.f;
+        const uint8_t* const from =
+            live ? base + (int64_t)t * ld + ((2 * RPL * i >> 4) & 1 ? col1 : col0) : (const uint8_t*)tokens->zeros;
+        __builtin_amdgcn_global_load_lds((global_void*)(uintptr_t)from, (lds_void*)(lds + to), 16, 0, 0);
+        to = __builtin_amdgcn_readfirstlane(to + 2048);
       }
     } else {
       // A descriptor of its own per slab: offsets stay within 64 rows.
@@ -328,8 +352,8 @@ __device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t
     t.kb1 = min(p.kblocks, t.kb0 + p.kb_per_split);
     return t;
   };
-  SlabLoader<BM, AKM> la;
-  SlabLoader<BN, BKM> lb;
+  SlabLoader<BM, AKM, false> la;
+  SlabLoader<BN, BKM, EPI == kOut> lb;
   auto issue = [&](int kb, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
     if (wave < 2) {
       la.issue(kb, sa);
@@ -345,7 +369,12 @@ __device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t
     }
   };
   float scale = 1.f;
-  if constexpr (EPI == kOut) scale = *p.scale;
+  if constexpr (EPI == kOut) {
+    scale = p.tokens->scale;
+    lb.tokens = p.tokens;
+    lb.row = p.row;
+    lb.masked = p.tokens->masked != 0;
+  }
 
   // Workgroups 0 .. kCus - 1 start with tiles 0 .. kCus - 1, the next kCus
   // after all of theirs.
@@ -679,10 +708,12 @@ __global__ __launch_bounds__(1024) void xent_join_kernel(const float2* __restric
 
 // scale = max |dloss| over the tokens that count, and per token (lse, dloss /
 // scale) and the target column; ignored and out-of-range targets get weight 0.
+// An infinity or NaN in a token's row of H makes every one of its logits
+// infinite or NaN, and so its lse.
 __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, const int64_t* __restrict__ target,
                                                          int64_t ignore_index, const float* __restrict__ dloss,
                                                          const float* __restrict__ lse, float2* __restrict__ row,
-                                                         int* __restrict__ local_target, float* __restrict__ scale) {
+                                                         int* __restrict__ local_target, XentTokens* __restrict__ tokens) {
   __shared__ float red[16];
   float m = 0.f;
   for (int t = threadIdx.x; t < T; t += 1024) {
@@ -694,13 +725,17 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, const
   __syncthreads();
   m = 0.f;
   for (int i = 0; i < 16; ++i) m = fmaxf(m, red[i]);
-  if (threadIdx.x == 0) *scale = m;
+  bool masked = false;
   for (int t = threadIdx.x; t < T; t += 1024) {
     const int64_t y = target[t];
     const bool counts = y != ignore_index && y >= 0 && y < V;
-    row[t] = make_float2(lse[t], counts && dloss[t] != 0.f ? dloss[t] / m : 0.f);
+    const float2 r = make_float2(lse[t], counts && dloss[t] != 0.f ? dloss[t] / m : 0.f);
+    row[t] = r;
     local_target[t] = counts ? (int)y : -1;
+    masked |= r.y == 0.f && !(fabsf(r.x) < INFINITY);
   }
+  const int any = __syncthreads_or(masked);
+  if (threadIdx.x == 0) *tokens = XentTokens{m, any, {0, 0}, {0.f, 0.f, 0.f, 0.f}};
 }
 
 // Zeros in columns [c0, c1) of bf16 rows: one row and 2048 columns a workgroup.
@@ -713,9 +748,9 @@ __global__ __launch_bounds__(256) void zero_columns_kernel(uint16_t* out, int64_
 
 // dH = scale * sum over the splits of their fp32 shares, to bf16.
 __global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ acc, int splits, int64_t T,
-                                                      int64_t K, const float* __restrict__ scale,
+                                                      int64_t K, const XentTokens* __restrict__ tokens,
                                                       uint16_t* __restrict__ dh, int64_t ld_dh) {
-  const float f = *scale;
+  const float f = tokens->scale;
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < T * K; i += (int64_t)gridDim.x * 1024) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = 0; k < splits; ++k) {
@@ -829,7 +864,7 @@ struct XentLayout {
   int64_t part_tiles;          // vocabulary tiles of the statistics
   int64_t tp, piece, ld_g;     // tokens in whole slabs; columns of a piece; G's row
   int splits;                  // of dH's contraction over the piece
-  size_t part, logit, row, target, scale, g, acc, total;
+  size_t part, logit, row, target, tokens, g, acc, total;
 };
 
 XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
@@ -870,7 +905,7 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
   }
   L.row = take((size_t)T * sizeof(float2));
   L.target = take((size_t)T * 4);
-  L.scale = take(4);
+  L.tokens = take(sizeof(XentTokens));
   L.g = take((size_t)L.tp * L.ld_g * 2);
   L.acc = take((size_t)L.splits * T * K * 4);
   L.total = off;
@@ -912,11 +947,11 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
   uint8_t* const base = (uint8_t*)ws;
   float2* const row = (float2*)(base + L.row);
   int* const target = (int*)(base + L.target);
-  float* const scale = (float*)(base + L.scale);
+  XentTokens* const tokens = (XentTokens*)(base + L.tokens);
   uint16_t* const g = (uint16_t*)(base + L.g);
   float* const acc = (float*)(base + L.acc);
   hipLaunchKernelGGL(xent_rows_kernel, dim3(1), dim3(1024), 0, stream, (int)p.T, p.V, p.target,
-                     p.ignore_index, p.dloss, p.lse, row, target, scale);
+                     p.ignore_index, p.dloss, p.lse, row, target, tokens);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   for (int64_t v0 = 0; v0 < p.V; v0 += L.piece) {
@@ -936,7 +971,7 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
     dw.a = (const uint8_t*)g; dw.lda = L.ld_g * 2; dw.a_rows = (int)L.tp;
     dw.b = (const uint8_t*)p.h; dw.ldb = p.ld_h * 2; dw.b_rows = (int)p.T;
     dw.M = (int)nv; dw.N = (int)p.K; dw.kblocks = (int)(L.tp / 64);
-    dw.out = p.dw ? (uint16_t*)p.dw + v0 * p.ld_dw : nullptr; dw.ldo = p.ld_dw; dw.scale = scale;
+    dw.out = p.dw ? (uint16_t*)p.dw + v0 * p.ld_dw : nullptr; dw.ldo = p.ld_dw; dw.tokens = tokens; dw.row = row;
     XentGemm dh = {};   // dH[t, k] += sum_v G[t, v] W[v, k]
     dh.a = (const uint8_t*)g; dh.lda = L.ld_g * 2; dh.a_rows = (int)p.T;
     dh.b = (const uint8_t*)w; dh.ldb = p.ld_w * 2; dh.b_rows = (int)nv;
@@ -950,7 +985,7 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
   if (!p.dh) return hipSuccess;
   const int64_t groups = (p.T * p.K / 4 + 255) / 256;
   hipLaunchKernelGGL(xent_dh_kernel, dim3((unsigned)(groups < (1 << 20) ? groups : (1 << 20))), dim3(256), 0, stream, acc,
-                     L.splits, p.T, p.K, scale, (uint16_t*)p.dh, p.ld_dh);
+                     L.splits, p.T, p.K, tokens, (uint16_t*)p.dh, p.ld_dh);
   return hipGetLastError();
 }
 

@@ -461,7 +461,8 @@ int fp8bw_rms_norm_bwd(const void* dy, int64_t ld_dy, const void* s, int64_t ld_
  *   h, w     device bf16 [T, K] (ld_h) and [V, K] (ld_w).
  *   target   device int64 [T].  A target equal to ignore_index gives loss 0
  *            and no gradient.  Any other target outside [0, V) gives a NaN
- *            loss and no gradient.
+ *            loss and no gradient.  What the rows of h of tokens without a
+ *            gradient (those, and dloss 0) hold reaches neither dh nor dw.
  *   loss, lse, dloss  device fp32 [T]; one loss per token, so that a caller's
  *            mean, sum or weights are dloss.
  *   dh, dw   device bf16 [T, K] (ld_dh) and [V, K] (ld_dw); either may be NULL.

@@ -155,6 +155,26 @@ def test_masked_token_with_infinities(gpu):
     assert not dh[7].any() and torch.equal(dh, want)
 
 
+@pytest.mark.parametrize("shape", [(40, 500, 64), (130, 1000, 192), (1025, 7777, 256)])
+def test_masked_infinities_stay_out_of_dw(gpu, shape):
+    """Infinities and NaN in tokens that have no gradient (ignored, outside the
+    vocabulary, weight 0), the last one among them: dw and dh are those of
+    finite values there."""
+    T, V, K = shape
+    h, w, target, dloss = _case(T, V, K, seed=16)
+    target[7], target[T - 1], target[33], dloss[21] = IGNORE, IGNORE, V + 3, 0.0
+    bad = h.clone()
+    bad[7, 3], bad[T - 1, 0], bad[33, 5], bad[21, K - 1] = float("inf"), float("nan"), float("-inf"), float("nan")
+    w, target, dloss = (t.to(gpu) for t in (w, target, dloss))
+    say(f"linear_xent masked infinities {shape}")
+    grads = []
+    for x in (h.to(gpu), bad.to(gpu)):
+        lse = fp8.linear_xent_fwd(x, w, target)[1]
+        grads.append(fp8.linear_xent_bwd(dloss, x, w, target, lse))
+    for got, want in zip(grads[1], grads[0]):
+        assert torch.equal(got, want)
+
+
 def test_large_logits(gpu):
     """Logits of thousands: the maximum is taken out before the exponential."""
     T, V, K = 66, 777, 64
