@@ -151,15 +151,15 @@ __device__ __forceinline__ bf16x8 frag_km(const uint8_t* tile, uint32_t off) {
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// One operand's slab by direct loads from waves 0 and 1: C rows of 128 bytes,
+// One operand's slab by direct loads from LW waves: C rows of 128 bytes,
 // or with KM 64 rows of 2 C bytes; 1 KB an instruction either way.  Nothing
 // past the operand is read: rows (KM: columns) past its end are replaced by
 // ones before it, which reach only results that nobody stores.
 // MASK (H in dW, KM): once some token without a gradient holds an infinity or
 // NaN, the rows of such tokens are loaded as zeros, as 0 times those is no 0.
-template <int C, bool KM, bool MASK>
+template <int C, bool KM, bool MASK, int LW>
 struct SlabLoader {
-  static constexpr int N = C / 16;                 // loads a wave
+  static constexpr int N = C / (8 * LW);           // loads a wave
   static constexpr int RPL = KM ? 512 / C : 8;     // rows a load covers
   uint32_t off, off_edge;       // a lane's offset in a load's rows; in the load that holds the last row
   uint32_t col0, col1;          // KM: a lane's column bytes, by the swizzle's top bit
@@ -171,6 +171,7 @@ struct SlabLoader {
   const float2* row;
   bool masked;
 
+  static __device__ __forceinline__ bool upper(int i) { return LW * RPL < 32 && (LW * RPL * i >> 4) & 1; }
   // first: first row (KM: column) of the tile; limit: the operand's; k_rows:
   // its contraction rows (KM).
   __device__ __forceinline__ void init(const uint8_t* p, int64_t ld_, int first, int limit, int k_rows,
@@ -182,13 +183,14 @@ struct SlabLoader {
       base = p + 2 * (int64_t)first;
       lrow = lane / (64 / RPL);
       const int chunk = lane % (64 / RPL);
-      // row = RPL (wave + 2 i) + lrow; its bit 4 comes from i alone
+      // row = RPL (wave + LW i) + lrow; its bit 4 comes from i or, if LW rows
+      // of loads are 32 rows, from the wave
       const int swz = km_swz<C>((RPL * wave + lrow) & 15);
       auto column = [&](int top) {
         const int c = 16 * ((chunk >> 1) ^ (swz | top << (C >= 128 ? 2 : 1))) + 8 * (chunk & 1);
         return (uint32_t)(2 * min(c, limit - first - 8));
       };
-      col0 = column(0);
+      col0 = column(LW * RPL == 32 ? RPL * wave >> 4 : 0);
       col1 = column(1);
       off = (uint32_t)((RPL * wave + lrow) * (int)ld);
     } else {
@@ -214,8 +216,8 @@ struct SlabLoader {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + to), 16, off, so, 0, 0);
-          so += 2 * step;
-          to += 2048;
+          so += LW * step;
+          to += LW * 1024;
           asm volatile("" : "+s"(so), "+s"(to));
         }
       } else {
@@ -224,34 +226,34 @@ struct SlabLoader {
         for (int i = 0; i < N; ++i) {
           __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void*)(lds + to), 16, o < edge ? off : off_edge,
                                                    kb * 128 + min(o, edge) * step, 0, 0);
-          o += 2;
-          to += 2048;
+          o += LW;
+          to += LW * 1024;
           asm volatile("" : "+s"(o), "+s"(to));
         }
       }
     } else if (MASK && masked) {
 #pragma unroll 1
       for (int i = 0; i < N; ++i) {
-        const int t = kb * 64 + RPL * (wave + 2 * i) + lrow;
+        const int t = kb * 64 + RPL * (wave + LW * i) + lrow;
         const bool live = t < rows && row[min(t, rows - 1)].y != 0.f;
         const uint8_t* const from =
-            live ? base + (int64_t)t * ld + ((2 * RPL * i >> 4) & 1 ? col1 : col0) : (const uint8_t*)tokens->zeros;
+            live ? base + (int64_t)t * ld + (upper(i) ? col1 : col0) : (const uint8_t*)tokens->zeros;
         __builtin_amdgcn_global_load_lds((global_void*)(uintptr_t)from, (lds_void*)(lds + to), 16, 0, 0);
-        to = __builtin_amdgcn_readfirstlane(to + 2048);
+        to = __builtin_amdgcn_readfirstlane(to + LW * 1024);
       }
     } else {
       // A descriptor of its own per slab: offsets stay within 64 rows.
       const __amdgpu_buffer_rsrc_t rs = rsrc_of(base + (int64_t)kb * 64 * ld, 64 * ld);
       const int left = rows - kb * 64;
       if (left >= 64) {
-        const int step = __builtin_amdgcn_readfirstlane(2 * RPL * (int)ld);
+        const int step = __builtin_amdgcn_readfirstlane(LW * RPL * (int)ld);
         int so = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + to), 16,
-                                                   off + ((2 * RPL * i >> 4) & 1 ? col1 : col0), so, 0, 0);
+                                                   off + (upper(i) ? col1 : col0), so, 0, 0);
           so += step;
-          to += 2048;
+          to += LW * 1024;
           asm volatile("" : "+s"(so), "+s"(to));
         }
       } else {
@@ -259,9 +261,9 @@ struct SlabLoader {
 #pragma unroll
         for (int i = 0; i < N; ++i)
           __builtin_amdgcn_raw_ptr_buffer_load_lds(
-              rs, (lds_void*)(lds + (wave + 2 * i) * 1024), 16,
-              (uint32_t)(min(RPL * (wave + 2 * i) + lrow, left - 1) * (int)ld) +
-                  ((2 * RPL * i >> 4) & 1 ? col1 : col0),
+              rs, (lds_void*)(lds + (wave + LW * i) * 1024), 16,
+              (uint32_t)(min(RPL * (wave + LW * i) + lrow, left - 1) * (int)ld) +
+                  (upper(i) ? col1 : col0),
               0, 0, 0);
       }
     }
@@ -311,7 +313,9 @@ struct Tile {
 // C[m, n] = sum_k A[m, k] B[n, k] on BM x BN tiles of WGM x WGN waves.  A ring
 // of stages of 64 contraction elements in LDS, filled by direct buffer -> LDS
 // loads from waves 0 and 1 (a direct load keeps the issuing wave for about 16
-// cycles; the others go straight to their MFMAs).  Each stage is an LDS
+// cycles; the others go straight to their MFMAs), or from all four of the 64-row
+// kernels, where a tile waits for its slabs (12 tokens, 6853 x 3840: forward 40.2
+// us from two, 37.7 from four).  Each stage is an LDS
 // variable of its own and the stage loop is unrolled, so that the compiler
 // sees that reads of one stage do not depend on loads into another.
 //
@@ -330,7 +334,8 @@ template <int BM, int BN, int WGM, int WGN, int STAGES, int EPI, bool AKM, bool 
 __device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t* const (&sA)[kMaxStages],
                                            uint8_t* const (&sB)[kMaxStages], uint8_t* sE) {
   constexpr bool SMALL = BM == 64;
-  constexpr int LATER = (STAGES - 2) * (BM + BN) / 16;         // a loading wave's loads of the later slabs
+  constexpr int LW = SMALL ? 4 : 2;                       // loading waves
+  constexpr int LATER = (STAGES - 2) * (BM + BN) / (8 * LW);         // a loading wave's loads of the later slabs
   constexpr int NW = WGM * WGN;
   constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16;
   constexpr bool ROWS = EPI == kStats || EPI == kGrad;       // the epilogue needs its rows' targets
@@ -352,10 +357,10 @@ __device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t
     t.kb1 = min(p.kblocks, t.kb0 + p.kb_per_split);
     return t;
   };
-  SlabLoader<BM, AKM, false> la;
-  SlabLoader<BN, BKM, EPI == kOut> lb;
+  SlabLoader<BM, AKM, false, LW> la;
+  SlabLoader<BN, BKM, EPI == kOut, LW> lb;
   auto issue = [&](int kb, uint8_t* sa, uint8_t* sb) __attribute__((always_inline)) {
-    if (wave < 2) {
+    if (LW == WGM * WGN || wave < LW) {
       la.issue(kb, sa);
       lb.issue(kb, sb);
     }
@@ -738,6 +743,80 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, const
   if (threadIdx.x == 0) *tokens = XentTokens{m, any, {0, 0}, {0.f, 0.f, 0.f, 0.f}};
 }
 
+// Columns c .. c + 3 of the sum of `splits` shares of the logits, in order.
+__device__ __forceinline__ float4 sum_shares(const float* z, int64_t c, int splits, int64_t share) {
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < splits; ++k) {
+    const float4 e = *(const float4*)(z + k * share + c);
+    s.x += e.x; s.y += e.y; s.z += e.z; s.w += e.w;
+  }
+  return s;
+}
+
+// One token's lse and loss from shares of its logits, [splits][T][ld].  (16000
+// columns: with 256 threads a token 7 us more than with 1024.)
+__global__ __launch_bounds__(1024) void xent_few_stats_kernel(const float* __restrict__ z, int splits, int T,
+                                                             int64_t V, int64_t ld,
+                                                             const int64_t* __restrict__ target,
+                                                             int64_t ignore_index, float* __restrict__ loss,
+                                                             float* __restrict__ lse) {
+  __shared__ float2 red[16];
+  const int t = blockIdx.x;
+  const float* const row = z + t * ld;
+  const int64_t share = T * ld;
+  float m = -INFINITY, s = 0.f;
+  for (int64_t c = 4 * threadIdx.x; c < V; c += 4 * blockDim.x) {
+    const float4 e = sum_shares(row, c, splits, share);
+    join_sums(m, s, e.x, 1.f);
+    if (c + 1 < V) join_sums(m, s, e.y, 1.f);
+    if (c + 2 < V) join_sums(m, s, e.z, 1.f);
+    if (c + 3 < V) join_sums(m, s, e.w, 1.f);
+  }
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) join_sums(m, s, __shfl_xor(m, x), __shfl_xor(s, x));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.x) return;
+  for (int i = 1; i < (int)blockDim.x / 64; ++i) join_sums(m, s, red[i].x, red[i].y);
+  const float l = (m == -INFINITY ? 0.f : m) + __logf(s);
+  lse[t] = l;
+  const int64_t y = target[t];
+  float d = 0.f;
+  if (y != ignore_index) {
+    d = __builtin_nanf("");
+    if (y >= 0 && y < V) {
+      float own = 0.f;
+      for (int k = 0; k < splits; ++k) own += row[k * share + y];
+      d = l - own;
+    }
+  }
+  loss[t] = d;
+}
+
+// G from shares of the logits, [splits][T][ld]; zeros past T and V.
+__global__ __launch_bounds__(256) void xent_few_grad_kernel(const float* __restrict__ z, int splits, int T, int V,
+                                                            int ld, const float2* __restrict__ row,
+                                                            const int* __restrict__ local_target, int v0,
+                                                            uint16_t* __restrict__ g, int64_t ld_g) {
+  const int t = blockIdx.x, c = 4 * (blockIdx.y * 256 + threadIdx.x);
+  if (c >= ld) return;
+  uint2 w = make_uint2(0, 0);
+  const float2 info = t < T ? row[t] : make_float2(0.f, 0.f);
+  if (info.y != 0.f) {
+    const float4 e = sum_shares(z + (int64_t)t * ld, c, splits, (int64_t)T * ld);
+    float p[4] = {e.x, e.y, e.z, e.w};
+    const int y = local_target[t] - v0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] = __builtin_amdgcn_exp2f((p[i] - info.x) * kLog2e);
+      if (c + i == y) p[i] -= 1.f;
+      p[i] = c + i < V ? p[i] * info.y : 0.f;
+    }
+    w = make_uint2(pack_bf16x2_rne(p[0], p[1]), pack_bf16x2_rne(p[2], p[3]));
+  }
+  *(uint2*)(g + t * ld_g + c) = w;
+}
+
 // Zeros in columns [c0, c1) of bf16 rows: one row and 2048 columns a workgroup.
 __global__ __launch_bounds__(256) void zero_columns_kernel(uint16_t* out, int64_t ld, int64_t rows, int64_t c0,
                                                            int64_t c1) {
@@ -763,6 +842,8 @@ __global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ 
   }
 }
 
+
+int64_t pad64(int64_t n) { return (n + 63) & ~(int64_t)63; }
 
 // Large tiles for more than 128 rows, once they (times the splits of the
 // contraction) fill half the chip's compute units; else 64-row tiles.
@@ -827,6 +908,28 @@ hipError_t run_gemm(XentGemm p, int splits, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Shares of the logits' contraction, where their tiles leave half the chip idle
+// and it is long: a slab takes such a tile about 0.55 us, whether three or six
+// stages are on their way.  The fp32 shares, at least 8 slabs each, are then
+// summed by kernels of their own.  (12 tokens, 6853 x 3840: forward 38 to 24 us;
+// 12 tokens, 3426 x 4224: step 101 to 58 us; 64 tokens, 16000 x 4096: 141 to 127
+// us.  With 16 slabs no gain: 12 tokens, 6853 x 1024 16 us either way.)
+int logit_splits(int64_t T, int64_t V, int64_t K) {
+  const TileShape tile = logit_tiles(T, V);
+  const int64_t tiles = ((T + 63) / 64) * ((V + 127) / 128), slabs = K / 64;
+  if (tile.rows != 64 || tile.cols != 128 || tiles > kCus / 2 || slabs < 24) return 1;
+  return (int)(kCus / tiles < slabs / 8 ? kCus / tiles : slabs / 8);
+}
+
+hipError_t run_logit_shares(XentGemm p, int splits, float* z, hipStream_t stream) {
+  p.M = p.a_rows;
+  p.N = (int)pad64(p.b_rows);
+  p.acc = z;
+  const dim3 grid((unsigned)lay_out(&p, {64, 128}, splits, 1));
+  hipLaunchKernelGGL((xent_gemm_kernel<64, 128, 1, 4, 3, kAcc, false, false>), grid, dim3(256), 0, stream, p);
+  return hipGetLastError();
+}
+
 // dH's share of a piece and the piece's dW, in one launch where both take the
 // same tiles: one launch fewer (128 tokens, 2048 x 512: 42.6 to 38 us a step),
 // and dW's tiles fill the compute units that dH's leave (1777 tokens, 50001 x
@@ -848,7 +951,6 @@ hipError_t run_pair(XentGemm h, int splits, XentGemm w, hipStream_t stream) {
   return hipGetLastError();
 }
 
-int64_t pad64(int64_t n) { return (n + 63) & ~(int64_t)63; }
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Vocabulary columns per piece: whole tiles, as many as keep G at 128 MB, so
@@ -864,14 +966,21 @@ struct XentLayout {
   int64_t part_tiles;          // vocabulary tiles of the statistics
   int64_t tp, piece, ld_g;     // tokens in whole slabs; columns of a piece; G's row
   int splits;                  // of dH's contraction over the piece
-  size_t part, logit, row, target, tokens, g, acc, total;
+  int z_splits;                // of the logits'; 1: their tiles take all of it
+  size_t z, part, logit, row, target, tokens, g, acc, total;
 };
 
 XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
   XentLayout L = {};
   size_t off = 0;
   auto take = [&](size_t bytes) { const size_t at = off; off += pad256(bytes); return at; };
+  L.z_splits = logit_splits(T, V, K);
+  if (L.z_splits > 1) L.z = take((size_t)L.z_splits * T * pad64(V) * 4);   // one piece: V columns
   if (!backward) {
+    if (L.z_splits > 1) {
+      L.total = off;
+      return L;
+    }
     const int cols = logit_tiles(T, V).cols;
     L.part_tiles = (V + cols - 1) / cols;
     L.part = take((size_t)L.part_tiles * T * sizeof(float2));
@@ -934,8 +1043,15 @@ hipError_t launch_xent_fwd(const XentArgs& p, void* ws, hipStream_t stream) {
   g.part = (float2*)(base + L.part);
   g.target = p.target;
   g.target_logit = (float*)(base + L.logit);
-  hipError_t e = run_gemm<kStats>(g, 1, stream);
-  if (e != hipSuccess) return e;
+  hipError_t e;
+  if (L.z_splits > 1) {
+    float* const z = (float*)(base + L.z);
+    if ((e = run_logit_shares(g, L.z_splits, z, stream)) != hipSuccess) return e;
+    hipLaunchKernelGGL(xent_few_stats_kernel, dim3((unsigned)p.T), dim3(p.V > 1024 ? 1024 : 256), 0, stream, z, L.z_splits, (int)p.T, p.V,
+                       pad64(p.V), p.target, p.ignore_index, p.loss, p.lse);
+    return hipGetLastError();
+  }
+  if ((e = run_gemm<kStats>(g, 1, stream)) != hipSuccess) return e;
   hipLaunchKernelGGL(xent_join_kernel, dim3((unsigned)((p.T + 15) / 16)), dim3(1024), 0, stream, g.part,
                      (int)L.part_tiles, (int)p.T, p.V, g.target_logit, p.target, p.ignore_index,
                      p.loss, p.lse);
@@ -966,7 +1082,16 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
     z.a_rows = (int)p.T; z.b_rows = (int)nv;
     z.row = row; z.local_target = target; z.v0 = (int)v0;
     z.out = g; z.ldo = L.ld_g;
-    if ((e = run_gemm<kGrad>(z, 1, stream)) != hipSuccess) return e;
+    if (L.z_splits > 1) {
+      float* const shares = (float*)(base + L.z);
+      if ((e = run_logit_shares(z, L.z_splits, shares, stream)) != hipSuccess) return e;
+      hipLaunchKernelGGL(xent_few_grad_kernel, dim3((unsigned)L.tp, (unsigned)((z.N + 1023) / 1024)), dim3(256), 0,
+                         stream, shares, L.z_splits, (int)p.T, (int)nv, z.N, row, target, (int)v0, g, L.ld_g);
+      e = hipGetLastError();
+    } else {
+      e = run_gemm<kGrad>(z, 1, stream);
+    }
+    if (e != hipSuccess) return e;
     XentGemm dw = {};   // dW[v, k] = sum_t G[t, v] H[t, k]
     dw.a = (const uint8_t*)g; dw.lda = L.ld_g * 2; dw.a_rows = (int)L.tp;
     dw.b = (const uint8_t*)p.h; dw.ldb = p.ld_h * 2; dw.b_rows = (int)p.T;

@@ -86,6 +86,21 @@ def test_forward_backward(gpu, shape):
     _check(h, w, target, dloss, loss, lse, dh, dw)
 
 
+@pytest.mark.parametrize("shape", [(1, 500, 1600), (3, 1001, 4096), (64, 4097, 1536), (70, 129, 2112), (1000, 65, 1600)])
+def test_long_contractions_of_few_tiles(gpu, shape):
+    """Logits whose contraction is shared out; with targets that do not count."""
+    h, w, target, dloss = _case(*shape, seed=sum(shape))
+    target[0 if shape[0] > 1 else 1:1] = shape[1] + 5
+    target[2::5] = IGNORE
+    args = [t.to(gpu) for t in (h, w, target)]
+    say(f"linear_xent shares {shape}")
+    loss, lse = fp8.linear_xent_fwd(*args)
+    dh, dw = fp8.linear_xent_bwd(dloss.to(gpu), *args, lse)
+    _check(h, w, target, dloss, loss, lse, dh, dw)
+    again = fp8.linear_xent_bwd(dloss.to(gpu), *args, lse)
+    assert torch.equal(fp8.linear_xent_fwd(*args)[1], lse) and torch.equal(again[0], dh) and torch.equal(again[1], dw)
+
+
 def test_strided_operands_and_single_gradients(gpu):
     """Column slices of wider buffers; a gradient left out changes nothing."""
     T, V, K = 200, 1500, 192
@@ -155,7 +170,7 @@ def test_masked_token_with_infinities(gpu):
     assert not dh[7].any() and torch.equal(dh, want)
 
 
-@pytest.mark.parametrize("shape", [(40, 500, 64), (130, 1000, 192), (1025, 7777, 256)])
+@pytest.mark.parametrize("shape", [(40, 500, 64), (40, 500, 1600), (130, 1000, 192), (1025, 7777, 256)])
 def test_masked_infinities_stay_out_of_dw(gpu, shape):
     """Infinities and NaN in tokens that have no gradient (ignored, outside the
     vocabulary, weight 0), the last one among them: dw and dh are those of
