@@ -709,15 +709,17 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, beta1=0.9, bet
         if not kinds[-1] <= set(dtypes):
             raise ValueError(f"{name} must be of {' or '.join(str(d) for d in dtypes)}")
     zeros = [0] * n
+    blocks = [(_cdiv(m, 128),) for m in numels] if eight else None
     scales = []
     for ts in (exp_avg_scales, root_scales):
         if ts is None:
             scales.append(zeros)
             continue
-        if any([t.get_device() != index for t in ts]):
+        if {t.get_device() for t in ts} != here:
             raise ValueError("fp8bw ops take CUDA (HIP) tensors on one device")
-        for t, m in zip(ts, numels):
-            _vector(t, _cdiv(m, 128), torch.float32, "scales")
+        if ([t.shape for t in ts] != blocks or {t.dtype for t in ts} != {torch.float32}
+                or {t.is_contiguous() for t in ts} != yes):
+            raise ValueError("scales must be contiguous float32 vectors, one element per 128 of the state")
         scales.append([t.data_ptr() for t in ts])
     if masters is None:
         master_ptrs = zeros
