@@ -86,6 +86,9 @@ PROTOTYPES = {
     "fp8bw_linear_xent_bwd": (c_int, [c_ptr, c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_i64, c_ptr,
                                       c_i64, c_i64, c_i64, c_ptr, c_i64, c_ptr, c_i64, c_ptr,
                                       c_size, c_ptr]),
+    "fp8bw_linear_xent_bwd_loss": (c_int, [c_ptr, c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_i64, c_ptr,
+                                           c_ptr, c_i64, c_i64, c_i64, c_ptr, c_i64, c_ptr, c_i64,
+                                           c_ptr, c_size, c_ptr]),
     "fp8bw_adamw_step": (c_int, [ctypes.POINTER(AdamwTensor), c_int, c_int, c_i64, c_f64, c_f64,
                                  c_f64, c_f64, c_f64, c_ptr, c_int, c_u64, c_ptr]),
 }

@@ -168,6 +168,7 @@ struct XentArgs {
   float* loss;                        // [T] (forward)
   float* lse;                         // [T] (forward writes, backward reads)
   const float* dloss;                 // [T] (backward)
+  const float* nll;                   // [T] the forward's losses or nullptr (backward)
   void* dh; int64_t ld_dh;            // bf16 [T, K] or nullptr
   void* dw; int64_t ld_dw;            // bf16 [V, K] or nullptr
 };

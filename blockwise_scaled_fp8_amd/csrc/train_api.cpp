@@ -221,6 +221,15 @@ FP8BW_API int fp8bw_linear_xent_bwd(const float* dloss, const void* h, int64_t l
                                     const float* lse, int64_t T, int64_t V, int64_t K, void* dh,
                                     int64_t ld_dh, void* dw, int64_t ld_dw, void* ws, size_t ws_bytes,
                                     void* stream) {
+  return fp8bw_linear_xent_bwd_loss(dloss, h, ld_h, w, ld_w, target, ignore_index, lse, nullptr, T, V, K, dh,
+                                    ld_dh, dw, ld_dw, ws, ws_bytes, stream);
+}
+
+FP8BW_API int fp8bw_linear_xent_bwd_loss(const float* dloss, const void* h, int64_t ld_h, const void* w,
+                                         int64_t ld_w, const int64_t* target, int64_t ignore_index,
+                                         const float* lse, const float* loss, int64_t T, int64_t V,
+                                         int64_t K, void* dh, int64_t ld_dh, void* dw, int64_t ld_dw,
+                                         void* ws, size_t ws_bytes, void* stream) {
   int st = check_xent(h, ld_h, w, ld_w, target, T, V, K);
   if (st != FP8BW_OK) return st;
   if (dw && V > 0 && (st = check_bf16(dw, V, K, ld_dw, "dw")) != FP8BW_OK) return st;
@@ -232,6 +241,7 @@ FP8BW_API int fp8bw_linear_xent_bwd(const float* dloss, const void* h, int64_t l
   if (dh && (st = check_bf16(dh, T, K, ld_dh, "dh")) != FP8BW_OK) return st;
   if ((st = check_f32(dloss, "dloss")) != FP8BW_OK) return st;
   if ((st = check_f32(lse, "lse")) != FP8BW_OK) return st;
+  if (loss && (st = check_f32(loss, "loss")) != FP8BW_OK) return st;
   if (!dh && !dw) return ok();
   if ((st = check_ws(ws, ws_bytes, fp8bw_linear_xent_ws_bytes(T, V, K, 1))) != FP8BW_OK) return st;
   fp8bw::XentArgs p = {};
@@ -241,6 +251,7 @@ FP8BW_API int fp8bw_linear_xent_bwd(const float* dloss, const void* h, int64_t l
   p.target = target; p.ignore_index = ignore_index;
   p.lse = const_cast<float*>(lse);
   p.dloss = dloss;
+  p.nll = loss;
   p.dh = dh; p.ld_dh = T > 1 ? ld_dh : K;
   p.dw = dw; p.ld_dw = V > 1 ? ld_dw : K;
   return hip_status(fp8bw::launch_xent_bwd(p, ws, (hipStream_t)stream), "fp8bw_linear_xent_bwd");

@@ -7,8 +7,13 @@
 //   dH = G W,   dW = G^T H
 //
 // Forward: one product whose epilogue keeps, per token and tile of 256
-// vocabulary columns, the maximum and the sum of exponentials over it; a
-// second kernel joins the tiles.  Backward: the vocabulary is taken in
+// vocabulary columns, the maximum and the sum of exponentials over the tile's
+// columns but the target; a second kernel joins the tiles.  The target's share
+// of the sum is added last: loss = log(1 + sum_{v != target} exp(z_v -
+// z_target)), so that a token whose target has almost all of the probability
+// keeps its loss, 1 - p to first order, to fp32's relative precision, where lse
+// - z_target would leave the rounding of two large numbers.  The backward takes
+// the target's entry of G, p - 1, from that loss as expm1(-loss).  Backward: the vocabulary is taken in
 // pieces; per piece the logits are made again, their epilogue turns them into
 // G (bf16), and two products add G's share to dH and finish the piece's rows
 // of dW.  The workspace holds one piece, whatever the vocabulary.
@@ -80,6 +85,7 @@ struct XentGemm {
   // kGrad
   const float2* row;               // [M], kOut [contraction]: (lse, dloss / scale)
   const int* local_target;         // [M] target column of the whole vocabulary, or -1
+  const float* target_grad;        // [M] p - 1 of the target, or nullptr: from lse
   int v0;                          // first vocabulary column of this piece
   // outputs
   void* out; int64_t ldo;          // kGrad, kOut: bf16 elements
@@ -479,8 +485,10 @@ __device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t
             for (int j = 0; j < TN; ++j)
 #pragma unroll
               for (int v = 0; v < 4; ++v)
-                if (16 * j + 4 * fq + v == tgt[i] && r < p.M)
-                  p.target_logit[r] = acc[i][j][v];
+                if (16 * j + 4 * fq + v == tgt[i]) {
+                  if (r < p.M) p.target_logit[r] = acc[i][j][v];
+                  acc[i][j][v] = -INFINITY;   // joined to the others last
+                }
           }
           float m = -INFINITY;
 #pragma unroll
@@ -556,7 +564,8 @@ __device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t
             for (int j = 0; j < TN; ++j)
 #pragma unroll
               for (int v = 0; v < 4; ++v)
-                if (16 * j + 4 * fq + v == tgt[i]) acc[i][j][v] -= 1.f;
+                if (16 * j + 4 * fq + v == tgt[i])
+                  acc[i][j][v] = p.target_grad ? p.target_grad[min(row0 + 16 * i, p.a_rows - 1)] : acc[i][j][v] - 1.f;
           }
         }
         const float f = EPI == kGrad ? info[i].y : scale;
@@ -675,6 +684,28 @@ __device__ __forceinline__ void join_sums(float& m, float& s, float m2, float s2
   m = top;
 }
 
+// lse and loss of a token from the maximum m and the sum of exponentials s of
+// the columns beside its target (of all, where the target counts not or is
+// outside the vocabulary), and the target's logit z.
+__device__ __forceinline__ void token_loss(float m, float s, int64_t y, int64_t V, int64_t ignore_index, float z,
+                                           float* lse, float* loss) {
+  const bool known = y >= 0 && y < V;
+  float l, d;
+  if (known && fabsf(z) < INFINITY) {
+    // log of the others' sum over the target's exponential
+    const float gap = s == 0.f ? -INFINITY : (m - z) + logf(s);
+    const float tail = log1pf(expf(-fabsf(gap)));
+    d = gap > 0.f ? gap + tail : tail;
+    l = gap > 0.f ? (m + logf(s)) + tail : z + tail;
+  } else {
+    if (known) join_sums(m, s, z, 1.f);
+    l = (m == -INFINITY ? 0.f : m) + logf(s);
+    d = known ? l - z : __builtin_nanf("");
+  }
+  *lse = l;
+  *loss = y == ignore_index ? 0.f : d;
+}
+
 // Joins the tiles' (max, sum) of 16 tokens: 64 threads a token over the
 // tiles, then over the threads in a fixed order.
 __global__ __launch_bounds__(1024) void xent_join_kernel(const float2* __restrict__ part, int tiles,
@@ -701,24 +732,22 @@ __global__ __launch_bounds__(1024) void xent_join_kernel(const float2* __restric
   if (g == 0 && t < T) {
 #pragma unroll
     for (int i = 1; i < 16; ++i) join_sums(m, s, red[i][c].x, red[i][c].y);
-    const float base = m == -INFINITY ? 0.f : m;
-    const float l = base + __logf(s);
-    lse[t] = l;
     const int64_t y = target[t];
-    float d = 0.f;
-    if (y != ignore_index) d = (y >= 0 && y < V) ? l - target_logit[t] : __builtin_nanf("");
-    loss[t] = d;
+    const float z = y >= 0 && y < V ? target_logit[t] : 0.f;
+    token_loss(m, s, y, V, ignore_index, z, lse + t, loss + t);
   }
 }
 
 // scale = max |dloss| over the tokens that count, and per token (lse, dloss /
-// scale) and the target column; ignored and out-of-range targets get weight 0.
+// scale), the target column and, with the losses, the target's p - 1; ignored
+// and out-of-range targets get weight 0.
 // An infinity or NaN in a token's row of H makes every one of its logits
 // infinite or NaN, and so its lse.
 __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, const int64_t* __restrict__ target,
                                                          int64_t ignore_index, const float* __restrict__ dloss,
-                                                         const float* __restrict__ lse, float2* __restrict__ row,
-                                                         int* __restrict__ local_target, XentTokens* __restrict__ tokens) {
+                                                         const float* __restrict__ lse, const float* __restrict__ loss,
+                                                         float2* __restrict__ row, int* __restrict__ local_target,
+                                                         float* __restrict__ target_grad, XentTokens* __restrict__ tokens) {
   __shared__ float red[16];
   float m = 0.f;
   for (int t = threadIdx.x; t < T; t += 1024) {
@@ -737,6 +766,7 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, const
     const float2 r = make_float2(lse[t], counts && dloss[t] != 0.f ? dloss[t] / m : 0.f);
     row[t] = r;
     local_target[t] = counts ? (int)y : -1;
+    if (loss) target_grad[t] = expm1f(-loss[t]);
     masked |= r.y == 0.f && !(fabsf(r.x) < INFINITY);
   }
   const int any = __syncthreads_or(masked);
@@ -764,13 +794,14 @@ __global__ __launch_bounds__(1024) void xent_few_stats_kernel(const float* __res
   const int t = blockIdx.x;
   const float* const row = z + t * ld;
   const int64_t share = T * ld;
+  const int64_t y = target[t];
   float m = -INFINITY, s = 0.f;
   for (int64_t c = 4 * threadIdx.x; c < V; c += 4 * blockDim.x) {
     const float4 e = sum_shares(row, c, splits, share);
-    join_sums(m, s, e.x, 1.f);
-    if (c + 1 < V) join_sums(m, s, e.y, 1.f);
-    if (c + 2 < V) join_sums(m, s, e.z, 1.f);
-    if (c + 3 < V) join_sums(m, s, e.w, 1.f);
+    if (c != y) join_sums(m, s, e.x, 1.f);
+    if (c + 1 < V && c + 1 != y) join_sums(m, s, e.y, 1.f);
+    if (c + 2 < V && c + 2 != y) join_sums(m, s, e.z, 1.f);
+    if (c + 3 < V && c + 3 != y) join_sums(m, s, e.w, 1.f);
   }
 #pragma unroll
   for (int x = 1; x < 64; x *= 2) join_sums(m, s, __shfl_xor(m, x), __shfl_xor(s, x));
@@ -778,25 +809,17 @@ __global__ __launch_bounds__(1024) void xent_few_stats_kernel(const float* __res
   __syncthreads();
   if (threadIdx.x) return;
   for (int i = 1; i < (int)blockDim.x / 64; ++i) join_sums(m, s, red[i].x, red[i].y);
-  const float l = (m == -INFINITY ? 0.f : m) + __logf(s);
-  lse[t] = l;
-  const int64_t y = target[t];
-  float d = 0.f;
-  if (y != ignore_index) {
-    d = __builtin_nanf("");
-    if (y >= 0 && y < V) {
-      float own = 0.f;
-      for (int k = 0; k < splits; ++k) own += row[k * share + y];
-      d = l - own;
-    }
-  }
-  loss[t] = d;
+  float own = 0.f;
+  if (y >= 0 && y < V)
+    for (int k = 0; k < splits; ++k) own += row[k * share + y];
+  token_loss(m, s, y, V, ignore_index, own, lse + t, loss + t);
 }
 
 // G from shares of the logits, [splits][T][ld]; zeros past T and V.
 __global__ __launch_bounds__(256) void xent_few_grad_kernel(const float* __restrict__ z, int splits, int T, int V,
                                                             int ld, const float2* __restrict__ row,
-                                                            const int* __restrict__ local_target, int v0,
+                                                            const int* __restrict__ local_target,
+                                                            const float* __restrict__ target_grad, int v0,
                                                             uint16_t* __restrict__ g, int64_t ld_g) {
   const int t = blockIdx.x, c = 4 * (blockIdx.y * 256 + threadIdx.x);
   if (c >= ld) return;
@@ -809,7 +832,7 @@ __global__ __launch_bounds__(256) void xent_few_grad_kernel(const float* __restr
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       p[i] = __builtin_amdgcn_exp2f((p[i] - info.x) * kLog2e);
-      if (c + i == y) p[i] -= 1.f;
+      if (c + i == y) p[i] = target_grad ? target_grad[t] : p[i] - 1.f;
       p[i] = c + i < V ? p[i] * info.y : 0.f;
     }
     w = make_uint2(pack_bf16x2_rne(p[0], p[1]), pack_bf16x2_rne(p[2], p[3]));
@@ -967,7 +990,7 @@ struct XentLayout {
   int64_t tp, piece, ld_g;     // tokens in whole slabs; columns of a piece; G's row
   int splits;                  // of dH's contraction over the piece
   int z_splits;                // of the logits'; 1: their tiles take all of it
-  size_t z, part, logit, row, target, tokens, g, acc, total;
+  size_t z, part, logit, row, target, target_grad, tokens, g, acc, total;
 };
 
 XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
@@ -1014,6 +1037,7 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
   }
   L.row = take((size_t)T * sizeof(float2));
   L.target = take((size_t)T * 4);
+  L.target_grad = take((size_t)T * 4);
   L.tokens = take(sizeof(XentTokens));
   L.g = take((size_t)L.tp * L.ld_g * 2);
   L.acc = take((size_t)L.splits * T * K * 4);
@@ -1063,11 +1087,12 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
   uint8_t* const base = (uint8_t*)ws;
   float2* const row = (float2*)(base + L.row);
   int* const target = (int*)(base + L.target);
+  float* const target_grad = p.nll ? (float*)(base + L.target_grad) : nullptr;
   XentTokens* const tokens = (XentTokens*)(base + L.tokens);
   uint16_t* const g = (uint16_t*)(base + L.g);
   float* const acc = (float*)(base + L.acc);
   hipLaunchKernelGGL(xent_rows_kernel, dim3(1), dim3(1024), 0, stream, (int)p.T, p.V, p.target,
-                     p.ignore_index, p.dloss, p.lse, row, target, tokens);
+                     p.ignore_index, p.dloss, p.lse, p.nll, row, target, target_grad, tokens);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   for (int64_t v0 = 0; v0 < p.V; v0 += L.piece) {
@@ -1080,13 +1105,14 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
     // no gradient: zeros.
     z.M = (int)L.tp; z.N = (int)pad64(nv); z.kblocks = (int)(p.K / 64);
     z.a_rows = (int)p.T; z.b_rows = (int)nv;
-    z.row = row; z.local_target = target; z.v0 = (int)v0;
+    z.row = row; z.local_target = target; z.target_grad = target_grad; z.v0 = (int)v0;
     z.out = g; z.ldo = L.ld_g;
     if (L.z_splits > 1) {
       float* const shares = (float*)(base + L.z);
       if ((e = run_logit_shares(z, L.z_splits, shares, stream)) != hipSuccess) return e;
       hipLaunchKernelGGL(xent_few_grad_kernel, dim3((unsigned)L.tp, (unsigned)((z.N + 1023) / 1024)), dim3(256), 0,
-                         stream, shares, L.z_splits, (int)p.T, (int)nv, z.N, row, target, (int)v0, g, L.ld_g);
+                         stream, shares, L.z_splits, (int)p.T, (int)nv, z.N, row, target, target_grad, (int)v0, g,
+                         L.ld_g);
       e = hipGetLastError();
     } else {
       e = run_gemm<kGrad>(z, 1, stream);

@@ -636,22 +636,29 @@ def linear_xent_fwd(h, w, target, ignore_index=-100):
 
 
 @_on_tensor_device
-def linear_xent_bwd(dloss, h, w, target, lse, ignore_index=-100, need_dh=True, need_dw=True):
+def linear_xent_bwd(dloss, h, w, target, lse, ignore_index=-100, need_dh=True, need_dw=True,
+                    loss=None):
     """(dh, dw), bf16, of linear_xent_fwd from dloss fp32 [T], one weight per
-    token's loss, and the forward's lse; a gradient not needed is None."""
+    token's loss, and the forward's lse; a gradient not needed is None.
+
+    loss: the forward's losses, from which the target's entry of the softmax's
+    gradient, p - 1, comes to fp32's relative precision; without them it is off
+    by the rounding of lse, which is all of it for very confident tokens."""
     lib = load_library()
     T, V, K = _check_xent(h, w, target)
     _need_cuda(dloss, lse)
     _vector(dloss, T, torch.float32, "dloss")
     _vector(lse, T, torch.float32, "lse")
+    if loss is not None:
+        _vector(loss, T, torch.float32, "loss")
     dh = torch.empty((T, K), dtype=torch.bfloat16, device=h.device) if need_dh else None
     dw = torch.empty((V, K), dtype=torch.bfloat16, device=h.device) if need_dw else None
     nws = lib.fp8bw_linear_xent_ws_bytes(T, V, K, 1)
     ws = torch.empty(max(nws, 1), dtype=torch.uint8, device=h.device)
-    check(lib.fp8bw_linear_xent_bwd(dloss.data_ptr(), h.data_ptr(), h.stride(0), w.data_ptr(),
-                                    w.stride(0), target.data_ptr(), int(ignore_index),
-                                    lse.data_ptr(), T, V, K, _ptr(dh), _ld(dh), _ptr(dw), _ld(dw),
-                                    ws.data_ptr(), nws, _stream(h)))
+    check(lib.fp8bw_linear_xent_bwd_loss(dloss.data_ptr(), h.data_ptr(), h.stride(0), w.data_ptr(),
+                                         w.stride(0), target.data_ptr(), int(ignore_index),
+                                         lse.data_ptr(), _ptr(loss), T, V, K, _ptr(dh), _ld(dh),
+                                         _ptr(dw), _ld(dw), ws.data_ptr(), nws, _stream(h)))
     return dh, dw
 
 

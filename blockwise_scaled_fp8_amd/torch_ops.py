@@ -426,34 +426,36 @@ def _linear_xent_fwd_fake(h, w, target, ignore_index):
 
 @torch.library.custom_op("fp8bw::linear_xent_bwd", mutates_args=())
 def linear_xent_bwd(dloss: torch.Tensor, h: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
-                    lse: torch.Tensor, ignore_index: int, need_dh: bool,
-                    need_dw: bool) -> tuple[torch.Tensor, torch.Tensor]:
+                    lse: torch.Tensor, ignore_index: int, need_dh: bool, need_dw: bool,
+                    loss: Optional[torch.Tensor] = None) -> tuple[torch.Tensor, torch.Tensor]:
     """(dh, dw) of ops.linear_xent_bwd; one not asked for comes back empty."""
-    dh, dw = ops.linear_xent_bwd(dloss, h, w, target, lse, ignore_index, need_dh, need_dw)
+    dh, dw = ops.linear_xent_bwd(dloss, h, w, target, lse, ignore_index, need_dh, need_dw, loss)
     return (_empty(h) if dh is None else dh), (_empty(w) if dw is None else dw)
 
 
 @linear_xent_bwd.register_fake
-def _linear_xent_bwd_fake(dloss, h, w, target, lse, ignore_index, need_dh, need_dw):
+def _linear_xent_bwd_fake(dloss, h, w, target, lse, ignore_index, need_dh, need_dw, loss=None):
     return (h.new_empty(h.shape) if need_dh else _empty(h),
             w.new_empty(w.shape) if need_dw else _empty(w))
 
 
 class _LinearXent(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, h, w, target, ignore_index):
+    def forward(ctx, h, w, target, ignore_index, exposed):
         loss, lse = torch.ops.fp8bw.linear_xent_fwd(h, w, target, ignore_index)
         ctx.ignore_index = ignore_index
-        ctx.save_for_backward(h, w, target, lse)
+        # the backward's own losses, where the caller gets these and may change them
+        ctx.save_for_backward(h, w, target, lse,
+                              loss.clone() if exposed and any(ctx.needs_input_grad) else loss)
         return loss
 
     @staticmethod
     def backward(ctx, dloss):
-        h, w, target, lse = ctx.saved_tensors
+        h, w, target, lse, loss = ctx.saved_tensors
         need = ctx.needs_input_grad[:2]
         dh, dw = torch.ops.fp8bw.linear_xent_bwd(dloss.contiguous(), h, w, target, lse,
-                                                 ctx.ignore_index, *need)
-        return (dh if need[0] else None), (dw if need[1] else None), None, None
+                                                 ctx.ignore_index, *need, loss)
+        return (dh if need[0] else None), (dw if need[1] else None), None, None, None
 
 
 def linear_cross_entropy(h, w, target, ignore_index=-100, reduction="mean"):
@@ -464,7 +466,7 @@ def linear_cross_entropy(h, w, target, ignore_index=-100, reduction="mean"):
     if reduction not in ("mean", "sum", "none"):
         raise ValueError(f"unknown reduction {reduction!r}")
     flat = target.reshape(-1).contiguous()
-    loss = _LinearXent.apply(h.reshape(-1, h.shape[-1]), w, flat, ignore_index)
+    loss = _LinearXent.apply(h.reshape(-1, h.shape[-1]), w, flat, ignore_index, reduction == "none")
     if reduction == "none":
         return loss.reshape(target.shape)
     if reduction == "sum":

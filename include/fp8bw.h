@@ -451,7 +451,7 @@ int fp8bw_rms_norm_bwd(const void* dy, int64_t ld_dy, const void* s, int64_t ld_
                        void* dweight, void* ws, size_t ws_bytes, void* stream);
 
 /*
- * fp8bw_linear_xent_fwd / _bwd -- softmax cross entropy of a linear head over
+ * fp8bw_linear_xent_fwd / _bwd / _bwd_loss -- softmax cross entropy of a linear head over
  * a large vocabulary, logits z = h . w^T, without keeping the logits:
  *
  *   lse[t]  = log sum_v exp(z[t, v]);  loss[t] = lse[t] - z[t, target[t]]
@@ -464,7 +464,13 @@ int fp8bw_rms_norm_bwd(const void* dy, int64_t ld_dy, const void* s, int64_t ld_
  *            loss and no gradient.  What the rows of h of tokens without a
  *            gradient (those, and dloss 0) hold reaches neither dh nor dw.
  *   loss, lse, dloss  device fp32 [T]; one loss per token, so that a caller's
- *            mean, sum or weights are dloss.
+ *            mean, sum or weights are dloss.  The loss is formed as log(1 + sum_{v !=
+ *            target} exp(z[t, v] - z[t, target])): its relative error is a few units
+ *            of fp32 beside the logits', also where it is far below a rounding of lse.
+ *            fp8bw_linear_xent_bwd_loss takes the forward's losses (or NULL) and forms
+ *            the target's entry of G, p - 1, as expm1(-loss).  From lse alone
+ *            (fp8bw_linear_xent_bwd, or loss NULL) that entry is off by lse's rounding,
+ *            about 2^-24 |lse|, which is all of it for a token that confident.
  *   dh, dw   device bf16 [T, K] (ld_dh) and [V, K] (ld_dw); either may be NULL.
  *   The backward takes the vocabulary in pieces: each piece's logits are made
  *   again and become its part of G (bf16) in the workspace, whose size does
@@ -487,6 +493,11 @@ int fp8bw_linear_xent_bwd(const float* dloss, const void* h, int64_t ld_h, const
                           const float* lse, int64_t T, int64_t V, int64_t K, void* dh,
                           int64_t ld_dh, void* dw, int64_t ld_dw, void* ws, size_t ws_bytes,
                           void* stream);
+int fp8bw_linear_xent_bwd_loss(const float* dloss, const void* h, int64_t ld_h, const void* w,
+                               int64_t ld_w, const int64_t* target, int64_t ignore_index,
+                               const float* lse, const float* loss, int64_t T, int64_t V, int64_t K,
+                               void* dh, int64_t ld_dh, void* dw, int64_t ld_dw, void* ws,
+                               size_t ws_bytes, void* stream);
 
 /*
  * fp8bw_adamw_step -- one AdamW step over many tensors, in place:
