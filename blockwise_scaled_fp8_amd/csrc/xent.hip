@@ -31,6 +31,14 @@
 // It is formed with dloss divided by its largest magnitude, which the
 // epilogues multiply back in fp32: with the usual equal weights of a mean
 // loss nothing but G's own rounding remains.
+//
+// A row of G sums to zero, so what all rows of W share cancels in dH.  The
+// rounded G's rows do not: their sums (fp32, from the epilogue that rounds
+// them) times the target's row of W are taken out of dH in the end, which
+// makes dH[t] = sum_v G[t, v] (W[v] - W[target]), where only the rows'
+// differences meet G's rounding (and a target's own entry does not matter).
+// 0.9% of a step of 8192 tokens, 131072 x 4096 (25.9 to 26.1 ms); with sums
+// added up in memory by each wave 2%.
 
 #include <type_traits>
 
@@ -87,11 +95,12 @@ struct XentGemm {
   const int* local_target;         // [M] target column of the whole vocabulary, or -1
   const float* target_grad;        // [M] p - 1 of the target, or nullptr: from lse
   int v0;                          // first vocabulary column of this piece
+  float* sums;                     // [tiles_n][a_rows] sums of G's rounded rows over a tile, or nullptr
   // outputs
   void* out; int64_t ldo;          // kGrad, kOut: bf16 elements
   const XentTokens* tokens;        // kOut
   float* acc;                      // kAcc
-  int add;
+  int add;                         // acc, sums: add to what is there
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* base, int64_t bytes) {
@@ -345,6 +354,7 @@ __device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t
   constexpr int NW = WGM * WGN;
   constexpr int WM = BM / WGM, WN = BN / WGN, TM = WM / 16, TN = WN / 16;
   constexpr bool ROWS = EPI == kStats || EPI == kGrad;       // the epilogue needs its rows' targets
+  constexpr int SUM_LD = BM + 16;                            // kGrad's row sums: no bank twice in a write
   constexpr bool STAGED = !SMALL && (EPI == kGrad || EPI == kOut);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm0 = (wave / WGN) * WM, wn0 = (wave % WGN) * WN;
@@ -582,6 +592,26 @@ __device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t
         for (int j = 0; j < TN; ++j)
           w[j] = make_uint2(pack_bf16x2_rne(acc[i][j][0] * f, acc[i][j][1] * f) & keep,
                             pack_bf16x2_rne(acc[i][j][2] * f, acc[i][j][3] * f) & keep);
+        if constexpr (EPI == kGrad) {   // the lane's share of the rounded row's sum
+          float s = 0.f;
+#pragma unroll
+          for (int j = 0; j < TN; ++j) s += (bf16lo(w[j].x) + bf16hi(w[j].x)) + (bf16lo(w[j].y) + bf16hi(w[j].y));
+          ((float*)sE)[(wave % WGN * 4 + fq) * SUM_LD + wm0 + 16 * i + frow] = s;
+        }
+      };
+      // Thread `r` of the last BM joins row r's 4 WGN shares.  What an earlier
+      // piece left is read before the epilogue's work.
+      const int sum_row = (int)threadIdx.x - (64 * NW - BM);
+      float sum = 0.f;
+      float* const sum_at = p.sums + (int64_t)d.tn * p.a_rows + d.m0 + sum_row;
+      const bool sums = EPI == kGrad && p.sums && sum_row >= 0 && d.m0 + sum_row < p.a_rows;
+      if (sums && p.add) sum = *sum_at;
+      auto join = [&]() __attribute__((always_inline)) {
+        if (!sums) return;
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4 * WGN; ++k) s += ((const float*)sE)[k * SUM_LD + sum_row];
+        *sum_at = sum + s;
       };
       if constexpr (STAGED) {
         // Through LDS, so that every store writes whole lines (in the MFMA
@@ -601,6 +631,7 @@ __device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t
               *(uint2*)(rowp + 16 * (((wn0 >> 3) + 2 * j + (fq >> 1)) ^ frow) + 8 * (fq & 1)) = w[j];
           }
           __syncthreads();
+          if (h == 1) join();
           const int c = lane & 31, n = d.n0 + 8 * c;
           if (wave >= 2) {
             constexpr int PAIRS = WM / 4;   // of rows, in half of a wave's
@@ -642,19 +673,26 @@ __device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t
             }
           }
         }
+        if constexpr (EPI == kGrad) {
+          __syncthreads();
+          join();
+        }
       }
     }
     if (!more) return;
   }
 }
 
-// A kernel's stages, and its waves' row statistics (64-row kernels: in a stage).
+// A kernel's stages, and its waves' row statistics or sums (64-row kernels: in a stage).
 #define XENT_LDS(BM, BN, WGN, STAGES, EPI)                                                            \
   __shared__ __attribute__((aligned(1024))) uint8_t sA0[BM * 128], sA1[BM * 128];                     \
   __shared__ __attribute__((aligned(1024))) uint8_t sB0[BN * 128], sB1[BN * 128];                     \
   __shared__ __attribute__((aligned(1024))) uint8_t sA2[STAGES > 2 ? BM * 128 : 16];                  \
   __shared__ __attribute__((aligned(1024))) uint8_t sB2[STAGES > 2 ? BN * 128 : 16];                  \
-  __shared__ __attribute__((aligned(16))) uint8_t sums[BM > 64 && EPI == kStats ? WGN * BM * 8 : 16]; \
+  __shared__ __attribute__((aligned(16))) uint8_t sums[BM == 64        ? 16                           \
+                                                       : EPI == kStats ? WGN * BM * 8                 \
+                                                       : EPI == kGrad  ? WGN * (BM + 16) * 16         \
+                                                                       : 16];                         \
   uint8_t* const sA[kMaxStages] = {sA0, sA1, sA2};                                                    \
   uint8_t* const sB[kMaxStages] = {sB0, sB1, sB2};                                                    \
   uint8_t* const sE = BM > 64 ? sums : sA0
@@ -773,6 +811,16 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, const
   if (threadIdx.x == 0) *tokens = XentTokens{m, any, {0, 0}, {0.f, 0.f, 0.f, 0.f}};
 }
 
+// Sum over the 256 threads of a workgroup, in a fixed order; `red` is free
+// again after the caller's next barrier.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+  for (int x = 1; x < 64; x *= 2) v += __shfl_xor(v, x);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
 // Columns c .. c + 3 of the sum of `splits` shares of the logits, in order.
 __device__ __forceinline__ float4 sum_shares(const float* z, int64_t c, int splits, int64_t share) {
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -815,17 +863,19 @@ __global__ __launch_bounds__(1024) void xent_few_stats_kernel(const float* __res
   token_loss(m, s, y, V, ignore_index, own, lse + t, loss + t);
 }
 
-// G from shares of the logits, [splits][T][ld]; zeros past T and V.
+// G from shares of the logits, [splits][T][ld]; zeros past T and V.  sums: a
+// workgroup's of G's rounded row.
 __global__ __launch_bounds__(256) void xent_few_grad_kernel(const float* __restrict__ z, int splits, int T, int V,
                                                             int ld, const float2* __restrict__ row,
                                                             const int* __restrict__ local_target,
                                                             const float* __restrict__ target_grad, int v0,
-                                                            uint16_t* __restrict__ g, int64_t ld_g) {
+                                                            uint16_t* __restrict__ g, int64_t ld_g,
+                                                            float* __restrict__ sums) {
+  __shared__ float red[4];
   const int t = blockIdx.x, c = 4 * (blockIdx.y * 256 + threadIdx.x);
-  if (c >= ld) return;
   uint2 w = make_uint2(0, 0);
   const float2 info = t < T ? row[t] : make_float2(0.f, 0.f);
-  if (info.y != 0.f) {
+  if (info.y != 0.f && c < ld) {
     const float4 e = sum_shares(z + (int64_t)t * ld, c, splits, (int64_t)T * ld);
     float p[4] = {e.x, e.y, e.z, e.w};
     const int y = local_target[t] - v0;
@@ -837,7 +887,10 @@ __global__ __launch_bounds__(256) void xent_few_grad_kernel(const float* __restr
     }
     w = make_uint2(pack_bf16x2_rne(p[0], p[1]), pack_bf16x2_rne(p[2], p[3]));
   }
-  *(uint2*)(g + t * ld_g + c) = w;
+  if (c < ld) *(uint2*)(g + t * ld_g + c) = w;
+  if (!sums || t >= T) return;
+  const float s = block_sum((bf16lo(w.x) + bf16hi(w.x)) + (bf16lo(w.y) + bf16hi(w.y)), red);
+  if (threadIdx.x == 0) sums[(int64_t)blockIdx.y * T + t] = s;
 }
 
 // Zeros in columns [c0, c1) of bf16 rows: one row and 2048 columns a workgroup.
@@ -848,23 +901,36 @@ __global__ __launch_bounds__(256) void zero_columns_kernel(uint16_t* out, int64_
     for (int64_t c = c0 + (int64_t)blockIdx.y * 2048 + threadIdx.x; c < end; c += 256) out[r * ld + c] = 0;
 }
 
-// dH = scale * sum over the splits of their fp32 shares, to bf16.
+// dH = scale * (sum over the splits of their fp32 shares - the sum of the
+// token's rounded G times the target's row of W), to bf16: a token and 1024
+// columns a workgroup.
 __global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ acc, int splits, int64_t T,
                                                       int64_t K, const XentTokens* __restrict__ tokens,
+                                                      const float2* __restrict__ row,
+                                                      const int* __restrict__ target,
+                                                      const float* __restrict__ sums, int parts,
+                                                      const uint16_t* __restrict__ w, int64_t ld_w,
                                                       uint16_t* __restrict__ dh, int64_t ld_dh) {
+  __shared__ float red[2][4];
   const float f = tokens->scale;
-  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < T * K; i += (int64_t)gridDim.x * 1024) {
+  const int64_t c = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
+  int flip = 0;   // one barrier a token
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x, flip ^= 1) {
+    float part = 0.f;
+    for (int i = threadIdx.x; i < parts; i += 256) part += sums[i * T + t];
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < splits; ++k) {
-      const float4 e = *(const float4*)(acc + (int64_t)k * T * K + i);
-      s.x += e.x; s.y += e.y; s.z += e.z; s.w += e.w;
+    if (c < K) s = sum_shares(acc + t * K, c, splits, T * K);
+    const float off = block_sum(part, red[flip]);
+    if (c >= K) continue;
+    if (row[t].y != 0.f) {   // else G is zero, and W's row may be anything
+      const uint2 u = *(const uint2*)(w + target[t] * ld_w + c);
+      s.x -= off * bf16lo(u.x); s.y -= off * bf16hi(u.x);
+      s.z -= off * bf16lo(u.y); s.w -= off * bf16hi(u.y);
     }
-    const int64_t t = i / K;
-    *(uint2*)(dh + t * ld_dh + (i - t * K)) =
+    *(uint2*)(dh + t * ld_dh + c) =
         make_uint2(pack_bf16x2_rne(s.x * f, s.y * f), pack_bf16x2_rne(s.z * f, s.w * f));
   }
 }
-
 
 int64_t pad64(int64_t n) { return (n + 63) & ~(int64_t)63; }
 
@@ -914,9 +980,8 @@ int64_t lay_out(XentGemm* p, TileShape tile, int splits, int rounds) {
 }
 
 template <int EPI, bool AKM = false, bool BKM = false>
-hipError_t run_gemm(XentGemm p, int splits, hipStream_t stream) {
+hipError_t run_gemm(XentGemm p, TileShape tile, int splits, hipStream_t stream) {
   constexpr bool LOGITS = EPI == kStats || EPI == kGrad;
-  const TileShape tile = LOGITS ? logit_tiles(p.M, p.N) : gradient_tiles(p.M, p.N, splits);
   const dim3 grid((unsigned)lay_out(&p, tile, splits, kRounds));
   if (tile.rows == 256)
     hipLaunchKernelGGL((xent_gemm_kernel<256, 256, 2, 4, 2, EPI, AKM, BKM>), grid, dim3(512), 0, stream, p);
@@ -961,8 +1026,8 @@ hipError_t run_logit_shares(XentGemm p, int splits, float* z, hipStream_t stream
 hipError_t run_pair(XentGemm h, int splits, XentGemm w, hipStream_t stream) {
   const TileShape th = gradient_tiles(h.M, h.N, splits), tw = gradient_tiles(w.M, w.N, 1);
   if (th.rows != tw.rows) {
-    const hipError_t e = run_gemm<kAcc, false, true>(h, splits, stream);
-    return e != hipSuccess ? e : run_gemm<kOut, true, true>(w, 1, stream);
+    const hipError_t e = run_gemm<kAcc, false, true>(h, th, splits, stream);
+    return e != hipSuccess ? e : run_gemm<kOut, true, true>(w, tw, 1, stream);
   }
   // whole turns of the XCDs, so that dW's workgroups start on the first
   const int64_t nh = (lay_out(&h, th, splits, kRounds) + 7) / 8 * 8;
@@ -990,7 +1055,9 @@ struct XentLayout {
   int64_t tp, piece, ld_g;     // tokens in whole slabs; columns of a piece; G's row
   int splits;                  // of dH's contraction over the piece
   int z_splits;                // of the logits'; 1: their tiles take all of it
-  size_t z, part, logit, row, target, target_grad, tokens, g, acc, total;
+  TileShape grad_tile;         // of G's product, the same in all pieces
+  int parts;                   // sums a row of G: one per tile of a piece; every piece adds to the first one's
+  size_t z, part, logit, row, target, target_grad, tokens, sums, g, acc, total;
 };
 
 XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
@@ -1033,12 +1100,16 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
   for (const TileShape t : {TileShape{256, 256}, TileShape{128, 256}, TileShape{64, 128}}) {
     const int64_t n_splits = splits_of(t.rows, t.cols);
     L.splits = (int)n_splits;
-    if (gradient_tiles(T, K, n_splits).rows == t.rows) break;   // as run_gemm will choose
+    if (gradient_tiles(T, K, n_splits).rows == t.rows) break;   // as the launch will choose
   }
   L.row = take((size_t)T * sizeof(float2));
   L.target = take((size_t)T * 4);
   L.target_grad = take((size_t)T * 4);
   L.tokens = take(sizeof(XentTokens));
+  L.grad_tile = logit_tiles(L.tp, pad64(piece));
+  const int sum_cols = L.z_splits > 1 ? 1024 : L.grad_tile.cols;
+  L.parts = (int)((pad64(piece) + sum_cols - 1) / sum_cols);
+  L.sums = take((size_t)T * L.parts * 4);
   L.g = take((size_t)L.tp * L.ld_g * 2);
   L.acc = take((size_t)L.splits * T * K * 4);
   L.total = off;
@@ -1075,7 +1146,7 @@ hipError_t launch_xent_fwd(const XentArgs& p, void* ws, hipStream_t stream) {
                        pad64(p.V), p.target, p.ignore_index, p.loss, p.lse);
     return hipGetLastError();
   }
-  if ((e = run_gemm<kStats>(g, 1, stream)) != hipSuccess) return e;
+  if ((e = run_gemm<kStats>(g, logit_tiles(g.M, g.N), 1, stream)) != hipSuccess) return e;
   hipLaunchKernelGGL(xent_join_kernel, dim3((unsigned)((p.T + 15) / 16)), dim3(1024), 0, stream, g.part,
                      (int)L.part_tiles, (int)p.T, p.V, g.target_logit, p.target, p.ignore_index,
                      p.loss, p.lse);
@@ -1089,6 +1160,7 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
   int* const target = (int*)(base + L.target);
   float* const target_grad = p.nll ? (float*)(base + L.target_grad) : nullptr;
   XentTokens* const tokens = (XentTokens*)(base + L.tokens);
+  float* const sums = p.dh ? (float*)(base + L.sums) : nullptr;
   uint16_t* const g = (uint16_t*)(base + L.g);
   float* const acc = (float*)(base + L.acc);
   hipLaunchKernelGGL(xent_rows_kernel, dim3(1), dim3(1024), 0, stream, (int)p.T, p.V, p.target,
@@ -1107,15 +1179,16 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
     z.a_rows = (int)p.T; z.b_rows = (int)nv;
     z.row = row; z.local_target = target; z.target_grad = target_grad; z.v0 = (int)v0;
     z.out = g; z.ldo = L.ld_g;
+    z.sums = sums; z.add = v0 > 0;
     if (L.z_splits > 1) {
       float* const shares = (float*)(base + L.z);
       if ((e = run_logit_shares(z, L.z_splits, shares, stream)) != hipSuccess) return e;
       hipLaunchKernelGGL(xent_few_grad_kernel, dim3((unsigned)L.tp, (unsigned)((z.N + 1023) / 1024)), dim3(256), 0,
                          stream, shares, L.z_splits, (int)p.T, (int)nv, z.N, row, target, target_grad, (int)v0, g,
-                         L.ld_g);
+                         L.ld_g, sums);
       e = hipGetLastError();
     } else {
-      e = run_gemm<kGrad>(z, 1, stream);
+      e = run_gemm<kGrad>(z, L.grad_tile, 1, stream);
     }
     if (e != hipSuccess) return e;
     XentGemm dw = {};   // dW[v, k] = sum_t G[t, v] H[t, k]
@@ -1129,14 +1202,15 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
     dh.M = (int)p.T; dh.N = (int)p.K; dh.kblocks = (int)(pad64(nv) / 64);
     dh.acc = acc; dh.add = v0 > 0;
     if (p.dh && p.dw) e = run_pair(dh, L.splits, dw, stream);
-    else if (p.dw) e = run_gemm<kOut, true, true>(dw, 1, stream);
-    else if (p.dh) e = run_gemm<kAcc, false, true>(dh, L.splits, stream);
+    else if (p.dw) e = run_gemm<kOut, true, true>(dw, gradient_tiles(dw.M, dw.N, 1), 1, stream);
+    else if (p.dh) e = run_gemm<kAcc, false, true>(dh, gradient_tiles(dh.M, dh.N, L.splits), L.splits, stream);
     if (e != hipSuccess) return e;
   }
   if (!p.dh) return hipSuccess;
-  const int64_t groups = (p.T * p.K / 4 + 255) / 256;
-  hipLaunchKernelGGL(xent_dh_kernel, dim3((unsigned)(groups < (1 << 20) ? groups : (1 << 20))), dim3(256), 0, stream, acc,
-                     L.splits, p.T, p.K, tokens, (uint16_t*)p.dh, p.ld_dh);
+  const unsigned wide = (unsigned)((p.K + 1023) / 1024);   // at most 2^10
+  hipLaunchKernelGGL(xent_dh_kernel, dim3((unsigned)(p.T < (1 << 20) ? p.T : (1 << 20)), wide), dim3(256), 0, stream,
+                     acc, L.splits, p.T, p.K, tokens, row, target, sums, L.parts, (const uint16_t*)p.w, p.ld_w,
+                     (uint16_t*)p.dh, p.ld_dh);
   return hipGetLastError();
 }
 

@@ -474,7 +474,10 @@ int fp8bw_rms_norm_bwd(const void* dy, int64_t ld_dy, const void* s, int64_t ld_
  *   dh, dw   device bf16 [T, K] (ld_dh) and [V, K] (ld_dw); either may be NULL.
  *   The backward takes the vocabulary in pieces: each piece's logits are made
  *   again and become its part of G (bf16) in the workspace, whose size does
- *   not grow with V beyond one piece.
+ *   not grow with V beyond one piece.  G's rows are rounded to bf16 and their
+ *   sums, which are zero in exact numbers, taken out of dh with the target's
+ *   row of w: dh[t] = sum_v G[t, v] (w[v] - w[target[t]]), so that what the
+ *   rows of w share does not carry G's rounding into dh.
  *   ws       fp8bw_linear_xent_ws_bytes(T, V, K, backward) bytes, 256-byte
  *            aligned (backward: 0 or 1).
  *   Requires K % 64 == 0, 64 <= K <= 2^20, V <= 2^28, T <= 2^24, leading
