@@ -202,6 +202,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamwLaunch L) {
       load8_f32((const float*)T.m + at, n, m);
       load8_f32((const float*)T.v + at, n, v);
     }
+    // the first 2^32 elements' hash is of key + element alone
+    const uint32_t far = RANDOM ? mix32((uint32_t)(i >> 32)) : 0u;
     uint32_t rnd[8];
     float am = 0.f, av = 0.f;
 #pragma unroll
@@ -209,7 +211,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamwLaunch L) {
       const float gj = g[j] * gs;
       m[j] = m[j] * L.beta1 + gj * L.one_minus_beta1;
       v[j] = v[j] * L.beta2 + gj * gj * L.one_minus_beta2;
-      rnd[j] = RANDOM ? mix32(T.key + (uint32_t)i + j) : 0u;
+      rnd[j] = RANDOM ? mix32((T.key + (uint32_t)i + j) ^ far) : 0u;
       if (EIGHT && j < n) {
         am = fmaxf(am, fabsf(m[j]));
         av = fmaxf(av, v[j]);

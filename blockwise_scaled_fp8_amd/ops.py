@@ -675,7 +675,7 @@ def _adamw_list(ts, n, name):
 
 def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
                weight_decay=0.0, exp_avg_scales=None, root_scales=None, masters=None,
-               grad_scale=None, seed=None):
+               grad_scale=None, seed=None, ordinals=None):
     """One AdamW step over lists of contiguous tensors, in place.
 
     params and grads bf16 or fp32.  With fp32 exp_avgs and exp_avg_sqs the
@@ -684,7 +684,10 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, beta1=0.9, bet
     are exp_avg_scales and root_scales.  masters: fp32 weights behind bf16
     params (a list, None for tensors without one).  grad_scale: one-element
     fp32 tensor that multiplies every gradient.  seed: a new integer each step
-    to round codes and bf16 params at random; None rounds to nearest."""
+    to round codes and bf16 params at random; None rounds to nearest.  ordinals:
+    one distinct number below 2^20 per tensor, which with the seed picks its
+    random numbers; default its place in the lists.  Calls that share a seed (one
+    per parameter group) give every tensor another."""
     lib = load_library()
     n = len(params)
     if n == 0:
@@ -741,17 +744,27 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, beta1=0.9, bet
         types = [OUT_DTYPES[params[0].dtype] | OUT_DTYPES[grads[0].dtype] << 32] * n
     else:
         types = [OUT_DTYPES[p.dtype] | OUT_DTYPES[g.dtype] << 32 for p, g in zip(params, grads)]
+    places = range(n) if ordinals is None else [int(o) for o in ordinals]
+    if ordinals is not None and (len(places) != n or len(set(places)) != n or min(places) < 0
+                                 or max(places) >= 1 << 20):
+        raise ValueError("ordinals must be distinct numbers below 2^20, one per param")
     fields = ([t.data_ptr() for t in params], [t.data_ptr() for t in grads],
               [t.data_ptr() for t in exp_avgs], [t.data_ptr() for t in exp_avg_sqs],
               *scales, master_ptrs, numels, types)
-    words = [0] * (9 * n)
-    for k, column in enumerate(fields):
-        words[k::9] = column
-    arr = (AdamwTensor * n).from_buffer(array.array("q", words))
+    # a tensor's ordinal is its place in the array; the places between stay empty
+    count = n if ordinals is None else max(places) + 1
+    words = [0] * (9 * count)
+    if ordinals is None:
+        for k, column in enumerate(fields):
+            words[k::9] = column
+    else:
+        for place, row in zip(places, zip(*fields)):
+            words[9 * place:9 * place + 9] = row
+    arr = (AdamwTensor * count).from_buffer(array.array("q", words))
     if grad_scale is not None and (grad_scale.device != device or grad_scale.dtype != torch.float32
                                    or grad_scale.numel() != 1):
         raise ValueError("grad_scale must be a one-element float32 tensor on the params' device")
-    args = (arr, n, int(eight), int(step), float(lr), float(beta1), float(beta2), float(eps),
+    args = (arr, count, int(eight), int(step), float(lr), float(beta1), float(beta2), float(eps),
             float(weight_decay), _ptr(grad_scale), int(seed is not None),
             0 if seed is None else int(seed) & 0xFFFFFFFFFFFFFFFF, _stream(params[0]))
     if index == torch._C._cuda_getDevice():

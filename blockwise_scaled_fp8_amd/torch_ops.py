@@ -484,8 +484,10 @@ class AdamW(torch.optim.Optimizer):
     bytes of state per parameter instead of 8).  master_weights: fp32 copies
     behind bf16 parameters.  stochastic: round codes, and bf16 parameters
     without a master, up or down at random by a hash of (seed, step, tensor,
-    element); default: wherever something is so held.  ``step(grad_scale=t)``
-    multiplies every gradient by the one-element fp32 tensor t."""
+    element), a tensor being known by its place among the parameters of all
+    groups; default: wherever something is so held.  Optimizers that train side
+    by side take different seeds.  ``step(grad_scale=t)`` multiplies every
+    gradient by the one-element fp32 tensor t."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1, state_bits=32,
                  master_weights=False, stochastic=True, seed=0):
@@ -517,25 +519,29 @@ class AdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        first = 0
         for group in self.param_groups:
             by_step = {}
-            for p in group["params"]:
+            for ordinal, p in enumerate(group["params"], first):
                 if p.grad is None:
                     continue
                 if not self.state[p]:
                     self.state[p].update(self._new_state(p))
                 st = self.state[p]
                 st["step"] += 1
-                by_step.setdefault((p.device, st["step"]), []).append((p, st))
+                by_step.setdefault((p.device, st["step"]), []).append((p, st, ordinal))
+            first += len(group["params"])
             for (_, step), tensors in by_step.items():
                 self._step_group(group, step, tensors, grad_scale)
         return loss
 
     def _step_group(self, group, step, tensors, grad_scale):
-        states = [st for _, st in tensors]
+        params, states, ordinals = zip(*tensors)
+        if ordinals == tuple(range(len(ordinals))):
+            ordinals = None   # their places in the lists
         eight = self.state_bits == 8
         second = "exp_avg_root" if eight else "exp_avg_sq"
-        ops.adamw_step([p for p, _ in tensors], [p.grad.contiguous() for p, _ in tensors],
+        ops.adamw_step(params, [p.grad.contiguous() for p in params],
                        [st["exp_avg"] for st in states], [st[second] for st in states], step=step,
                        lr=group["lr"], beta1=group["betas"][0], beta2=group["betas"][1],
                        eps=group["eps"], weight_decay=group["weight_decay"],
@@ -543,7 +549,7 @@ class AdamW(torch.optim.Optimizer):
                        root_scales=[st["exp_avg_root_scale"] for st in states] if eight else None,
                        masters=[st.get("master") for st in states], grad_scale=grad_scale,
                        seed=(self.seed + 0x9E3779B97F4A7C15 * step) & 0xFFFFFFFFFFFFFFFF
-                       if self.stochastic else None)
+                       if self.stochastic else None, ordinals=ordinals)
 
     def load_state_dict(self, state_dict):
         """As torch's, but states keep their types (torch casts floating

@@ -525,7 +525,11 @@ int fp8bw_linear_xent_bwd_loss(const float* dloss, const void* h, int64_t ld_h, 
  *            rounded up or down at random, in proportion to the remainder, by
  *            16 bits per value of a hash of (seed, index of the tensor in
  *            `tensors`, element).  Equal arguments give equal results; use
- *            another seed each step.  Zero: to nearest.
+ *            another seed each step, and in calls that share a seed another
+ *            index for every tensor (an entry of numel 0 takes up an index and
+ *            may be all zeros).  The hash is of 32 bits, the tensor's key added
+ *            to the element: of 2^32 elements and more some share their numbers.
+ *            Zero: to nearest.
  *   step     counts from 1.  lr, weight_decay and eps >= 0; 0 <= beta1, beta2 < 1.
  * One launch per 40 tensors.  numel < 2^35.
  */
