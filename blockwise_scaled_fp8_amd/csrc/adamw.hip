@@ -13,6 +13,10 @@
 // while the scale stays.  A positive root never becomes code 0: an element
 // whose v vanished next to a large neighbour would be stepped by m / eps.
 //
+// A moment that is infinite or NaN becomes the NaN code, and the block's scale
+// goes by the others: one bad gradient costs its own element, as with fp32
+// states.
+//
 // With a seed, what is held in fewer bits (codes, and bf16 parameters that
 // have no fp32 master) is rounded up or down by 16 random bits per value, in
 // proportion to the remainder.  Round-to-nearest would freeze slow averages:
@@ -136,7 +140,8 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 // drops, and cuts: up with the probability of the remainder in units of
 // 2^-16, subnormal codes included (checked on the GPU against that definition
 // on a million values of 22 octaves).  `shift` picks the 16 random bits.
-// KEEP: what is not zero gets at least the smallest code.
+// KEEP: what is positive gets at least the smallest code; no NaN among f.
+// Infinite values (and NaN without KEEP) convert to the NaN code.
 template <bool RANDOM, bool KEEP>
 __device__ __forceinline__ uint2 encode8(const float (&f)[8], int exponent, const uint32_t (&rnd)[8], int shift) {
   const float inv = __builtin_amdgcn_ldexpf(1.f, -exponent);
@@ -147,7 +152,12 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], int exponent, cons
     if constexpr (KEEP) y[j] = f[j] > 0.f ? fmaxf(y[j], 0x1p-9f) : 0.f;
   }
   if constexpr (!RANDOM) {
-    return make_uint2(cvt4_e4m3(y[0], y[1], y[2], y[3]), cvt4_e4m3(y[4], y[5], y[6], y[7]));
+    // no clamp: the scale holds magnitudes within 448, and NaN stays NaN
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
+    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], hi, true);
+    return make_uint2((uint32_t)lo, (uint32_t)hi);
   } else {
     uint32_t r[8];
 #pragma unroll
@@ -202,60 +212,66 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamwLaunch L) {
       load8_f32((const float*)T.m + at, n, m);
       load8_f32((const float*)T.v + at, n, v);
     }
-    // the first 2^32 elements' hash is of key + element alone
-    const uint32_t far = RANDOM ? mix32((uint32_t)(i >> 32)) : 0u;
-    uint32_t rnd[8];
     float am = 0.f, av = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float gj = g[j] * gs;
       m[j] = m[j] * L.beta1 + gj * L.one_minus_beta1;
       v[j] = v[j] * L.beta2 + gj * gj * L.one_minus_beta2;
-      rnd[j] = RANDOM ? mix32((T.key + (uint32_t)i + j) ^ far) : 0u;
       if (EIGHT && j < n) {
         am = fmaxf(am, fabsf(m[j]));
         av = fmaxf(av, v[j]);
       }
     }
+    bool rare = false;
     if constexpr (EIGHT) {
-      am = row16_max(am);
-      av = row16_max(av);
       // Hardware square root and reciprocal, each within 1 ulp (9.2e-8 and
       // 9.0e-8 measured): codes keep 4 bits and the step is far smaller than
       // p, while the IEEE forms bind this kernel by its arithmetic (723
-      // against 655 us for 336M elements).  They do not take subnormals:
-      // where a wave has some, it takes the IEEE root.
-      bool tiny = false;
+      // against 655 us for 336M elements).  They do not take subnormals, which
+      // get the IEEE root.  The same test finds the moments that are not finite
+      // (an infinite or NaN gradient shows in v), which the scales leave out.
+      rare = !(am < INFINITY);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         root[j] = __builtin_amdgcn_sqrtf(v[j]);
-        tiny |= __builtin_amdgcn_classf(v[j], 1 << 7);   // positive subnormal
+        rare |= __builtin_amdgcn_classf(v[j], 1 << 0 | 1 << 1 | 1 << 7 | 1 << 9);   // NaN, subnormal, infinite
       }
-      if (__builtin_amdgcn_ballot_w64(tiny)) {
+      rare = __builtin_amdgcn_ballot_w64(rare) != 0;
+      if (rare) {
+        am = av = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) root[j] = __builtin_sqrtf(v[j]);
+        for (int j = 0; j < 8; ++j) {
+          if (v[j] < 0x1p-126f) root[j] = __builtin_sqrtf(v[j]);
+          if (j < n && fabsf(m[j]) < INFINITY) am = fmaxf(am, fabsf(m[j]));
+          if (j < n && v[j] < INFINITY) av = fmaxf(av, v[j]);
+        }
       }
+      am = row16_max(am);
+      av = row16_max(av);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         p[j] = p[j] * L.decay - m[j] * __builtin_amdgcn_rcpf(root[j] * L.root_factor + L.eps) * L.step_size;
+      if (rare) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) root[j] = root[j] >= 0.f ? root[j] : INFINITY;   // encode8 takes no NaN here
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         p[j] = p[j] * L.decay - m[j] / (__builtin_sqrtf(v[j]) * L.root_factor + L.eps) * L.step_size;
     }
-    if constexpr (EIGHT) {
-      // The root's scale comes from the correctly rounded root of the largest v.
-      const int em = scale_exponent(am), er = scale_exponent(__builtin_sqrtf(av));
-      store8_codes((uint8_t*)T.m + at, n, encode8<RANDOM, false>(m, em, rnd, 0));
-      store8_codes((uint8_t*)T.v + at, n, encode8<RANDOM, true>(root, er, rnd, 16));
-      if ((threadIdx.x & 15) == 0) {
-        T.m_scale[blk] = __builtin_amdgcn_ldexpf(1.f, em);
-        T.root_scale[blk] = __builtin_amdgcn_ldexpf(1.f, er);
-      }
-    } else {
+    // the first 2^32 elements' hash is of key + element alone
+    const uint32_t far = RANDOM ? mix32((uint32_t)(i >> 32)) : 0u;
+    uint32_t rnd[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rnd[j] = RANDOM ? mix32((T.key + (uint32_t)i + j) ^ far) : 0u;
+    if constexpr (!EIGHT) {
       store8_f32((float*)T.m + at, n, m);
       store8_f32((float*)T.v + at, n, v);
     }
+    // The parameter leaves before 8-bit states are encoded: 72 registers, 7
+    // waves a SIMD, instead of 81 and 5 (336M elements: 682 us, 736 us).
     if (T.master) store8_f32(T.master + at, n, p);
     if (T.flags & kAdamwParamF32) {
       store8_f32((float*)T.param + at, n, p);
@@ -270,6 +286,16 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamwLaunch L) {
         for (int j = 0; j < 8; ++j) b[j] = f32_to_bf16_rne(p[j]);
       }
       store8_u16((uint16_t*)T.param + at, n, b);
+    }
+    if constexpr (EIGHT) {
+      // The root's scale comes from the correctly rounded root of the largest v.
+      const int em = scale_exponent(am), er = scale_exponent(__builtin_sqrtf(av));
+      store8_codes((uint8_t*)T.m + at, n, encode8<RANDOM, false>(m, em, rnd, 0));
+      store8_codes((uint8_t*)T.v + at, n, encode8<RANDOM, true>(root, er, rnd, 16));
+      if ((threadIdx.x & 15) == 0) {
+        T.m_scale[blk] = __builtin_amdgcn_ldexpf(1.f, em);
+        T.root_scale[blk] = __builtin_amdgcn_ldexpf(1.f, er);
+      }
     }
   }
 }

@@ -519,8 +519,9 @@ int fp8bw_linear_xent_bwd_loss(const float* dloss, const void* h, int64_t ld_h, 
  *            m = code * exp_avg_scale, sqrt(v) = code * root_scale; the step
  *            writes power-of-two scales, the least that hold the block's
  *            largest value within 448 (1 for a block of zeros).  A positive
- *            sqrt(v) is never rounded to code 0.  Codes 0 with any finite
- *            scale are the start.
+ *            sqrt(v) is never rounded to code 0.  A moment that is infinite or
+ *            NaN becomes the NaN code and has no part in its block's scale.
+ *            Codes 0 with any finite scale are the start.
  *   stochastic  nonzero: codes, and bf16 parameters without a master, are
  *            rounded up or down at random, in proportion to the remainder, by
  *            16 bits per value of a hash of (seed, index of the tensor in
