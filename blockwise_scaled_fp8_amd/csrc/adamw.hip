@@ -280,7 +280,10 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamwLaunch L) {
       if (RANDOM && !T.master) {
         // add 16 random bits below the cut, then cut: up with the probability of the remainder
 #pragma unroll
-        for (int j = 0; j < 8; ++j) b[j] = (__float_as_uint(p[j]) + ((rnd[j] * 0x9E3779B9u) >> 16)) >> 16;
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t up = (__float_as_uint(p[j]) + ((rnd[j] * 0x9E3779B9u) >> 16)) >> 16;
+          b[j] = p[j] == p[j] ? up : 0x7FC0u;   // a NaN's mantissa may carry into its sign
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) b[j] = f32_to_bf16_rne(p[j]);

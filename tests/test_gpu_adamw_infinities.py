@@ -1,4 +1,4 @@
-"""8-bit AdamW and gradients that are infinite or NaN: the element itself is
+"""AdamW and gradients that are infinite or NaN.  8-bit states: the element itself is
 lost (NaN from then on, as its fp32 states would be), its block's other
 elements are not."""
 
@@ -100,3 +100,14 @@ def test_a_nan_moment_stays_one(gpu, seed):
             assert bad[300] and bad[301] and bad.sum() == 2
         assert int(p.isnan().sum()) == 2 and bool(p[300:302].isnan().all())
         assert bool(s[2].isfinite().all()) and bool(s[3].isfinite().all())
+def test_nan_stays_nan_in_bf16_parameters(gpu):
+    """A NaN with every mantissa bit set does not carry into the sign."""
+    n = 256
+    for bits in (8, 32):
+        p = torch.ones(n, device=gpu).bfloat16()
+        grad = torch.full((n,), -1, dtype=torch.int32, device=gpu).view(torch.float32)
+        m, v = (torch.zeros(n, dtype=torch.uint8 if bits == 8 else torch.float32, device=gpu) for _ in range(2))
+        s = [torch.ones(2, device=gpu) for _ in range(2)] if bits == 8 else None
+        say("adamw nan", bits)
+        fp8.adamw_step([p], [grad], [m], [v], exp_avg_scales=s and [s[0]], root_scales=s and [s[1]], step=1, lr=0.1, seed=3)
+        assert bool(p.isnan().all()), (bits, p[:8])
