@@ -321,7 +321,7 @@ def norm_linear_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], norm_weig
                     w: torch.Tensor, eps: float, train: bool
                     ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
     """(Y, s, rstd, qt, recip_t): Y = norm(x + residual) . W^T; s empty without
-    a residual, qt and recip_t empty unless train."""
+    a residual, qt and recip_t (for W's gradient) empty unless train."""
     _check_2d_bf16(x, w)
     o = ops.rms_norm_fwd(x, norm_weight, residual=residual, eps=eps, y=False, q=True, qt=train)
     wq, wr = ops.fp8_blockwise_quant(w.contiguous(), "128x128")
@@ -345,27 +345,40 @@ def _norm_linear_fwd_fake(x, residual, norm_weight, w, eps, train):
 @torch.library.custom_op("fp8bw::norm_linear_bwd", mutates_args=())
 def norm_linear_bwd(dy: torch.Tensor, ds: Optional[torch.Tensor], s: torch.Tensor,
                     rstd: torch.Tensor, norm_weight: torch.Tensor, w: torch.Tensor,
-                    qt: torch.Tensor, recip_t: torch.Tensor
-                    ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+                    qt: torch.Tensor, recip_t: torch.Tensor, need_dx: bool = True,
+                    need_dw: bool = True) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(dx, dnorm_weight, dW): dgrad and wgrad GEMMs on the linear's recipe,
-    then the norm's backward on the dgrad."""
-    dyq, dyr, dytq, dytr = ops.fp8_blockwise_quant_dual(dy.contiguous(), "1x128")
-    wtq, wtr = ops.fp8_blockwise_quant(w.contiguous(), "128x128", transpose=True)
-    dv = ops.fp8_scaled_gemm_blockwise(dyq, dyr, wtq, wtr)
-    dw = ops.fp8_scaled_gemm_blockwise(dytq, dytr, qt, recip_t, b_block="1x128")
-    dx, dnorm = ops.rms_norm_bwd(dv, s, rstd, norm_weight, ds)
-    return dx, dnorm, dw
+    then the norm's backward on the dgrad.  Without need_dx (dx and
+    dnorm_weight) or need_dw those come back empty."""
+    dy = dy.contiguous()
+    if need_dx and need_dw:
+        dyq, dyr, dytq, dytr = ops.fp8_blockwise_quant_dual(dy, "1x128")
+    elif need_dx:
+        dyq, dyr = ops.fp8_blockwise_quant(dy, "1x128")
+    elif need_dw:
+        dytq, dytr = ops.fp8_blockwise_quant(dy, "1x128", transpose=True)
+    dx = dnorm = dw = None
+    if need_dx:
+        wtq, wtr = ops.fp8_blockwise_quant(w.contiguous(), "128x128", transpose=True)
+        dx, dnorm = ops.rms_norm_bwd(ops.fp8_scaled_gemm_blockwise(dyq, dyr, wtq, wtr), s, rstd, norm_weight, ds)
+    if need_dw:
+        dw = ops.fp8_scaled_gemm_blockwise(dytq, dytr, qt, recip_t, b_block="1x128")
+    return (_empty(s) if dx is None else dx, _empty(norm_weight) if dnorm is None else dnorm,
+            _empty(w) if dw is None else dw)
 
 
 @norm_linear_bwd.register_fake
-def _norm_linear_bwd_fake(dy, ds, s, rstd, norm_weight, w, qt, recip_t):
-    return torch.empty_like(s), torch.empty_like(norm_weight), torch.empty_like(w)
+def _norm_linear_bwd_fake(dy, ds, s, rstd, norm_weight, w, qt, recip_t, need_dx=True, need_dw=True):
+    return (torch.empty_like(s) if need_dx else _empty(s),
+            torch.empty_like(norm_weight) if need_dx else _empty(norm_weight),
+            torch.empty_like(w) if need_dw else _empty(w))
 
 
 class _RMSNormLinear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, norm_weight, w, eps):
-        y, s, rstd, qt, recip_t = torch.ops.fp8bw.norm_linear_fwd(x, residual, norm_weight, w, eps, True)
+        y, s, rstd, qt, recip_t = torch.ops.fp8bw.norm_linear_fwd(x, residual, norm_weight, w, eps,
+                                                                  ctx.needs_input_grad[3])
         ctx.has_residual = residual is not None
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(x if residual is None else s, rstd, norm_weight, w, qt, recip_t)
@@ -377,9 +390,13 @@ class _RMSNormLinear(torch.autograd.Function):
         dres = ds.contiguous() if ctx.has_residual and ds is not None else None
         if dy is None:
             return dres, dres, None, None, None
+        need_dx, need_dw = any(ctx.needs_input_grad[:3]), ctx.needs_input_grad[3]
         dx, dnorm, dw = torch.ops.fp8bw.norm_linear_bwd(dy.contiguous(), dres, s, rstd, norm_weight,
-                                                        w, qt, recip_t)
-        return dx, (dx if ctx.has_residual else None), dnorm, dw, None
+                                                        w, qt, recip_t, need_dx, need_dw)
+        if not need_dx:
+            dx = dnorm = None
+        return (dx, (dx if ctx.has_residual else None), dnorm,
+                dw if need_dw else None, None)
 
 
 class RMSNormLinear(torch.nn.Module):
