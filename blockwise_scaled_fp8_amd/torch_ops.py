@@ -240,12 +240,23 @@ def _empty(like, dtype=None):
     return like.new_empty((0,), dtype=dtype)
 
 
+def _aligned(t):
+    """t where it is laid out as the kernels read it (16-byte aligned rows of
+    unit column stride), else a copy that is."""
+    if t is None or t.numel() == 0:
+        return t
+    rows_fit = t.dim() < 2 or t.shape[0] == 1 or (t.stride(0) >= t.shape[1] and t.stride(0) % 8 == 0)
+    if t.data_ptr() % 16 == 0 and t.stride(-1) == 1 and rows_fit:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 @torch.library.custom_op("fp8bw::rms_norm_fwd", mutates_args=())
 def rms_norm_fwd(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor],
                  eps: float) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(y, s, rstd) of ops.rms_norm_fwd; s comes back empty without a
     residual (it is x)."""
-    o = ops.rms_norm_fwd(x, weight, residual=residual, eps=eps)
+    o = ops.rms_norm_fwd(_aligned(x), _aligned(weight), residual=_aligned(residual), eps=eps)
     return o.y, (_empty(x) if residual is None else o.s), o.rstd
 
 
@@ -261,12 +272,12 @@ def _rms_norm_fwd_fake(x, weight, residual, eps):
 def rms_norm_bwd(dy: torch.Tensor, s: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
                  dres: Optional[torch.Tensor]) -> tuple[torch.Tensor, torch.Tensor]:
     """(dx, dweight) of ops.rms_norm_bwd."""
-    return ops.rms_norm_bwd(dy, s, rstd, weight, dres)
+    return ops.rms_norm_bwd(_aligned(dy), _aligned(s), rstd, _aligned(weight), _aligned(dres))
 
 
 @rms_norm_bwd.register_fake
 def _rms_norm_bwd_fake(dy, s, rstd, weight, dres):
-    return torch.empty_like(dy), torch.empty_like(weight)
+    return dy.new_empty(dy.shape), torch.empty_like(weight)
 
 
 class _RMSNorm(torch.autograd.Function):
@@ -281,10 +292,10 @@ class _RMSNorm(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy, ds):
         s, rstd, weight = ctx.saved_tensors
-        dres = ds.contiguous() if ctx.has_residual and ds is not None else None
+        dres = ds if ctx.has_residual else None
         if dy is None:
             return dres, dres, None, None
-        dx, dweight = torch.ops.fp8bw.rms_norm_bwd(dy.contiguous(), s, rstd, weight, dres)
+        dx, dweight = torch.ops.fp8bw.rms_norm_bwd(dy, s, rstd, weight, dres)
         return dx, (dx if ctx.has_residual else None), dweight, None
 
 
@@ -323,8 +334,9 @@ def norm_linear_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], norm_weig
     """(Y, s, rstd, qt, recip_t): Y = norm(x + residual) . W^T; s empty without
     a residual, qt and recip_t (for W's gradient) empty unless train."""
     _check_2d_bf16(x, w)
-    o = ops.rms_norm_fwd(x, norm_weight, residual=residual, eps=eps, y=False, q=True, qt=train)
-    wq, wr = ops.fp8_blockwise_quant(w.contiguous(), "128x128")
+    o = ops.rms_norm_fwd(_aligned(x), _aligned(norm_weight), residual=_aligned(residual), eps=eps, y=False,
+                         q=True, qt=train)
+    wq, wr = ops.fp8_blockwise_quant(_aligned(w), "128x128")
     out = ops.fp8_scaled_gemm_blockwise(o.q, o.recip, wq, wr)
     return (out, _empty(x) if residual is None else o.s, o.rstd,
             o.qt if train else _empty(x, torch.uint8),
@@ -350,7 +362,7 @@ def norm_linear_bwd(dy: torch.Tensor, ds: Optional[torch.Tensor], s: torch.Tenso
     """(dx, dnorm_weight, dW): dgrad and wgrad GEMMs on the linear's recipe,
     then the norm's backward on the dgrad.  Without need_dx (dx and
     dnorm_weight) or need_dw those come back empty."""
-    dy = dy.contiguous()
+    dy = _aligned(dy)
     if need_dx and need_dw:
         dyq, dyr, dytq, dytr = ops.fp8_blockwise_quant_dual(dy, "1x128")
     elif need_dx:
@@ -359,8 +371,9 @@ def norm_linear_bwd(dy: torch.Tensor, ds: Optional[torch.Tensor], s: torch.Tenso
         dytq, dytr = ops.fp8_blockwise_quant(dy, "1x128", transpose=True)
     dx = dnorm = dw = None
     if need_dx:
-        wtq, wtr = ops.fp8_blockwise_quant(w.contiguous(), "128x128", transpose=True)
-        dx, dnorm = ops.rms_norm_bwd(ops.fp8_scaled_gemm_blockwise(dyq, dyr, wtq, wtr), s, rstd, norm_weight, ds)
+        wtq, wtr = ops.fp8_blockwise_quant(_aligned(w), "128x128", transpose=True)
+        dx, dnorm = ops.rms_norm_bwd(ops.fp8_scaled_gemm_blockwise(dyq, dyr, wtq, wtr), _aligned(s), rstd,
+                                     _aligned(norm_weight), _aligned(ds))
     if need_dw:
         dw = ops.fp8_scaled_gemm_blockwise(dytq, dytr, qt, recip_t, b_block="1x128")
     return (_empty(s) if dx is None else dx, _empty(norm_weight) if dnorm is None else dnorm,
@@ -369,9 +382,9 @@ def norm_linear_bwd(dy: torch.Tensor, ds: Optional[torch.Tensor], s: torch.Tenso
 
 @norm_linear_bwd.register_fake
 def _norm_linear_bwd_fake(dy, ds, s, rstd, norm_weight, w, qt, recip_t, need_dx=True, need_dw=True):
-    return (torch.empty_like(s) if need_dx else _empty(s),
+    return (s.new_empty(s.shape) if need_dx else _empty(s),
             torch.empty_like(norm_weight) if need_dx else _empty(norm_weight),
-            torch.empty_like(w) if need_dw else _empty(w))
+            w.new_empty(w.shape) if need_dw else _empty(w))
 
 
 class _RMSNormLinear(torch.autograd.Function):
@@ -387,12 +400,12 @@ class _RMSNormLinear(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy, ds):
         s, rstd, norm_weight, w, qt, recip_t = ctx.saved_tensors
-        dres = ds.contiguous() if ctx.has_residual and ds is not None else None
+        dres = ds if ctx.has_residual else None
         if dy is None:
             return dres, dres, None, None, None
         need_dx, need_dw = any(ctx.needs_input_grad[:3]), ctx.needs_input_grad[3]
-        dx, dnorm, dw = torch.ops.fp8bw.norm_linear_bwd(dy.contiguous(), dres, s, rstd, norm_weight,
-                                                        w, qt, recip_t, need_dx, need_dw)
+        dx, dnorm, dw = torch.ops.fp8bw.norm_linear_bwd(dy, dres, s, rstd, norm_weight, w,
+                                                        qt, recip_t, need_dx, need_dw)
         if not need_dx:
             dx = dnorm = None
         return (dx, (dx if ctx.has_residual else None), dnorm,
@@ -432,7 +445,7 @@ class RMSNormLinear(torch.nn.Module):
 def linear_xent_fwd(h: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
                     ignore_index: int) -> tuple[torch.Tensor, torch.Tensor]:
     """(loss, lse) per token of ops.linear_xent_fwd."""
-    return ops.linear_xent_fwd(h, w, target, ignore_index)
+    return ops.linear_xent_fwd(_aligned(h), _aligned(w), target, ignore_index)
 
 
 @linear_xent_fwd.register_fake
@@ -446,7 +459,8 @@ def linear_xent_bwd(dloss: torch.Tensor, h: torch.Tensor, w: torch.Tensor, targe
                     lse: torch.Tensor, ignore_index: int, need_dh: bool, need_dw: bool,
                     loss: Optional[torch.Tensor] = None) -> tuple[torch.Tensor, torch.Tensor]:
     """(dh, dw) of ops.linear_xent_bwd; one not asked for comes back empty."""
-    dh, dw = ops.linear_xent_bwd(dloss, h, w, target, lse, ignore_index, need_dh, need_dw, loss)
+    dh, dw = ops.linear_xent_bwd(dloss, _aligned(h), _aligned(w), target, lse, ignore_index, need_dh,
+                                 need_dw, loss)
     return (_empty(h) if dh is None else dh), (_empty(w) if dw is None else dw)
 
 

@@ -65,3 +65,51 @@ def _layouts(t):
     wide = torch.zeros(rows, cols + 5, dtype=t.dtype, device=t.device)
     wide[:, 3:3 + cols] = t
     return {"transposed": t.t().contiguous().t(), "unaligned": flat[1:].view(rows, cols), "pitch": wide[:, 3:3 + cols]}
+
+
+@pytest.mark.parametrize("layout", ["transposed", "unaligned", "pitch"])
+def test_inputs_and_gradients_of_any_layout(gpu, layout):
+    M, K, N = 128, 256, 384
+    x, r, dy, ds = (_randn(gpu, M, k, seed=i) for i, k in enumerate((K, K, K, K)))
+    norm, block = fp8.RMSNorm(K, device=gpu), fp8.RMSNormLinear(K, N, device=gpu)
+    w, t = _randn(gpu, 700, K, seed=9, std=0.1), torch.arange(M, device=gpu)
+    dl = _randn(gpu, M, N, seed=7)
+    other = {id(a): _layouts(a)[layout] for a in (x, r, dy, ds, w, dl)}
+    results = []
+    say("layouts", layout)
+    for pick in (lambda a: a, lambda a: other[id(a)]):
+        out = []
+        for run in ("norm", "block", "head"):
+            a, b, c = (pick(v).detach().requires_grad_() for v in (x, r, w))
+            if run == "norm":
+                y, s = norm(a, b)
+                torch.autograd.backward([y, s], [pick(dy), pick(ds)])
+                out += [y, s, a.grad, b.grad]
+            elif run == "block":
+                y, s = block(a, b)
+                torch.autograd.backward([y, s], [pick(dl), pick(ds)])
+                out += [y, s, a.grad, b.grad]
+                with torch.no_grad():
+                    out += list(block(a, b))
+            else:
+                loss = fp8.linear_cross_entropy(a, c, t)
+                loss.backward()
+                out += [loss, a.grad, c.grad]
+        results.append(out)
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+def test_a_broadcast_residual(gpu):
+    """One row for all tokens: its gradient is the sum over them."""
+    M, K = 50, 256
+    x, row, dy = _randn(gpu, M, K, seed=1), _randn(gpu, 1, K, seed=2), _randn(gpu, M, K, seed=3)
+    norm = fp8.RMSNorm(K, device=gpu)
+    results = []
+    say("broadcast residual")
+    for copy in (False, True):
+        a, b = x.clone().requires_grad_(), row.clone().requires_grad_()
+        wide = b.expand(M, K)
+        y, s = norm(a, wide.contiguous() if copy else wide)
+        y.backward(dy)
+        results.append((y, s, a.grad, b.grad))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
