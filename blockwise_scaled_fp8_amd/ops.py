@@ -555,6 +555,7 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-6, y=True, q=False, qt=False, 
     rows, cols = x.shape
     _norm_weight(weight, cols)
     dev = x.device
+    given = s
     if residual is not None:
         _bf16_matrix(residual, "residual", (rows, cols))
         if s is None:
@@ -577,6 +578,8 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-6, y=True, q=False, qt=False, 
         _ptr(ty), _ld(ty), _ptr(tq), _ld(tq), _ptr(tr), tr.stride(0) if q else 0,
         tr.stride(1) if q else 0, _ptr(tqt), _ld(tqt), _ptr(trt), trt.stride(0) if qt else 0,
         trt.stride(1) if qt else 0, _stream(x)))
+    if given is not None:
+        torch.autograd.graph.increment_version(given)
     return RMSNormOut(x if residual is None else s, rstd, ty, tq, tr, tqt, trt)
 
 
@@ -772,3 +775,5 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, beta1=0.9, bet
     else:
         with torch.cuda.device(device):
             check(lib.fp8bw_adamw_step(*args))
+    # a graph that saved a parameter refuses to run backward through the new values
+    torch.autograd.graph.increment_version(params)

@@ -113,3 +113,30 @@ def test_a_broadcast_residual(gpu):
         y.backward(dy)
         results.append((y, s, a.grad, b.grad))
     assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+def test_changes_in_place_are_recorded(gpu):
+    """A graph made before the optimizer's step does not run backward through
+    the weights after it; nor one whose input became the norm's sum."""
+    p = torch.nn.Parameter(torch.ones(256, device=gpu))
+    opt = fp8.AdamW([p], lr=0.1)
+    a = torch.ones(256, device=gpu).requires_grad_()
+    product = (p * a).sum()
+    p.grad = torch.ones_like(p)
+    say("version counters")
+    opt.step()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        product.backward()
+    x = _randn(gpu, 32, 256, seed=1)
+    b = torch.ones(256, device=gpu, dtype=torch.bfloat16).requires_grad_()
+    product = (x * b).sum()
+    fp8.rms_norm_fwd(x, torch.ones(256, device=gpu), residual=x.clone(), s=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        product.backward()
+    # tensors without a counter are taken all the same
+    with torch.inference_mode():
+        q = [torch.ones(256, device=gpu) for _ in range(4)]
+        fp8.adamw_step([q[0]], [q[1]], [q[2]], [q[3]], step=1, lr=0.1)
+        x = _randn(gpu, 32, 256, seed=1)
+        fp8.rms_norm_fwd(x, torch.ones(256, device=gpu), residual=x.clone(), s=x)
+    assert bool((q[0] < 1).all())
