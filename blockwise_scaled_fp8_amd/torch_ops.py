@@ -559,8 +559,7 @@ class AdamW(torch.optim.Optimizer):
                 if not self.state[p]:
                     self.state[p].update(self._new_state(p))
                 st = self.state[p]
-                st["step"] += 1
-                by_step.setdefault((p.device, st["step"]), []).append((p, st, ordinal))
+                by_step.setdefault((p.device, st["step"] + 1), []).append((p, st, ordinal))
             first += len(group["params"])
             for (_, step), tensors in by_step.items():
                 self._step_group(group, step, tensors, grad_scale)
@@ -581,6 +580,8 @@ class AdamW(torch.optim.Optimizer):
                        masters=[st.get("master") for st in states], grad_scale=grad_scale,
                        seed=(self.seed + 0x9E3779B97F4A7C15 * step) & 0xFFFFFFFFFFFFFFFF
                        if self.stochastic else None, ordinals=ordinals)
+        for st in states:
+            st["step"] = step
 
     def load_state_dict(self, state_dict):
         """As torch's, but states keep their types (torch casts floating

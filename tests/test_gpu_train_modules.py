@@ -140,3 +140,16 @@ def test_changes_in_place_are_recorded(gpu):
         x = _randn(gpu, 32, 256, seed=1)
         fp8.rms_norm_fwd(x, torch.ones(256, device=gpu), residual=x.clone(), s=x)
     assert bool((q[0] < 1).all())
+
+
+def test_a_refused_step_changes_nothing(gpu):
+    """A wrong gradient scale is refused before any state moves on."""
+    p = torch.nn.Parameter(torch.ones(256, device=gpu))
+    opt = fp8.AdamW([p], lr=0.1)
+    p.grad = torch.ones_like(p)
+    opt.step()
+    before = p.detach().clone()
+    say("refused step")
+    with pytest.raises(ValueError):
+        opt.step(grad_scale=torch.ones(2, device=gpu))
+    assert torch.equal(p, before) and opt.state[p]["step"] == 1
