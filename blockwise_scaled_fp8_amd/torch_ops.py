@@ -585,10 +585,17 @@ class AdamW(torch.optim.Optimizer):
 
     def load_state_dict(self, state_dict):
         """As torch's, but states keep their types (torch casts floating
-        parameters' states to the parameter's type, which codes do not survive)."""
+        parameters' states to the parameter's type, which codes do not survive).
+        States must be of this optimizer's state_bits; masters that the
+        checkpoint lacks are made from the parameters."""
+        for st in state_dict["state"].values():
+            if st and ("exp_avg_root" in st) != (self.state_bits == 8):
+                raise ValueError(f"the checkpoint's states do not have state_bits={self.state_bits}")
         super().load_state_dict(state_dict)
         saved = [i for g in state_dict["param_groups"] for i in g["params"]]
         mine = [p for g in self.param_groups for p in g["params"]]
         for i, p in zip(saved, mine):
             for k, v in state_dict["state"].get(i, {}).items():
                 self.state[p][k] = v.detach().clone().to(p.device) if isinstance(v, torch.Tensor) else v
+            if self.state.get(p) and self.master_weights and p.dtype == torch.bfloat16:
+                self.state[p].setdefault("master", p.detach().float().contiguous())

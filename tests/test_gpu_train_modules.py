@@ -153,3 +153,28 @@ def test_a_refused_step_changes_nothing(gpu):
     with pytest.raises(ValueError):
         opt.step(grad_scale=torch.ones(2, device=gpu))
     assert torch.equal(p, before) and opt.state[p]["step"] == 1
+
+
+def test_checkpoints_of_other_settings(gpu):
+    """States of another width are refused; masters that a checkpoint does not
+    have are made from the parameters."""
+    def params():
+        return [torch.nn.Parameter(_randn(gpu, 300, seed=4))]
+
+    def stepped(**kw):
+        ps = params()
+        opt = fp8.AdamW(ps, lr=1e-2, **kw)
+        ps[0].grad = _randn(gpu, 300, seed=5)
+        opt.step()
+        return opt.state_dict(), ps
+    say("checkpoints")
+    for a, b in ((8, 32), (32, 8)):
+        with pytest.raises(ValueError, match="state_bits"):
+            fp8.AdamW(params(), state_bits=b).load_state_dict(stepped(state_bits=a)[0])
+    saved, ps = stepped(state_bits=32)
+    opt = fp8.AdamW(ps, lr=1e-2, master_weights=True)
+    opt.load_state_dict(saved)
+    assert torch.equal(opt.state[ps[0]]["master"], ps[0].detach().float())
+    ps[0].grad = _randn(gpu, 300, seed=6)
+    opt.step()
+    assert torch.equal(opt.state[ps[0]]["master"].bfloat16(), ps[0].detach())
