@@ -178,3 +178,40 @@ def test_checkpoints_of_other_settings(gpu):
     ps[0].grad = _randn(gpu, 300, seed=6)
     opt.step()
     assert torch.equal(opt.state[ps[0]]["master"].bfloat16(), ps[0].detach())
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sum"])
+def test_loss_in_a_graph(gpu, reduction):
+    """The reduced loss of many tokens and its gradients, captured: every
+    replay, with eager work in between, gives the eager values."""
+    T, V, K = 70000, 300, 64
+    h, w = _randn(gpu, T, K, seed=1).requires_grad_(), _randn(gpu, V, K, seed=2, std=0.2).requires_grad_()
+    target = torch.randint(0, V, (T,), generator=torch.Generator().manual_seed(3)).to(gpu)
+    target[::9] = -100
+
+    def work():
+        loss = fp8.linear_cross_entropy(h, w, target, reduction=reduction)
+        return (loss, *torch.autograd.grad(loss, (h, w)))
+    say("loss graph: eager")
+    eager = [t.detach().clone() for t in work()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    say("loss graph: capture")
+    with torch.cuda.graph(graph):
+        outs = [t.detach() for t in work()]
+    for rep in range(5):
+        for o in outs:
+            o.zero_()
+        work()
+        (torch.randn(3000000, device=gpu) * 2).sum()
+        torch.cuda.synchronize()
+        say("loss graph: replay", rep)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (o, e) in enumerate(zip(outs, eager)):
+            assert torch.equal(o, e), f"replay {rep}: output {i}"
