@@ -68,7 +68,7 @@ enum XentEpilogue {
 
 // What the tokens of a backward have in common.
 struct XentTokens {
-  float scale;                     // largest |dloss| of those that count
+  float scale;                     // largest finite |dloss| of those that count
   int masked;                      // one that has no gradient holds an infinity or NaN
   int pad[2];
   float zeros[4];
@@ -776,7 +776,7 @@ __global__ __launch_bounds__(1024) void xent_join_kernel(const float2* __restric
   }
 }
 
-// scale = max |dloss| over the tokens that count, and per token (lse, dloss /
+// scale = max finite |dloss| over the tokens that count, and per token (lse, dloss /
 // scale), the target column and, with the losses, the target's p - 1; ignored
 // and out-of-range targets get weight 0.
 // An infinity or NaN in a token's row of H makes every one of its logits
@@ -790,7 +790,8 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, const
   float m = 0.f;
   for (int t = threadIdx.x; t < T; t += 1024) {
     const int64_t y = target[t];
-    if (y != ignore_index && y >= 0 && y < V) m = fmaxf(m, fabsf(dloss[t]));
+    const float d = fabsf(dloss[t]);
+    if (y != ignore_index && y >= 0 && y < V && d < INFINITY) m = fmaxf(m, d);
   }
   m = wave_max(m);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
