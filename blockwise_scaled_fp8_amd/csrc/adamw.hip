@@ -27,8 +27,8 @@
 // block's scale takes does not hang on how an expression was compiled.
 //
 // Every element is read and written once; the kernel is bound by HBM: 336M bf16
-// parameters with 8-bit states 660 us (5.2 TB/s; 885 us with IEEE square root and
-// division and the rounding in integer arithmetic), with fp32 states and
+// parameters with 8-bit states 680 to 690 us (5.0 TB/s; 885 us with IEEE square
+// root and division and the rounding in integer arithmetic), with fp32 states and
 // masters 1810 us (5.2 TB/s).
 
 #include "device_common.h"
@@ -138,8 +138,8 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 // 8 values times 2^-exponent as E4M3 codes, magnitudes at most 448.  RANDOM:
 // v_cvt_sr_fp8_f32 adds its random number, aligned to the bits that the code
 // drops, and cuts: up with the probability of the remainder in units of
-// 2^-16, subnormal codes included (checked on the GPU against that definition
-// on a million values of 22 octaves).  `shift` picks the 16 random bits.
+// 2^-16, subnormal codes included (a test compares a million values of 22
+// octaves with that definition).  `shift` picks the 16 random bits.
 // KEEP: what is positive gets at least the smallest code; no NaN among f.
 // Infinite values (and NaN without KEEP) convert to the NaN code.
 template <bool RANDOM, bool KEEP>
@@ -227,8 +227,8 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamwLaunch L) {
     if constexpr (EIGHT) {
       // Hardware square root and reciprocal, each within 1 ulp (9.2e-8 and
       // 9.0e-8 measured): codes keep 4 bits and the step is far smaller than
-      // p, while the IEEE forms bind this kernel by its arithmetic (723
-      // against 655 us for 336M elements).  They do not take subnormals, which
+      // p, while the IEEE forms bind this kernel by its arithmetic (336M
+      // elements: 10% more time).  They do not take subnormals, which
       // get the IEEE root.  The same test finds the moments that are not finite
       // (an infinite or NaN gradient shows in v), which the scales leave out.
       rare = !(am < INFINITY);
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamwLaunch L) {
       store8_f32((float*)T.v + at, n, v);
     }
     // The parameter leaves before 8-bit states are encoded: 72 registers, 7
-    // waves a SIMD, instead of 81 and 5 (336M elements: 682 us, 736 us).
+    // waves a SIMD, instead of 81 and 5 (336M elements: 679 us, 736 us).
     if (T.master) store8_f32(T.master + at, n, p);
     if (T.flags & kAdamwParamF32) {
       store8_f32((float*)T.param + at, n, p);

@@ -136,7 +136,7 @@ __device__ __forceinline__ int row_slot() {
 // Forward, one row per TPR threads: thread t holds chunks t, t + TPR, .. of 8
 // columns, so a 16-lane DPP row holds one 1x128 block.  The row stays in
 // registers between the sum of squares and the outputs.  Bound by HBM: 16640 x
-// 8192 with residual and codes 152 us (6.3 TB/s); one row of 8192 2.8 us.
+// 8192 with residual and codes 151 to 155 us (6.2 TB/s); one row of 8192 3 us.
 template <int TPR, int CH>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_fwd_kernel(const NormFwdArgs p) {
   constexpr int BLOCK = TPR < 256 ? 256 : TPR;
@@ -292,9 +292,10 @@ __global__ __launch_bounds__(256) void rms_norm_quant_t_kernel(const NormFwdArgs
 // the workgroup writes one partial row at the end, which a second kernel sums
 // in order (30000 x 2048: 124 us with a partial row per four rows' threads).
 // While a row is reduced and written, the next row's s and dy are on their
-// way; rows stay packed in registers, and bf16 weights over all rows.  Bound by
-// HBM: 16640 x 8192 with dres 187 us (6.0 TB/s; 243 us without the next row's
-// loads in flight).
+// way; rows stay packed in registers, and bf16 weights over all rows, while
+// fp32 weights, twice as many registers, are loaded again.  Bound by HBM: 16640 x
+// 8192 with dres 188 us (6.0 TB/s; 243 us without the next row's loads in
+// flight), with an fp32 weight 210 us.
 template <int TPR, int CH, bool WF32>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_bwd_kernel(const NormBwdArgs p) {
   constexpr int BLOCK = TPR < 256 ? 256 : TPR;

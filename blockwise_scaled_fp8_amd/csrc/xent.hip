@@ -22,10 +22,12 @@
 // fp32 accumulators).  An operand's rows run along the contraction (H and W in
 // the logits, G in dH) or across it (W in dH; G and H in dW): the latter are
 // turned by transposing LDS reads, so nothing is ever transposed in memory.
-// The products are bound by the matrix cores from a few hundred tokens on, by
-// the reading of W below: 8192 tokens, 131072 x 4096, statistics 6.1 ms (1.44
-// PFLOP/s, matrix cores busy 72% of the cycles at the 1.9 GHz they are given),
-// G 6.5, dH and dW 13.0 ms; 33 tokens, 131072 x 5120, forward 223 us (6 TB/s).
+// From a few hundred tokens on the products run at 85 to 95% of a library
+// product's rate: 8192 tokens, 131072 x 4096, statistics 6.2 ms (1.42 PFLOP/s), G
+// 6.9, dH and dW 13.4 ms.  Matrix cores are busy 71%, 59% and 64% of the cycles
+// (at 1.9 GHz), and waves wait 33 to 43% of theirs for operands.  With few
+// tokens the reading of W bounds them: 33 tokens, 131072 x 5120, forward 223 us
+// (6 TB/s).
 //
 // Rounding: G is held as bf16, the accuracy of the matrix cores' operands.
 // It is formed with dloss divided by its largest magnitude, which the
@@ -334,9 +336,10 @@ struct Tile {
 // variable of its own and the stage loop is unrolled, so that the compiler
 // sees that reads of one stage do not depend on loads into another.
 //
-// 256 x 256 tiles (8 waves, two stages, all of a CU's LDS) read the fewest
-// operand bytes per product; 128 x 256 tiles (8 waves, three stages) do for 65
-// to 128 tokens.  64-row tiles (4 waves, two workgroups a CU) serve few tokens
+// 256 x 256 tiles (8 waves, two stages, 128 KB of a CU's 160 KB of LDS and up to
+// 17 KB for an epilogue: one workgroup a CU) read the fewest operand bytes per
+// product; 128 x 256 tiles (8 waves, three stages, 144 KB) do for 65 to 128
+// tokens.  64-row tiles (4 waves, two workgroups a CU) serve few tokens
 // or columns: 64 x 256 with two stages where W streams by, 64 x 128 with three
 // where a tile takes what the wait for its slabs takes.
 //
@@ -945,8 +948,9 @@ bool large_tiles(int64_t M, int64_t N, int64_t splits) {
 // Tiles of the logits: rows and columns.  Below the large ones, 128 rows for 65
 // to 128 tokens once the columns fill half the chip; else 64, with 256 columns
 // once these tiles fill the chip twice.  (100 tokens, 131072 x 5120: 261 us on
-// 128 rows, 331 us on 64.  33 tokens: 231 us with 256 columns, 246 us with 128;
-// a step of 128 tokens, 2048 x 512: 43 us with 128, 52 us with 256.)
+// 128 rows, 331 us on 64.  33 tokens: 246 us with 128 columns, 223 to 231 us with
+// 256; a step of 128 tokens, 2048 x 512: 43 us with 128, 52 us with 256.  Each
+// pair on one build.)
 struct TileShape {
   int rows, cols;
 };
