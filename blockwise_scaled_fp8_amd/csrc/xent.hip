@@ -22,10 +22,10 @@
 // fp32 accumulators).  An operand's rows run along the contraction (H and W in
 // the logits, G in dH) or across it (W in dH; G and H in dW): the latter are
 // turned by transposing LDS reads, so nothing is ever transposed in memory.
-// From a few hundred tokens on the products run at 85 to 95% of a library
-// product's rate: 8192 tokens, 131072 x 4096, statistics 6.2 ms (1.42 PFLOP/s), G
-// 6.9, dH and dW 13.4 ms.  Matrix cores are busy 71%, 59% and 64% of the cycles
-// (at 1.9 GHz), and waves wait 33 to 43% of theirs for operands.  With few
+// From a few hundred tokens on the products run at 90 to 95% of a library
+// product's rate: 8192 tokens, 131072 x 4096, statistics 6.1 to 6.2 ms (1.43
+// PFLOP/s), G 6.6, dH and dW 12.9 to 13.4 ms.  Matrix cores are busy 70%, 60% and
+// 64% of the cycles (at 1.9 GHz), and waves wait 35 to 43% of theirs for operands.  With few
 // tokens the reading of W bounds them: 33 tokens, 131072 x 5120, forward 223 us
 // (6 TB/s).
 //
@@ -39,8 +39,8 @@
 // them) times the target's row of W are taken out of dH in the end, which
 // makes dH[t] = sum_v G[t, v] (W[v] - W[target]), where only the rows'
 // differences meet G's rounding (and a target's own entry does not matter).
-// 0.9% of a step of 8192 tokens, 131072 x 4096 (25.9 to 26.1 ms); with sums
-// added up in memory by each wave 2%.
+// With sums added up in memory by each wave a step of 8192 tokens, 131072 x
+// 4096, takes 1.5% longer.
 
 #include <type_traits>
 
@@ -76,6 +76,15 @@ struct XentTokens {
   float zeros[4];
 };
 
+// A token of the backward.
+struct alignas(16) XentRow {
+  float lse;
+  float weight;                    // dloss / scale; 0: it has no gradient
+  float entry;                     // p - 1 of its target, or kNoEntry: exp(z - lse) - 1
+  int target;                      // column of the whole vocabulary, or -1
+};
+constexpr float kNoEntry = 2.f;
+
 struct XentGemm {
   // Operands by rows of ld bytes: [M or N][contraction], or, for the kernel's
   // KM operands, [contraction][M or N].  a_rows, b_rows: the rows that exist;
@@ -93,9 +102,7 @@ struct XentGemm {
   const int64_t* target;
   float* target_logit;             // [M]
   // kGrad
-  const float2* row;               // [M], kOut [contraction]: (lse, dloss / scale)
-  const int* local_target;         // [M] target column of the whole vocabulary, or -1
-  const float* target_grad;        // [M] p - 1 of the target, or nullptr: from lse
+  const XentRow* row;              // [M], kOut [contraction]
   int v0;                          // first vocabulary column of this piece
   float* sums;                     // [tiles_n][a_rows] sums of G's rounded rows over a tile, or nullptr
   // outputs
@@ -185,7 +192,7 @@ struct SlabLoader {
   int rows, lrow, wave, edge;   // KM: contraction rows; else the load number that holds the last row, -1: all exist
   __amdgpu_buffer_rsrc_t rsrc;
   const XentTokens* tokens;     // MASK
-  const float2* row;
+  const XentRow* row;
   bool masked;
 
   static __device__ __forceinline__ bool upper(int i) { return LW * RPL < 32 && (LW * RPL * i >> 4) & 1; }
@@ -252,7 +259,7 @@ struct SlabLoader {
 #pragma unroll 1
       for (int i = 0; i < N; ++i) {
         const int t = kb * 64 + RPL * (wave + LW * i) + lrow;
-        const bool live = t < rows && row[min(t, rows - 1)].y != 0.f;
+        const bool live = t < rows && row[min(t, rows - 1)].weight != 0.f;
         const uint8_t* const from =
             live ? base + (int64_t)t * ld + (upper(i) ? col1 : col0) : (const uint8_t*)tokens->zeros;
         __builtin_amdgcn_global_load_lds((global_void*)(uintptr_t)from, (lds_void*)(lds + to), 16, 0, 0);
@@ -416,10 +423,17 @@ __device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         const int r = min(t.m0 + wm0 + 16 * i + frow, p.a_rows - 1);
-        const int64_t y = (EPI == kGrad ? (int64_t)p.local_target[r] - p.v0 : p.target[r]) - (t.n0 + wn0);
+        int64_t y;
+        if constexpr (EPI == kGrad) {
+          const XentRow e = p.row[r];
+          info[i] = make_float2(e.lse, e.weight);
+          y = (int64_t)e.target - p.v0;
+        } else {
+          y = p.target[r];
+        }
+        y -= t.n0 + wn0;
         tgt[i] = y >= 0 && y < WN ? (int)y : -1;
         if constexpr (EPI == kGrad) {
-          info[i] = p.row[r];
           if (t.m0 + wm0 + 16 * i + frow >= p.a_rows) info[i].y = 0.f;
         }
       }
@@ -573,12 +587,14 @@ __device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t
             for (int v = 0; v < 4; ++v)
               acc[i][j][v] = __builtin_amdgcn_exp2f((acc[i][j][v] - info[i].x) * kLog2e);
           if (__builtin_amdgcn_ballot_w64(tgt[i] >= 0)) {
+            int r = min(row0 + 16 * i, p.a_rows - 1);
+            asm volatile("" : "+v"(r));   // formed here, not for all rows ahead
+            const float entry = p.row[r].entry;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
               for (int v = 0; v < 4; ++v)
-                if (16 * j + 4 * fq + v == tgt[i])
-                  acc[i][j][v] = p.target_grad ? p.target_grad[min(row0 + 16 * i, p.a_rows - 1)] : acc[i][j][v] - 1.f;
+                if (16 * j + 4 * fq + v == tgt[i]) acc[i][j][v] = entry == kNoEntry ? acc[i][j][v] - 1.f : entry;
           }
         }
         const float f = EPI == kGrad ? info[i].y : scale;
@@ -604,17 +620,20 @@ __device__ __forceinline__ void xent_tiles(const XentGemm& p, int block, uint8_t
       };
       // Thread `r` of the last BM joins row r's 4 WGN shares.  What an earlier
       // piece left is read before the epilogue's work.
-      const int sum_row = (int)threadIdx.x - (64 * NW - BM);
+      auto sum_row = [&]() __attribute__((always_inline)) {
+        int r = (int)threadIdx.x - (64 * NW - BM);
+        asm volatile("" : "+v"(r));
+        return EPI == kGrad && p.sums && r >= 0 && d.m0 + r < p.a_rows ? r : -1;
+      };
       float sum = 0.f;
-      float* const sum_at = p.sums + (int64_t)d.tn * p.a_rows + d.m0 + sum_row;
-      const bool sums = EPI == kGrad && p.sums && sum_row >= 0 && d.m0 + sum_row < p.a_rows;
-      if (sums && p.add) sum = *sum_at;
+      if (const int r = sum_row(); p.add && r >= 0) sum = p.sums[(int64_t)d.tn * p.a_rows + d.m0 + r];
       auto join = [&]() __attribute__((always_inline)) {
-        if (!sums) return;
+        const int r = sum_row();
+        if (r < 0) return;
         float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4 * WGN; ++k) s += ((const float*)sE)[k * SUM_LD + sum_row];
-        *sum_at = sum + s;
+        for (int k = 0; k < 4 * WGN; ++k) s += ((const float*)sE)[k * SUM_LD + r];
+        p.sums[(int64_t)d.tn * p.a_rows + d.m0 + r] = sum + s;
       };
       if constexpr (STAGED) {
         // Through LDS, so that every store writes whole lines (in the MFMA
@@ -779,16 +798,14 @@ __global__ __launch_bounds__(1024) void xent_join_kernel(const float2* __restric
   }
 }
 
-// scale = max finite |dloss| over the tokens that count, and per token (lse, dloss /
-// scale), the target column and, with the losses, the target's p - 1; ignored
-// and out-of-range targets get weight 0.
+// scale = max finite |dloss| over the tokens that count, and the tokens' rows;
+// ignored and out-of-range targets get weight 0.
 // An infinity or NaN in a token's row of H makes every one of its logits
 // infinite or NaN, and so its lse.
 __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, const int64_t* __restrict__ target,
                                                          int64_t ignore_index, const float* __restrict__ dloss,
                                                          const float* __restrict__ lse, const float* __restrict__ loss,
-                                                         float2* __restrict__ row, int* __restrict__ local_target,
-                                                         float* __restrict__ target_grad, XentTokens* __restrict__ tokens) {
+                                                         XentRow* __restrict__ row, XentTokens* __restrict__ tokens) {
   __shared__ float red[16];
   float m = 0.f;
   for (int t = threadIdx.x; t < T; t += 1024) {
@@ -805,11 +822,13 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(int T, int64_t V, const
   for (int t = threadIdx.x; t < T; t += 1024) {
     const int64_t y = target[t];
     const bool counts = y != ignore_index && y >= 0 && y < V;
-    const float2 r = make_float2(lse[t], counts && dloss[t] != 0.f ? dloss[t] / m : 0.f);
+    XentRow r;
+    r.lse = lse[t];
+    r.weight = counts && dloss[t] != 0.f ? dloss[t] / m : 0.f;
+    r.entry = loss ? expm1f(-loss[t]) : kNoEntry;
+    r.target = counts ? (int)y : -1;
     row[t] = r;
-    local_target[t] = counts ? (int)y : -1;
-    if (loss) target_grad[t] = expm1f(-loss[t]);
-    masked |= r.y == 0.f && !(fabsf(r.x) < INFINITY);
+    masked |= r.weight == 0.f && !(fabsf(r.lse) < INFINITY);
   }
   const int any = __syncthreads_or(masked);
   if (threadIdx.x == 0) *tokens = XentTokens{m, any, {0, 0}, {0.f, 0.f, 0.f, 0.f}};
@@ -870,24 +889,22 @@ __global__ __launch_bounds__(1024) void xent_few_stats_kernel(const float* __res
 // G from shares of the logits, [splits][T][ld]; zeros past T and V.  sums: a
 // workgroup's of G's rounded row.
 __global__ __launch_bounds__(256) void xent_few_grad_kernel(const float* __restrict__ z, int splits, int T, int V,
-                                                            int ld, const float2* __restrict__ row,
-                                                            const int* __restrict__ local_target,
-                                                            const float* __restrict__ target_grad, int v0,
+                                                            int ld, const XentRow* __restrict__ row, int v0,
                                                             uint16_t* __restrict__ g, int64_t ld_g,
                                                             float* __restrict__ sums) {
   __shared__ float red[4];
   const int t = blockIdx.x, c = 4 * (blockIdx.y * 256 + threadIdx.x);
   uint2 w = make_uint2(0, 0);
-  const float2 info = t < T ? row[t] : make_float2(0.f, 0.f);
-  if (info.y != 0.f && c < ld) {
+  const XentRow info = t < T ? row[t] : XentRow{0.f, 0.f, 0.f, -1};
+  if (info.weight != 0.f && c < ld) {
     const float4 e = sum_shares(z + (int64_t)t * ld, c, splits, (int64_t)T * ld);
     float p[4] = {e.x, e.y, e.z, e.w};
-    const int y = local_target[t] - v0;
+    const int y = info.target - v0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      p[i] = __builtin_amdgcn_exp2f((p[i] - info.x) * kLog2e);
-      if (c + i == y) p[i] = target_grad ? target_grad[t] : p[i] - 1.f;
-      p[i] = c + i < V ? p[i] * info.y : 0.f;
+      p[i] = __builtin_amdgcn_exp2f((p[i] - info.lse) * kLog2e);
+      if (c + i == y) p[i] = info.entry == kNoEntry ? p[i] - 1.f : info.entry;
+      p[i] = c + i < V ? p[i] * info.weight : 0.f;
     }
     w = make_uint2(pack_bf16x2_rne(p[0], p[1]), pack_bf16x2_rne(p[2], p[3]));
   }
@@ -910,8 +927,7 @@ __global__ __launch_bounds__(256) void zero_columns_kernel(uint16_t* out, int64_
 // columns a workgroup.
 __global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ acc, int splits, int64_t T,
                                                       int64_t K, const XentTokens* __restrict__ tokens,
-                                                      const float2* __restrict__ row,
-                                                      const int* __restrict__ target,
+                                                      const XentRow* __restrict__ row,
                                                       const float* __restrict__ sums, int parts,
                                                       const uint16_t* __restrict__ w, int64_t ld_w,
                                                       uint16_t* __restrict__ dh, int64_t ld_dh) {
@@ -926,8 +942,8 @@ __global__ __launch_bounds__(256) void xent_dh_kernel(const float* __restrict__ 
     if (c < K) s = sum_shares(acc + t * K, c, splits, T * K);
     const float off = block_sum(part, red[flip]);
     if (c >= K) continue;
-    if (row[t].y != 0.f) {   // else G is zero, and W's row may be anything
-      const uint2 u = *(const uint2*)(w + target[t] * ld_w + c);
+    if (row[t].weight != 0.f) {   // else G is zero, and W's row may be anything
+      const uint2 u = *(const uint2*)(w + row[t].target * ld_w + c);
       s.x -= off * bf16lo(u.x); s.y -= off * bf16hi(u.x);
       s.z -= off * bf16lo(u.y); s.w -= off * bf16hi(u.y);
     }
@@ -1062,7 +1078,7 @@ struct XentLayout {
   int z_splits;                // of the logits'; 1: their tiles take all of it
   TileShape grad_tile;         // of G's product, the same in all pieces
   int parts;                   // sums a row of G: one per tile of a piece; every piece adds to the first one's
-  size_t z, part, logit, row, target, target_grad, tokens, sums, g, acc, total;
+  size_t z, part, logit, row, tokens, sums, g, acc, total;
 };
 
 XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
@@ -1107,9 +1123,7 @@ XentLayout xent_layout(int64_t T, int64_t V, int64_t K, bool backward) {
     L.splits = (int)n_splits;
     if (gradient_tiles(T, K, n_splits).rows == t.rows) break;   // as the launch will choose
   }
-  L.row = take((size_t)T * sizeof(float2));
-  L.target = take((size_t)T * 4);
-  L.target_grad = take((size_t)T * 4);
+  L.row = take((size_t)T * sizeof(XentRow));
   L.tokens = take(sizeof(XentTokens));
   L.grad_tile = logit_tiles(L.tp, pad64(piece));
   const int sum_cols = L.z_splits > 1 ? 1024 : L.grad_tile.cols;
@@ -1161,15 +1175,13 @@ hipError_t launch_xent_fwd(const XentArgs& p, void* ws, hipStream_t stream) {
 hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
   const XentLayout L = xent_layout(p.T, p.V, p.K, true);
   uint8_t* const base = (uint8_t*)ws;
-  float2* const row = (float2*)(base + L.row);
-  int* const target = (int*)(base + L.target);
-  float* const target_grad = p.nll ? (float*)(base + L.target_grad) : nullptr;
+  XentRow* const row = (XentRow*)(base + L.row);
   XentTokens* const tokens = (XentTokens*)(base + L.tokens);
   float* const sums = p.dh ? (float*)(base + L.sums) : nullptr;
   uint16_t* const g = (uint16_t*)(base + L.g);
   float* const acc = (float*)(base + L.acc);
   hipLaunchKernelGGL(xent_rows_kernel, dim3(1), dim3(1024), 0, stream, (int)p.T, p.V, p.target,
-                     p.ignore_index, p.dloss, p.lse, p.nll, row, target, target_grad, tokens);
+                     p.ignore_index, p.dloss, p.lse, p.nll, row, tokens);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   for (int64_t v0 = 0; v0 < p.V; v0 += L.piece) {
@@ -1182,15 +1194,14 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
     // no gradient: zeros.
     z.M = (int)L.tp; z.N = (int)pad64(nv); z.kblocks = (int)(p.K / 64);
     z.a_rows = (int)p.T; z.b_rows = (int)nv;
-    z.row = row; z.local_target = target; z.target_grad = target_grad; z.v0 = (int)v0;
+    z.row = row; z.v0 = (int)v0;
     z.out = g; z.ldo = L.ld_g;
     z.sums = sums; z.add = v0 > 0;
     if (L.z_splits > 1) {
       float* const shares = (float*)(base + L.z);
       if ((e = run_logit_shares(z, L.z_splits, shares, stream)) != hipSuccess) return e;
       hipLaunchKernelGGL(xent_few_grad_kernel, dim3((unsigned)L.tp, (unsigned)((z.N + 1023) / 1024)), dim3(256), 0,
-                         stream, shares, L.z_splits, (int)p.T, (int)nv, z.N, row, target, target_grad, (int)v0, g,
-                         L.ld_g, sums);
+                         stream, shares, L.z_splits, (int)p.T, (int)nv, z.N, row, (int)v0, g, L.ld_g, sums);
       e = hipGetLastError();
     } else {
       e = run_gemm<kGrad>(z, L.grad_tile, 1, stream);
@@ -1214,7 +1225,7 @@ hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream) {
   if (!p.dh) return hipSuccess;
   const unsigned wide = (unsigned)((p.K + 1023) / 1024);   // at most 2^10
   hipLaunchKernelGGL(xent_dh_kernel, dim3((unsigned)(p.T < (1 << 20) ? p.T : (1 << 20)), wide), dim3(256), 0, stream,
-                     acc, L.splits, p.T, p.K, tokens, row, target, sums, L.parts, (const uint16_t*)p.w, p.ld_w,
+                     acc, L.splits, p.T, p.K, tokens, row, sums, L.parts, (const uint16_t*)p.w, p.ld_w,
                      (uint16_t*)p.dh, p.ld_dh);
   return hipGetLastError();
 }
