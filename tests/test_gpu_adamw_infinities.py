@@ -50,7 +50,7 @@ def test_neighbours_of_infinities(gpu, seed):
     assert torch.equal(clean[3], got[3]) and torch.equal(clean[4], got[4])
     decoded = [e4m3.decode(t.numpy()) for t in got[1:3]]
     for i in BAD:
-        assert np.isnan(got[0][i]) and np.isnan(decoded[0][i]) and np.isnan(decoded[1][i]), i
+        assert bool(got[0][i].isnan()) and np.isnan(decoded[0][i]) and np.isnan(decoded[1][i]), i
 
 
 @pytest.mark.parametrize("seed", [None, 17])
