@@ -26,6 +26,13 @@ class AdamwTensor(ctypes.Structure):
                 ("numel", c_i64), ("param_dtype", c_int), ("grad_dtype", c_int)]
 
 
+class Layouts(ctypes.Structure):
+    """fp8bw_layouts of include/fp8bw.h."""
+    _fields_ = [("y", c_ptr), ("ld_y", c_i64), ("q", c_ptr), ("ld_q", c_i64), ("recip", c_ptr),
+                ("rs_row", c_i64), ("rs_kb", c_i64), ("qt", c_ptr), ("ld_qt", c_i64),
+                ("recip_t", c_ptr), ("rst_row", c_i64), ("rst_kb", c_i64)]
+
+
 # name -> (restype, argtypes), mirroring include/fp8bw.h
 PROTOTYPES = {
     "fp8bw_abi_version": (c_int, []),
@@ -91,6 +98,25 @@ PROTOTYPES = {
                                            c_ptr, c_size, c_ptr]),
     "fp8bw_adamw_step": (c_int, [ctypes.POINTER(AdamwTensor), c_int, c_int, c_i64, c_f64, c_f64,
                                  c_f64, c_f64, c_f64, c_ptr, c_int, c_u64, c_ptr]),
+    "fp8bw_moe_rows": (c_i64, [c_i64, c_i64, c_i64, c_i64]),
+    "fp8bw_moe_sort_ws_bytes": (c_size, [c_i64, c_i64, c_i64]),
+    "fp8bw_moe_sort": (c_int, [c_ptr, c_int, c_i64, c_i64, c_i64, c_i64, c_i64, c_ptr, c_ptr, c_ptr,
+                               c_ptr, c_size, c_ptr]),
+    "fp8bw_moe_gather": (c_int, [c_ptr, c_i64, c_i64, c_i64, c_ptr, c_ptr, c_i64, c_i64,
+                                 ctypes.POINTER(Layouts), c_ptr]),
+    "fp8bw_moe_combine": (c_int, [c_ptr, c_i64, c_ptr, c_int, c_i64, c_i64, c_ptr, c_i64, c_i64,
+                                  c_ptr, c_i64, c_ptr]),
+    "fp8bw_moe_combine_bwd": (c_int, [c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_int, c_i64, c_i64, c_ptr,
+                                      c_ptr, c_i64, c_i64, ctypes.POINTER(Layouts), c_ptr, c_ptr]),
+    "fp8bw_swiglu_fwd": (c_int, [c_ptr, c_i64, c_i64, c_i64, ctypes.POINTER(Layouts), c_ptr, c_i64,
+                                 c_ptr, c_i64, c_i64, c_ptr]),
+    "fp8bw_swiglu_bwd": (c_int, [c_ptr, c_i64, c_ptr, c_i64, c_ptr, c_i64, c_i64, c_i64, c_i64,
+                                 ctypes.POINTER(Layouts), c_ptr, c_i64, c_ptr, c_i64, c_i64, c_ptr]),
+    "fp8_scaled_grouped_gemm_blockwise_wgrad": (c_int, [c_ptr, c_i64, c_ptr, c_i64, c_i64, c_ptr, c_i64,
+                                                        c_ptr, c_i64, c_i64, c_int, c_ptr, c_i64, c_i64,
+                                                        c_i64, c_ptr, c_i64, c_i64, c_int, c_ptr]),
+    "fp8_blockwise_quant_grouped": (c_int, [c_ptr, c_i64, c_i64, c_i64, c_i64, c_int, c_int, c_ptr,
+                                            c_i64, c_i64, c_ptr, c_i64, c_i64, c_i64, c_ptr]),
 }
 
 STATUS = {0: "FP8BW_OK", 1: "FP8BW_ERR_NULL", 2: "FP8BW_ERR_SHAPE", 3: "FP8BW_ERR_LAYOUT",

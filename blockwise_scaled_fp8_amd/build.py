@@ -23,8 +23,8 @@ LIB = os.path.join(HERE, "libfp8bw.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["quant.hip", "gemm.hip", "rmsnorm.hip", "xent.hip", "adamw.hip", "api.cpp",
-           "train_api.cpp"]
+SOURCES = ["quant.hip", "gemm.hip", "rmsnorm.hip", "xent.hip", "adamw.hip", "moe.hip", "swiglu.hip", "api.cpp",
+           "train_api.cpp", "moe_api.cpp"]
 # Per-source extra flags.  gemm.hip, xent.hip: select the VGPR form of MFMA so
 # that the rescale's and the epilogues' VALU read the MFMA results without
 # AGPR->VGPR copies.

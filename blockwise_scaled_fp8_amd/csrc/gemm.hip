@@ -83,7 +83,20 @@ struct GemmArgs {
   // pieces and workgroup order as the separate split launch); 0: none.
   int rounds;
   int tail_pieces, tail_kbps, tail_base, tail_tiles;
+  // Weight gradients of a grouped GEMM (KGROUP kernels): `groups` row-major
+  // [M, N] outputs out_s_group elements apart, group g contracting the K
+  // blocks [group_end[g-1] / 128, group_end[g] / 128); `groups` stays 0 in the
+  // kernels that split rows.
+  int64_t out_s_group;
 };
+
+// The K blocks of group g of a weight gradient, clamped so that no table can
+// name a block outside the operands.
+__device__ __forceinline__ void group_kblocks(const GemmArgs& p, int g, int* begin, int* end) {
+  const int b = g == 0 ? 0 : p.group_end[g - 1] / 128;
+  *begin = max(0, min(b, p.kblocks));
+  *end = max(*begin, min(p.group_end[g] / 128, p.kblocks));
+}
 
 // A grouped GEMM on the large tiles runs as two launches: the large-tile
 // kernel takes every group's whole 256-row tiles, and its last partial tile
@@ -211,7 +224,7 @@ __device__ __forceinline__ v8i load_frag_at(const uint8_t* tile, uint32_t lo, ui
 template <int BM, int OUT>
 __device__ __forceinline__ bool locate_group_tile(GemmArgs& p, int t, int* tm, int* tn, int* row0);
 
-template <int BM, int BN, int MODE, int OUT, bool SPLIT>
+template <int BM, int BN, int MODE, int OUT, bool SPLIT, bool KGROUP = false>
 __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs p_in) {
   constexpr int WM = BM / 2, WN = BN / 2;
   constexpr int TM = WM / 16, TN = WN / 16;
@@ -229,7 +242,10 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs p_in) {
   const int wm0 = (wave >> 1) * WM, wn0 = (wave & 1) * WN;
   GemmArgs p = p_in;
   int tm, tn;
-  if (p.groups > 0) {
+  if constexpr (KGROUP) {
+    tm = blockIdx.x % (p.tiles_m * p.tiles_n) / p.tiles_n;
+    tn = blockIdx.x % p.tiles_n;
+  } else if (p.groups > 0) {
     // Grouped GEMM: p now addresses this tile's group (rows clamp to it).
     if (p.group_part == 2 && !grouped_split_pays(p)) return;
     int row0;
@@ -239,8 +255,13 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs p_in) {
     tn = blockIdx.x - tm * p.tiles_n;
   }
   const int m0 = tm * BM, n0 = tn * BN;
-  const int kb_begin = blockIdx.y * p.kb_per_split;
-  const int kb_end = min(p.kblocks, kb_begin + p.kb_per_split);
+  int kb_begin = blockIdx.y * p.kb_per_split;
+  int kb_end = min(p.kblocks, kb_begin + p.kb_per_split);
+  if constexpr (KGROUP) {
+    const int g = blockIdx.x / (p.tiles_m * p.tiles_n);
+    group_kblocks(p, g, &kb_begin, &kb_end);
+    p.out = (uint8_t*)p.out + g * p.out_s_group * (OUT == kOutBf16 ? 2 : 4);
+  }
 
   // Loader mapping: chunk (row = tid/8 + 32 i, 16-byte column tid%8).
   const int lrow = tid >> 3, lc = tid & 7;
@@ -791,7 +812,7 @@ __device__ __forceinline__ bool locate_group_tile(GemmArgs& p, int t, int* tm, i
 }
 
 template <int BM, int BN, int WGM, int WGN, int STAGES, int MODE, int OUT, bool SPLIT,
-          bool BKN = false, bool PERSIST = false>
+          bool BKN = false, bool PERSIST = false, bool KGROUP = false>
 __global__ __launch_bounds__(64 * WGM * WGN) void gemm_v2_kernel(const GemmArgs p_in) {
   constexpr int NW = WGM * WGN;
   constexpr int WM = BM / WGM, WN = BN / WGN;
@@ -864,7 +885,14 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_v2_kernel(const GemmArgs 
   const int gx = gridDim.x * rounds;
   const int nwg = gx * gridDim.y;
   int wg;
-  if (p.groups > 0) {
+  int kgroup = 0;
+  if constexpr (KGROUP) {
+    // One group's tiles after the other, each group dealt over all XCDs: with
+    // a run of groups per XCD, the XCD of the longest ones finished last.
+    const int tiles = p.tiles_m * p.tiles_n;
+    kgroup = blockIdx.x / tiles;
+    wg = xcd_remap(blockIdx.x - kgroup * tiles, tiles);
+  } else if (p.groups > 0) {
     if (p.group_part == 1 && !grouped_split_pays(p)) p.group_part = 0;
     const int T = grouped_tile_count<BM>(p);
     constexpr int kXcds = 8;
@@ -901,8 +929,12 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_v2_kernel(const GemmArgs 
   }
   const int m0 = tm * BM, n0 = tn * BN;
   const int nl = min(n0, p.N - BN);
-  const int kb_begin = split * p.kb_per_split;
-  const int kb_end = min(p.kblocks, kb_begin + p.kb_per_split);
+  int kb_begin = split * p.kb_per_split;
+  int kb_end = min(p.kblocks, kb_begin + p.kb_per_split);
+  if constexpr (KGROUP) {
+    group_kblocks(p, kgroup, &kb_begin, &kb_end);
+    p.out = (uint8_t*)p.out + kgroup * p.out_s_group * (OUT == kOutBf16 ? 2 : 4);
+  }
 
   // Per-lane byte offsets of this wave's first row octets of A and B.  Lane
   // 8q + c of a direct-load instruction fills physical chunk c of row 8o + q
@@ -1788,6 +1820,78 @@ hipError_t launch_grouped_gemm(const GemmProblem& p, int groups, const int* grou
   s2.tiles_n = (int)((p.N + 63) / 64);
   s2.tiles_m = 2 * groups;   // grid only
   return launch_mode<64, 64>(s2, p.mode, 1, p.out_kind, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Weight gradients of a grouped GEMM: one [M, N] product per group over the
+// group's K blocks (GemmArgs::out_s_group), all in one launch.
+static int grouped_wgrad_config(const GemmProblem& p, int groups) {
+  const int64_t cus = num_cus();
+  auto fills = [&](int c) {
+    return groups * ((p.M + kCfgs[c].bm - 1) / kCfgs[c].bm) * ((p.N + kCfgs[c].bn - 1) / kCfgs[c].bn) >= cus;
+  };
+  if (gemm_config_ok(p, 3) && fills(3)) return 3;
+  if (gemm_config_ok(p, 2) && fills(2)) return 2;
+  return p.M >= 128 && p.N >= 128 && fills(0) ? 0 : 1;
+}
+
+bool grouped_wgrad_ok(const GemmProblem& p, int groups) {
+  const int cfg = grouped_wgrad_config(p, groups);
+  // fewer than 2^32 threads a launch, at most 512 a workgroup
+  return groups * ((p.M + kCfgs[cfg].bm - 1) / kCfgs[cfg].bm) * ((p.N + kCfgs[cfg].bn - 1) / kCfgs[cfg].bn) <
+         (int64_t)1 << 23;
+}
+
+template <int OUT>
+static void launch_wgrad_cfg(int cfg, const GemmArgs& a, dim3 grid, hipStream_t stream) {
+  constexpr int MODE = kBlockB1x128;
+  switch (cfg) {
+    case 3:
+      hipLaunchKernelGGL((gemm_v2_kernel<256, 256, 2, 4, 2, MODE, OUT, false, false, false, true>), grid, dim3(512), 0,
+                         stream, a);
+      break;
+    case 2:
+      hipLaunchKernelGGL((gemm_v2_kernel<256, 128, 2, 2, 3, MODE, OUT, false, false, false, true>), grid, dim3(256), 0,
+                         stream, a);
+      break;
+    case 0:
+      hipLaunchKernelGGL((gemm_kernel<128, 128, MODE, OUT, false, true>), grid, dim3(256), 0, stream, a);
+      break;
+    default:
+      hipLaunchKernelGGL((gemm_kernel<64, 64, MODE, OUT, false, true>), grid, dim3(256), 0, stream, a);
+  }
+}
+
+hipError_t launch_grouped_wgrad(const GemmProblem& p, int groups, const int* group_end, int64_t out_s_group,
+                                hipStream_t stream) {
+  const int cfg = grouped_wgrad_config(p, groups);
+  GemmArgs a = {};
+  a.a = (const uint8_t*)p.a;
+  a.b = (const uint8_t*)p.b;
+  a.ra = p.ra;
+  a.rb = p.rb;
+  a.out = p.out;
+  a.lda = p.lda;
+  a.ldb = p.ldb;
+  a.ldo = p.ldo;
+  a.ra_s_row = p.ra_s_row;
+  a.ra_s_kb = p.ra_s_kb;
+  a.rb_s_row = p.rb_s_row;
+  a.rb_s_kb = p.rb_s_kb;
+  a.M = (int)p.M;
+  a.N = (int)p.N;
+  a.K = (int)p.K;
+  a.kblocks = (int)(p.K / 128);
+  a.kb_per_split = a.kblocks;
+  a.tiles_m = (int)((p.M + kCfgs[cfg].bm - 1) / kCfgs[cfg].bm);
+  a.tiles_n = (int)((p.N + kCfgs[cfg].bn - 1) / kCfgs[cfg].bn);
+  a.rounds = 1;
+  a.group_end = group_end;
+  a.out_s_group = out_s_group;
+  const dim3 grid((unsigned)(groups * a.tiles_m * a.tiles_n));
+  if (p.out_kind == kOutBf16) launch_wgrad_cfg<kOutBf16>(cfg, a, grid, stream);
+  else launch_wgrad_cfg<kOutF32>(cfg, a, grid, stream);
+  return hipGetLastError();
 }
 
 }  // namespace fp8bw

@@ -33,6 +33,12 @@ hipError_t launch_quant_dual(const void* x, int64_t rows, int64_t cols, int64_t 
                              void* q, int64_t ld_q, float* recip, int64_t rs_row, int64_t rs_kb,
                              void* qt, int64_t ld_qt, float* recip_t, int64_t rst_row,
                              int64_t rst_kb, bool stream_t, hipStream_t stream);
+// launch_quant_128x128 of `groups` matrices, x_group, q_group and rs_group
+// elements apart.
+hipError_t launch_quant_128x128_grouped(const void* x, int64_t rows, int64_t cols, int64_t ld_x, int64_t x_group,
+                                        int groups, int transpose, void* q, int64_t ld_q, int64_t q_group,
+                                        float* recip, int64_t rs_row, int64_t rs_kb, int64_t rs_group,
+                                        hipStream_t stream);
 // Per-tensor: partial amax into ws (n_partials floats, at most
 // kMaxTensorwisePartials), then quantize.
 constexpr int kMaxTensorwisePartials = 1024;
@@ -85,12 +91,17 @@ struct GemmPlan {
 // (no tail split); splits == 0 lets the plan choose when allow_split.
 GemmPlan gemm_plan(const GemmProblem& p, int config, int splits, bool allow_split);
 hipError_t launch_gemm(const GemmProblem& p, const GemmPlan& plan, void* ws, hipStream_t stream);
-// Fill a contiguous bf16 [rows, cols] matrix with +0.
 // Grouped blockwise GEMM: row groups of A / out ending at device int32
 // group_end[g] (cumulative), each with B + g*b_s_group and rb + g*rb_s_group.
 bool grouped_gemm_ok(const GemmProblem& p, int groups);
 hipError_t launch_grouped_gemm(const GemmProblem& p, int groups, const int* group_end,
                                int64_t b_s_group, int64_t rb_s_group, hipStream_t stream);
+// Weight gradients: out + g*out_s_group = A . B^T over the K blocks
+// [group_end[g-1] / 128, group_end[g] / 128), mode kBlockB1x128.
+bool grouped_wgrad_ok(const GemmProblem& p, int groups);
+hipError_t launch_grouped_wgrad(const GemmProblem& p, int groups, const int* group_end, int64_t out_s_group,
+                                hipStream_t stream);
+// Fill a contiguous bf16 [rows, cols] matrix with +0.
 hipError_t launch_zero_bf16(void* out, int64_t rows, int64_t cols, hipStream_t stream);
 
 // ---- RMS norm (rmsnorm.hip) ----
@@ -177,5 +188,73 @@ hipError_t launch_xent_fwd(const XentArgs& p, void* ws, hipStream_t stream);
 hipError_t launch_xent_bwd(const XentArgs& p, void* ws, hipStream_t stream);
 // +0 in a bf16 [rows, cols] matrix of leading dimension ld.
 hipError_t launch_zero_rows_bf16(void* out, int64_t rows, int64_t cols, int64_t ld, hipStream_t stream);
+
+// ---- mixture of experts (moe.hip) ----
+// A [rows, cols] result as bf16, as E4M3 codes in 1x128 blocks along the
+// columns, and as codes of the transpose in 1x128 blocks along the rows; a
+// nullptr is not written.
+struct LayoutsOut {
+  uint16_t* y; int64_t ld_y;
+  uint8_t* q; int64_t ld_q; float* recip; int64_t rs_row, rs_kb;
+  uint8_t* qt; int64_t ld_qt; float* recip_t; int64_t rst_row, rst_kb;
+};
+// Slots sorted by expert, as fp8bw_moe_sort writes them.
+struct MoeTable {
+  int64_t tokens, rows;
+  int topk;
+  const int* row;      // [tokens, topk]: row of a slot, or outside [0, rows)
+  const int* source;   // [rows]: slot of a row, or negative
+};
+struct MoeSortArgs {
+  const void* expert; int wide;   // int64 (wide) or int32 [n]
+  int64_t n;
+  int experts, align;
+  int64_t rows;
+  int *row, *source, *group_end;
+  int* counts;                    // [workgroups][experts]
+};
+constexpr int kMoeMaxExperts = 1024, kMoeMaxTopk = 64;
+size_t moe_sort_ws_bytes(int64_t n, int experts);
+hipError_t launch_moe_sort(const MoeSortArgs& p, hipStream_t stream);
+struct MoeWeight {
+  const void* p;   // bf16 or fp32 [tokens, topk], or nullptr: 1
+  int f32;
+};
+struct MoeGatherArgs {
+  MoeTable table;
+  int64_t cols;
+  const uint16_t* x; int64_t ld_x;   // [tokens, cols]
+  MoeWeight weight;                  // multiplies a slot's copy
+  LayoutsOut out;                    // [rows, cols]
+  const uint16_t* y; int64_t ld_y;   // with dweight: [rows, cols]
+  void* dweight;                     // nullptr, or <x[t], y[row]> per slot in the weight's type
+};
+hipError_t launch_moe_gather(const MoeGatherArgs& p, hipStream_t stream);
+struct MoeCombineArgs {
+  MoeTable table;
+  int64_t cols;
+  const uint16_t* y; int64_t ld_y;   // [rows, cols]
+  MoeWeight weight;
+  uint16_t* out; int64_t ld_out;     // [tokens, cols]
+};
+hipError_t launch_moe_combine(const MoeCombineArgs& p, hipStream_t stream);
+
+// ---- gated activation (swiglu.hip) ----
+struct SwigluFwdArgs {
+  int64_t rows, ffn;
+  const uint16_t* h; int64_t ld_h;                                // [rows, 2 ffn]
+  LayoutsOut out;                                                 // [rows, ffn]
+  uint8_t* hq; int64_t ld_hq; float* h_recip; int64_t hr_row, hr_kb;   // codes of h or nullptr
+};
+struct SwigluBwdArgs {
+  int64_t rows, ffn;
+  const uint16_t* dy; int64_t ld_dy;                              // [rows, ffn]
+  const void* h; int64_t ld_h;                                    // bf16, or codes with h_recip
+  const float* h_recip; int64_t hr_row, hr_kb;
+  LayoutsOut dh;                                                  // [rows, 2 ffn]
+  uint8_t* act_qt; int64_t ld_act_qt; float* act_recip_t; int64_t art_row, art_kb;   // or nullptr
+};
+hipError_t launch_swiglu_fwd(const SwigluFwdArgs& p, hipStream_t stream);
+hipError_t launch_swiglu_bwd(const SwigluBwdArgs& p, hipStream_t stream);
 
 }  // namespace fp8bw

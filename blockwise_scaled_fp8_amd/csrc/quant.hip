@@ -135,6 +135,10 @@ struct TileOut {
   float* recip_t;       // their scales (rst_row, rst_kb)
   int64_t rst_row, rst_kb;
 };
+// Matrices of a grouped launch (blockIdx.z), elements apart.
+struct TileGroups {
+  int64_t x, q, recip;
+};
 
 // STREAM_T: the transposed codes are written with nontemporal stores, for
 // a caller that will not read them until much later (the X^T codes a
@@ -142,9 +146,9 @@ struct TileOut {
 // memory-side cache by instead of evicting the operands of the GEMM that
 // runs next (the forward GEMM of the 16640 x 5120 x 8192 linear step ran
 // 576-578 us after the plain stores, 558-562 us after these).
-template <int MODE, bool STREAM_T = false>
-__global__ __launch_bounds__(256) void quant_tile_kernel(
-    const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld_x, const TileOut o) {
+template <int MODE, bool STREAM_T>
+__device__ __forceinline__ void quant_tile(const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld_x,
+                                           const TileOut& o) {
   constexpr bool PLAIN = MODE == kTileScale || MODE == kTileScaleBoth || MODE == kRowColBoth;
   constexpr bool T = MODE != kTileScale;
   constexpr bool COLS = MODE == kColScaleT || MODE == kRowColBoth;
@@ -252,6 +256,26 @@ __global__ __launch_bounds__(256) void quant_tile_kernel(
 }
 
 template <int MODE, bool STREAM_T = false>
+__global__ __launch_bounds__(256) void quant_tile_kernel(
+    const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld_x, const TileOut o) {
+  quant_tile<MODE, STREAM_T>(x, rows, cols, ld_x, o);
+}
+
+template <int MODE>
+__global__ __launch_bounds__(256) void quant_tile_grouped_kernel(
+    const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld_x, TileOut o, const TileGroups step) {
+  const int64_t g = blockIdx.z;
+  if (MODE == kTileScale) {
+    o.q += g * step.q;
+    o.recip += g * step.recip;
+  } else {
+    o.qt += g * step.q;
+    o.recip_t += g * step.recip;
+  }
+  quant_tile<MODE, false>(x + g * step.x, rows, cols, ld_x, o);
+}
+
+template <int MODE, bool STREAM_T = false>
 static hipError_t launch_tile(const void* x, int64_t rows, int64_t cols, int64_t ld_x,
                               const TileOut& o, hipStream_t stream) {
   if (rows == 0 || cols == 0) return hipSuccess;
@@ -274,6 +298,22 @@ hipError_t launch_quant_128x128(const void* x, int64_t rows, int64_t cols, int64
   return transpose
              ? launch_tile<kTileScaleT>(x, rows, cols, ld_x, trans_out(q, ld_q, recip, rs_row, rs_kb), stream)
              : launch_tile<kTileScale>(x, rows, cols, ld_x, plain_out(q, ld_q, recip, rs_row, rs_kb), stream);
+}
+
+hipError_t launch_quant_128x128_grouped(const void* x, int64_t rows, int64_t cols, int64_t ld_x, int64_t x_group,
+                                        int groups, int transpose, void* q, int64_t ld_q, int64_t q_group,
+                                        float* recip, int64_t rs_row, int64_t rs_kb, int64_t rs_group,
+                                        hipStream_t stream) {
+  if (rows == 0 || cols == 0) return hipSuccess;
+  const dim3 grid((unsigned)((cols + 127) / 128), (unsigned)((rows + 127) / 128), (unsigned)groups);
+  const TileGroups step{x_group, q_group, rs_group};
+  if (transpose)
+    hipLaunchKernelGGL(quant_tile_grouped_kernel<kTileScaleT>, grid, dim3(256), 0, stream, (const uint16_t*)x, rows,
+                       cols, ld_x, trans_out(q, ld_q, recip, rs_row, rs_kb), step);
+  else
+    hipLaunchKernelGGL(quant_tile_grouped_kernel<kTileScale>, grid, dim3(256), 0, stream, (const uint16_t*)x, rows,
+                       cols, ld_x, plain_out(q, ld_q, recip, rs_row, rs_kb), step);
+  return hipGetLastError();
 }
 
 hipError_t launch_quant_1x128_cols_t(const void* x, int64_t rows, int64_t cols, int64_t ld_x,

@@ -18,37 +18,10 @@
 // loads, sums are fp32 in a fixed order (DPP within a wave, then LDS, no
 // atomics), so results repeat bit for bit.
 
-#include "device_common.h"
 #include "launch.h"
+#include "vec8.h"
 
 namespace fp8bw {
-
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-
-// 16 bytes that nothing reads again soon: a load that leaves the caches alone.
-__device__ __forceinline__ uint4 load_stream(const uint16_t* p) {
-  const u32x4 t = __builtin_nontemporal_load((const u32x4*)p);
-  return make_uint4(t.x, t.y, t.z, t.w);
-}
-
-// Sum over the 16 lanes of a DPP row, then over the wavefront; every lane
-// receives the same value.
-__device__ __forceinline__ float row16_sum(float v) {
-  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false));
-  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false));
-  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false));
-  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, false));
-  return v;
-}
-__device__ __forceinline__ float wave_sum(float v) {
-  v = row16_sum(v);
-  const int i = __float_as_int(v);
-  const float a = __int_as_float(__builtin_amdgcn_readlane(i, 0));
-  const float b = __int_as_float(__builtin_amdgcn_readlane(i, 16));
-  const float c = __int_as_float(__builtin_amdgcn_readlane(i, 32));
-  const float d = __int_as_float(__builtin_amdgcn_readlane(i, 48));
-  return (a + b) + (c + d);
-}
 
 // Sum over the TPR threads of a row; `red` holds one float per wave and is
 // not written again before the caller's next barrier or its other half.
@@ -66,16 +39,6 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&f)[8]) {
-  f[0] = bf16lo(u.x); f[1] = bf16hi(u.x);
-  f[2] = bf16lo(u.y); f[3] = bf16hi(u.y);
-  f[4] = bf16lo(u.z); f[5] = bf16hi(u.z);
-  f[6] = bf16lo(u.w); f[7] = bf16hi(u.w);
-}
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2_rne(f[0], f[1]), pack_bf16x2_rne(f[2], f[3]),
-                    pack_bf16x2_rne(f[4], f[5]), pack_bf16x2_rne(f[6], f[7]));
-}
 __device__ __forceinline__ void load_weight8(const NormWeight& w, int col, float (&f)[8]) {
   if (w.f32) {
     const float4 a = *(const float4*)((const float*)w.p + col);

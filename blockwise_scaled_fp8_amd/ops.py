@@ -10,7 +10,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from ._lib import AdamwTensor, check, load_library
+from ._lib import AdamwTensor, Layouts, check, load_library
 
 BLOCKS = {"1x128": 0, "128x128": 1}
 OUT_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
@@ -777,3 +777,284 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, step, lr, beta1=0.9, bet
             check(lib.fp8bw_adamw_step(*args))
     # a graph that saved a parameter refuses to run backward through the new values
     torch.autograd.graph.increment_version(params)
+
+
+# ---------------------------------------------------------------------------
+# The operators around the grouped GEMM in a mixture-of-experts layer
+# (include/fp8bw.h): sort, gather, combine, gated activation, weight gradients.
+
+class MoeTable(NamedTuple):
+    """Slots (token, choice) sorted by expert, as moe_sort makes it."""
+    row: torch.Tensor         # int32 [tokens, topk]: a slot's row, -1 without an expert
+    source: torch.Tensor      # int32 [rows]: a row's slot t * topk + j, -1 without one
+    group_end: torch.Tensor   # int32 [experts], cumulative: the grouped GEMM's table
+
+
+class Rows(NamedTuple):
+    """Layouts of a [rows, cols] result; what was not asked for is None."""
+    y: Optional[torch.Tensor]        # bf16 [rows, cols]
+    q: Optional[torch.Tensor]        # uint8 codes [rows, cols]
+    recip: Optional[torch.Tensor]    # fp32 [rows, blocks], column-major
+    qt: Optional[torch.Tensor]       # uint8 codes [cols, rows]
+    recip_t: Optional[torch.Tensor]  # fp32 [cols, ceil(rows / 128)], column-major
+
+
+class SwigluOut(NamedTuple):
+    """Outputs of swiglu_fwd; what was not asked for is None."""
+    y: Optional[torch.Tensor]
+    q: Optional[torch.Tensor]
+    recip: Optional[torch.Tensor]
+    qt: Optional[torch.Tensor]
+    recip_t: Optional[torch.Tensor]
+    hq: Optional[torch.Tensor]       # uint8 codes [rows, 2 ffn] of h
+    h_recip: Optional[torch.Tensor]  # fp32 [rows, 2 ceil(ffn / 128)], column-major
+
+
+class SwigluGrads(NamedTuple):
+    """Outputs of swiglu_bwd; what was not asked for is None."""
+    dh: Optional[torch.Tensor]           # bf16 [rows, 2 ffn]
+    q: Optional[torch.Tensor]            # uint8 codes [rows, 2 ffn] of dh
+    recip: Optional[torch.Tensor]        # fp32 [rows, 2 ceil(ffn / 128)], column-major
+    qt: Optional[torch.Tensor]           # uint8 codes [2 ffn, rows] of dh^T
+    recip_t: Optional[torch.Tensor]      # fp32 [2 ffn, ceil(rows / 128)], column-major
+    act_qt: Optional[torch.Tensor]       # uint8 codes [ffn, rows] of the activation's transpose
+    act_recip_t: Optional[torch.Tensor]  # fp32 [ffn, ceil(rows / 128)], column-major
+
+
+def _codes_empty(rows, cols, blocks, device):
+    """(codes [rows, cols], column-major scales [rows, blocks])."""
+    return (torch.empty((rows, cols), dtype=torch.uint8, device=device),
+            torch.empty_strided((rows, blocks), (1, max(rows, 1)), dtype=torch.float32, device=device))
+
+
+def _layouts_empty(rows, cols, blocks, y, q, qt, device):
+    """(Rows, the C struct that names its tensors)."""
+    ty = tq = tr = tqt = trt = None
+    if y:
+        ty = torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+    if q:
+        tq, tr = _codes_empty(rows, cols, blocks, device)
+    if qt:
+        tqt, trt = _codes_empty(cols, rows, _cdiv(rows, 128), device)
+    return (Rows(ty, tq, tr, tqt, trt),
+            Layouts(_ptr(ty), cols, _ptr(tq), cols, _ptr(tr), 1, rows, _ptr(tqt), rows, _ptr(trt), 1, cols))
+
+
+def _moe_table(table, device):
+    """(tokens, topk, rows) of a table on `device`."""
+    row, source, group_end = table
+    for t, dim, name in ((row, 2, "row"), (source, 1, "source"), (group_end, 1, "group_end")):
+        if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"the table's {name} must be a contiguous int32 tensor of {dim} dimension"
+                             f"{'s' if dim > 1 else ''} on {device}")
+    return row.shape[0], row.shape[1], source.shape[0]
+
+
+def _moe_weight(weight, tokens, topk):
+    if weight.dtype not in OUT_DTYPES or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous bf16 or float32 tensor")
+    _check_shape(weight, (tokens, topk), "weight")
+
+
+def moe_rows(tokens, topk, experts, align=128):
+    """Rows of moe_sort's table: what holds the slots however they fall."""
+    return load_library().fp8bw_moe_rows(tokens, topk, experts, align)
+
+
+@_on_tensor_device
+def moe_sort(expert, experts, align=128):
+    """MoeTable of slots sorted by expert, each expert's rows padded to a
+    multiple of `align`.
+
+    expert int32 or int64 [tokens, topk]; a number outside [0, experts) is no
+    expert.  Slots of one expert keep their order."""
+    lib = load_library()
+    _need_cuda(expert)
+    if expert.dim() != 2 or expert.dtype not in (torch.int32, torch.int64) or not expert.is_contiguous():
+        raise ValueError("expert must be a contiguous int32 or int64 tensor [tokens, topk]")
+    tokens, topk = expert.shape
+    experts, align = int(experts), int(align)
+    rows = lib.fp8bw_moe_rows(tokens, topk, experts, align)
+    dev = expert.device
+    row = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
+    source = torch.empty(rows, dtype=torch.int32, device=dev)
+    group_end = torch.empty(max(experts, 0), dtype=torch.int32, device=dev)
+    nws = lib.fp8bw_moe_sort_ws_bytes(tokens, topk, experts)
+    ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
+    check(lib.fp8bw_moe_sort(expert.data_ptr(), 32 if expert.dtype == torch.int32 else 64, tokens, topk,
+                             experts, align, rows, row.data_ptr(), source.data_ptr(),
+                             group_end.data_ptr(), _ptr(ws), nws, _stream(expert)))
+    return MoeTable(row, source, group_end)
+
+
+@_on_tensor_device
+def moe_gather(x, table, y=True, q=False, qt=False):
+    """Rows of x bf16 [tokens, cols] in the table's order (zeros in rows without
+    a slot): bf16, E4M3 codes in 1x128 blocks along the columns, and codes of
+    the transpose in 1x128 blocks along the rows.  The gradient of y is
+    moe_combine(dy, table)."""
+    lib = load_library()
+    _need_cuda(x)
+    _bf16_matrix(x, "x")
+    tokens, topk, rows = _moe_table(table, x.device)
+    cols = x.shape[1]
+    _check_shape(x, (tokens, cols), "x")
+    out, c = _layouts_empty(rows, cols, _cdiv(cols, 128), y, q, qt, x.device)
+    check(lib.fp8bw_moe_gather(x.data_ptr(), x.stride(0), tokens, topk, table.row.data_ptr(),
+                               table.source.data_ptr(), rows, cols, c, _stream(x)))
+    return out
+
+
+@_on_tensor_device
+def moe_combine(y, table, weight=None):
+    """bf16 [tokens, cols]: every token's rows of y bf16 [rows, cols] summed in
+    fp32, times weight (fp32 or bf16 [tokens, topk]) if given."""
+    lib = load_library()
+    _need_cuda(y)
+    _bf16_matrix(y, "y")
+    tokens, topk, rows = _moe_table(table, y.device)
+    cols = y.shape[1]
+    _check_shape(y, (rows, cols), "y")
+    if weight is not None:
+        _moe_weight(weight, tokens, topk)
+    out = torch.empty((tokens, cols), dtype=torch.bfloat16, device=y.device)
+    check(lib.fp8bw_moe_combine(y.data_ptr(), y.stride(0), _ptr(weight),
+                                1 if weight is None else OUT_DTYPES[weight.dtype], tokens, topk,
+                                table.row.data_ptr(), rows, cols, out.data_ptr(), out.stride(0), _stream(y)))
+    return out
+
+
+@_on_tensor_device
+def moe_combine_bwd(dout, y, table, weight, dy=True, q=False, qt=False, need_dweight=True):
+    """(Rows, dweight) of moe_combine from dout bf16 [tokens, cols]: the
+    gradient of its y in the layouts asked for (as moe_gather), and that of
+    weight, in its type (None without need_dweight; y may then be None)."""
+    lib = load_library()
+    _need_cuda(dout, weight)
+    _bf16_matrix(dout, "dout")
+    tokens, topk, rows = _moe_table(table, dout.device)
+    cols = dout.shape[1]
+    _check_shape(dout, (tokens, cols), "dout")
+    _moe_weight(weight, tokens, topk)
+    dweight = None
+    if need_dweight:
+        _need_cuda(y)
+        _bf16_matrix(y, "y", (rows, cols))
+        dweight = torch.empty_like(weight)
+        if cols == 0:
+            dweight.zero_()
+    out, c = _layouts_empty(rows, cols, _cdiv(cols, 128), dy, q, qt, dout.device)
+    if cols:
+        check(lib.fp8bw_moe_combine_bwd(dout.data_ptr(), dout.stride(0), y.data_ptr() if need_dweight else None,
+                                        y.stride(0) if need_dweight else 0, weight.data_ptr(),
+                                        OUT_DTYPES[weight.dtype], tokens, topk, table.row.data_ptr(),
+                                        table.source.data_ptr(), rows, cols, c, _ptr(dweight), _stream(dout)))
+    return out, dweight
+
+
+def _halves(t, name):
+    if t.shape[1] % 2:
+        raise ValueError(f"{name} must have an even number of columns")
+    return t.shape[1] // 2
+
+
+@_on_tensor_device
+def swiglu_fwd(h, y=True, q=False, qt=False, save=False):
+    """SwigluOut of v = silu(gate) * up, h = [gate | up] bf16 [rows, 2 ffn].
+
+    y, q, qt choose v's layouts (as moe_gather).  save: also h itself in E4M3
+    codes with a scale per 1x128 block of each half, which swiglu_bwd takes in
+    the place of h at half its bytes."""
+    lib = load_library()
+    _need_cuda(h)
+    _bf16_matrix(h, "h")
+    rows, ffn = h.shape[0], _halves(h, "h")
+    out, c = _layouts_empty(rows, ffn, _cdiv(ffn, 128), y, q, qt, h.device)
+    hq = hr = None
+    if save:
+        hq, hr = _codes_empty(rows, 2 * ffn, 2 * _cdiv(ffn, 128), h.device)
+    check(lib.fp8bw_swiglu_fwd(h.data_ptr(), h.stride(0), rows, ffn, c, _ptr(hq), 2 * ffn, _ptr(hr), 1, rows,
+                               _stream(h)))
+    return SwigluOut(*out, hq, hr)
+
+
+@_on_tensor_device
+def swiglu_bwd(dy, h, h_recip=None, dh=True, q=False, qt=False, act_qt=False):
+    """SwigluGrads of swiglu_fwd from dy bf16 [rows, ffn] and h: bf16, or the
+    codes of a checkpoint with its scales h_recip.
+
+    dh, q, qt choose the layouts of the gradient of h (q in 1x128 blocks of each
+    half); act_qt makes the activation's transposed codes again, the operand of
+    the weight gradient of the product behind it."""
+    lib = load_library()
+    _need_cuda(dy, h)
+    _bf16_matrix(dy, "dy")
+    rows, ffn = dy.shape
+    if h_recip is None:
+        _bf16_matrix(h, "h", (rows, 2 * ffn))
+    else:
+        _check_codes_out(h, (rows, 2 * ffn), "h")
+        _check_scales(h_recip, (rows, 2 * _cdiv(ffn, 128)), "h_recip")
+    out, c = _layouts_empty(rows, 2 * ffn, 2 * _cdiv(ffn, 128), dh, q, qt, dy.device)
+    tq = tr = None
+    if act_qt:
+        tq, tr = _codes_empty(ffn, rows, _cdiv(rows, 128), dy.device)
+    check(lib.fp8bw_swiglu_bwd(dy.data_ptr(), dy.stride(0), h.data_ptr(), h.stride(0), _ptr(h_recip),
+                               0 if h_recip is None else h_recip.stride(0),
+                               0 if h_recip is None else h_recip.stride(1), rows, ffn, c, _ptr(tq), rows,
+                               _ptr(tr), 1, ffn, _stream(dy)))
+    return SwigluGrads(*out, tq, tr)
+
+
+@_on_tensor_device
+def fp8_scaled_grouped_gemm_blockwise_wgrad(a, ra, b, rb, group_end, out_dtype=torch.bfloat16, out=None):
+    """Weight gradients of a grouped GEMM: out[g] = A . B^T over the columns
+    [group_end[g-1], group_end[g]) of a uint8 [M, K] and b uint8 [N, K], the
+    transposed codes of dY and X in 1x128 blocks with scales ra fp32 [M, K/128]
+    and rb fp32 [N, K/128] -> out [G, M, N].  group_end: device int32 [G],
+    cumulative multiples of 128 (moe_sort with align 128)."""
+    lib = load_library()
+    _need_cuda(a, b, ra, rb, group_end)
+    _rowmajor(a, "a")
+    _rowmajor(b, "b")
+    M, K = a.shape
+    N = b.shape[0]
+    _check_codes(a, b, K)
+    kb = _cdiv(K, 128)
+    _check_scales(ra, (M, kb), "ra")
+    _check_scales(rb, (N, kb), "rb")
+    if group_end.dtype != torch.int32 or group_end.dim() != 1 or not group_end.is_contiguous():
+        raise ValueError("group_end must be a contiguous int32 [G] tensor")
+    G = group_end.shape[0]
+    if out is None:
+        out = torch.empty((G, M, N), dtype=out_dtype, device=a.device)
+    _check_shape(out, (G, M, N), "out")
+    if out.dtype not in OUT_DTYPES or out.stride(2) != 1:
+        raise ValueError("out must be bfloat16 or float32 with unit column stride")
+    if G == 0:
+        return out
+    check(lib.fp8_scaled_grouped_gemm_blockwise_wgrad(
+        a.data_ptr(), a.stride(0), ra.data_ptr(), ra.stride(0), ra.stride(1), b.data_ptr(), b.stride(0),
+        rb.data_ptr(), rb.stride(0), rb.stride(1), G, group_end.data_ptr(), M, N, K, out.data_ptr(),
+        out.stride(1), out.stride(0), OUT_DTYPES[out.dtype], _stream(a)))
+    return out
+
+
+@_on_tensor_device
+def fp8_blockwise_quant_grouped(x, transpose=False):
+    """fp8_blockwise_quant(x[g], "128x128", transpose) of every matrix of x bf16
+    [G, rows, cols] in one launch: (q uint8 [G, rows, cols], or [G, cols, rows]
+    with transpose, recip fp32 [G, ni, nj], column-major per matrix)."""
+    lib = load_library()
+    _need_cuda(x)
+    if x.dim() != 3 or x.stride(2) != 1 or x.dtype != torch.bfloat16:
+        raise ValueError("x must be bf16 [G, rows, cols] with unit column stride")
+    G, rows, cols = x.shape
+    q = torch.empty((G, cols, rows) if transpose else (G, rows, cols), dtype=torch.uint8, device=x.device)
+    ni, nj = scale_grid(rows, cols, "128x128", transpose)
+    recip = torch.empty((G, nj, ni), dtype=torch.float32, device=x.device).transpose(1, 2)
+    if G:
+        check(lib.fp8_blockwise_quant_grouped(x.data_ptr(), rows, cols, x.stride(1), x.stride(0), G,
+                                              int(bool(transpose)), q.data_ptr(), q.stride(1), q.stride(0),
+                                              recip.data_ptr(), 1, max(ni, 1), ni * nj, _stream(x)))
+    return q, recip

@@ -1,7 +1,7 @@
 /*
  * fp8bw.h -- C ABI of libfp8bw.so: blockwise- and tensorwise-scaled FP8
  * (OCP E4M3) quantization and GEMM for AMD MI355X (gfx950), and the operators
- * around an FP8 linear in a training step.
+ * around an FP8 linear and an FP8 mixture-of-experts layer in a training step.
  *
  * Sources, cited by page title and section:
  *   [REPRO]   pytorch/ao PR "add repro for blockwise _scaled_mm
@@ -550,6 +550,163 @@ typedef struct {
 int fp8bw_adamw_step(const fp8bw_adamw_tensor* tensors, int count, int state, int64_t step,
                      double lr, double beta1, double beta2, double eps, double weight_decay,
                      const float* grad_scale, int stochastic, uint64_t seed, void* stream);
+
+/*
+ * Experts: the operators around the grouped GEMM in a mixture-of-experts layer.
+ *
+ * A slot i = t * topk + j is token t's j-th choice of an expert.  fp8bw_moe_sort
+ * gives every slot a row, in the order of its expert and then of the slots, each
+ * expert's rows padded to a multiple of `align` (1, or 128 for the grouped weight
+ * gradient):
+ *
+ *   group_end[e] = sum_{f <= e} ceil(n_f / align) * align,  n_f slots of expert f
+ *   row[i]       = (group_end[e] - padded n_e) + number of slots i' < i of expert e
+ *   source[r]    = the slot with row r; -1 for padding and behind the last end
+ *
+ *   expert     device [tokens, topk], int32 (index_bits 32) or int64 (64).  A slot
+ *              whose number is outside [0, experts) has no expert: row -1.
+ *   rows       at least fp8bw_moe_rows(tokens, topk, experts, align), which holds
+ *              the slots however they fall; known without reading the device.
+ *   row, source, group_end   device int32 [tokens, topk], [rows], [experts].
+ *              group_end is the table that the grouped GEMM takes.
+ *   ws         fp8bw_moe_sort_ws_bytes(tokens, topk, experts) bytes, 256-byte aligned
+ *              (0 for few slots: ws may be NULL).
+ *   Requires 1 <= topk <= 64, 1 <= experts <= 1024, 1 <= align <= 65536,
+ *   tokens < 2^24, rows < 2^27 (fp8bw_moe_rows is 0 for larger ones).
+ */
+int64_t fp8bw_moe_rows(int64_t tokens, int64_t topk, int64_t experts, int64_t align);
+size_t fp8bw_moe_sort_ws_bytes(int64_t tokens, int64_t topk, int64_t experts);
+int fp8bw_moe_sort(const void* expert, int index_bits, int64_t tokens, int64_t topk, int64_t experts,
+                   int64_t align, int64_t rows, int32_t* row, int32_t* source, int32_t* group_end,
+                   void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The outputs of a [rows, cols] result v (fp32); each pointer may be NULL.  A host struct.
+ *   y   device bf16 [rows, cols]
+ *   q   device E4M3 [rows, cols] in 1x128 blocks along the columns, with
+ *       recip[r*rs_row + kb*rs_kb]
+ *   qt  device E4M3 [cols, rows]: codes of v^T in 1x128 blocks along the rows, with
+ *       recip_t[c*rst_row + mb*rst_kb]; needs rows % 16 == 0
+ * The codes follow the quantizers' recipe on v (not on y).
+ */
+typedef struct {
+  void* y;
+  int64_t ld_y;
+  void* q;
+  int64_t ld_q;
+  float* recip;
+  int64_t rs_row, rs_kb;
+  void* qt;
+  int64_t ld_qt;
+  float* recip_t;
+  int64_t rst_row, rst_kb;
+} fp8bw_layouts;
+
+/*
+ * fp8bw_moe_gather -- token rows in the sorted order: v[r] = x[source[r] / topk],
+ * zeros (code 0) where a row has no slot.  Its gradient is fp8bw_moe_combine without
+ * weights.
+ *   x   device bf16 [tokens, cols].  row and source: as fp8bw_moe_sort wrote them (a
+ *       row outside [0, rows) and a source outside [0, tokens * topk) count as -1; a
+ *       table whose row and source are not each other's inverse gives unspecified
+ *       values).
+ *
+ * fp8bw_moe_combine -- the experts' rows joined: out[t] = sum_j weight[t, j] *
+ * y[row[t, j]] over the slots that have a row, in fp32 in the slots' order; zeros for
+ * a token without any.  What y holds in other rows is not read.
+ *   y   device bf16 [rows, cols]; weight device [tokens, topk], fp32 or bf16
+ *       (weight_dtype), NULL: ones; out device bf16 [tokens, cols].
+ *
+ * fp8bw_moe_combine_bwd -- its gradients: v[r] = weight[source[r]] * dout[source[r] /
+ * topk] (zeros without a slot) in dy's layouts, and dweight[t, j] = sum_c dout[t, c] *
+ * y[row[t, j], c] (0 without a row) in the weight's type, or NULL.  y is read only for
+ * dweight.  With qt asked for and dweight, two launches.
+ *
+ * All three: cols % 16 == 0, cols <= 65536, tokens < 2^24, rows < 2^27, and fewer than
+ * 2^26 pieces of 512 columns of tokens and 2^23 tiles of 128 rows x 128 columns.
+ * rows >= 1 if tokens >= 1, and no rows without tokens.
+ */
+int fp8bw_moe_gather(const void* x, int64_t ld_x, int64_t tokens, int64_t topk, const int32_t* row,
+                     const int32_t* source, int64_t rows, int64_t cols, const fp8bw_layouts* out,
+                     void* stream);
+int fp8bw_moe_combine(const void* y, int64_t ld_y, const void* weight, int weight_dtype, int64_t tokens,
+                      int64_t topk, const int32_t* row, int64_t rows, int64_t cols, void* out,
+                      int64_t ld_out, void* stream);
+int fp8bw_moe_combine_bwd(const void* dout, int64_t ld_dout, const void* y, int64_t ld_y,
+                          const void* weight, int weight_dtype, int64_t tokens, int64_t topk,
+                          const int32_t* row, const int32_t* source, int64_t rows, int64_t cols,
+                          const fp8bw_layouts* dy, void* dweight, void* stream);
+
+/*
+ * fp8bw_swiglu_fwd -- the gated activation between an MLP's two products:
+ *
+ *   h = [g | u],  v = g * sigmoid(g) * u
+ *
+ *   h    device bf16 [rows, 2 ffn]; out: the layouts of v [rows, ffn].
+ *   hq   device E4M3 [rows, 2 ffn], a checkpoint of h for the backward in half its
+ *        bytes, in 1x128 blocks of each half: h_recip[r*hr_row + kb*hr_kb], kb in
+ *        [0, 2 ceil(ffn / 128)), the gate's blocks first.  NULL: not written.
+ *
+ * fp8bw_swiglu_bwd -- its gradient, with s = sigmoid(g):
+ *   dg = dy * u * s * (1 + g * (1 - s)),  du = dy * g * s
+ *
+ *   dy   device bf16 [rows, ffn].
+ *   h    bf16 with h_recip NULL, else a checkpoint's codes and its scales; g and u are
+ *        then the values that the codes stand for.
+ *   dh   the layouts of [dg | du] [rows, 2 ffn]; q in 1x128 blocks of each half.
+ *   act_qt   device E4M3 [ffn, rows] or NULL: codes of v^T, made again, in 1x128 blocks
+ *        along the rows, act_recip_t[c*art_row + mb*art_kb]: the second product's
+ *        operand of its weight gradient.
+ *
+ * Both: ffn % 16 == 0, ffn <= 2^20, rows < 2^27, fewer than 2^26 pieces of 512 columns
+ * and 2^23 tiles of 128 x 128 of v.  Transposed codes need rows % 16 == 0.
+ */
+int fp8bw_swiglu_fwd(const void* h, int64_t ld_h, int64_t rows, int64_t ffn, const fp8bw_layouts* out,
+                     void* hq, int64_t ld_hq, float* h_recip, int64_t hr_row, int64_t hr_kb,
+                     void* stream);
+int fp8bw_swiglu_bwd(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, const float* h_recip,
+                     int64_t hr_row, int64_t hr_kb, int64_t rows, int64_t ffn, const fp8bw_layouts* dh,
+                     void* act_qt, int64_t ld_act_qt, float* act_recip_t, int64_t art_row,
+                     int64_t art_kb, void* stream);
+
+/*
+ * fp8_scaled_grouped_gemm_blockwise_wgrad -- the weight gradients of a grouped GEMM,
+ * one [M, N] product per group over that group's rows, which are the contraction:
+ *
+ *   out_g[m, n] = sum_{kb in group g} ra[m, kb] * rb[n, kb] * sum_{k in kb} a[m, k] * b[n, k]
+ *
+ *   a, b       device E4M3 [M, K] and [N, K]: the transposed codes of the two [K, ..]
+ *              matrices (dY^T and X^T), in 1x128 blocks along K with scales
+ *              ra[m*ra_s_row + kb*ra_s_kb], rb[n*rb_s_row + kb*rb_s_kb] (strides as in
+ *              fp8_scaled_gemm_blockwise).
+ *   group_end  DEVICE int32 [groups], cumulative ends along K, multiples of 128 (a sort
+ *              with align 128): group g contracts the blocks [group_end[g-1] / 128,
+ *              group_end[g] / 128), clamped to K.  Codes outside are not used.  A group
+ *              without blocks gives zeros.
+ *   out        device [M, N] per group, bf16 or fp32, ldo, out_s_group elements apart
+ *              (>= (M - 1) * ldo + N).
+ *   Requires K % 128 == 0, 1 <= groups <= 2^20 and at most 2^23 output tiles; errors as
+ *   fp8_scaled_gemm_blockwise.
+ */
+int fp8_scaled_grouped_gemm_blockwise_wgrad(const void* a, int64_t lda, const float* ra,
+                                            int64_t ra_s_row, int64_t ra_s_kb, const void* b,
+                                            int64_t ldb, const float* rb, int64_t rb_s_row,
+                                            int64_t rb_s_kb, int groups, const int* group_end,
+                                            int64_t M, int64_t N, int64_t K, void* out, int64_t ldo,
+                                            int64_t out_s_group, int out_dtype, void* stream);
+
+/*
+ * fp8_blockwise_quant_grouped -- fp8_blockwise_quant with 128x128 blocks of `groups`
+ * matrices of one shape in one launch (the experts' weights, as they are or transposed):
+ * group g is x + g*x_s_group, with codes at q + g*q_s_group and scales at recip +
+ * g*recip_s_group.  Strides between groups must keep the outputs apart (x's may be any
+ * multiple of 8).  Arguments and errors otherwise as fp8_blockwise_quant; 1 <= groups
+ * <= 65535 and fewer than 2^24 blocks.
+ */
+int fp8_blockwise_quant_grouped(const void* x, int64_t rows, int64_t cols, int64_t ld_x,
+                                int64_t x_s_group, int groups, int transpose, void* q, int64_t ld_q,
+                                int64_t q_s_group, float* recip, int64_t rs_row, int64_t rs_kb,
+                                int64_t recip_s_group, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,135 @@
+"""Grouped weight gradients on the GPU against the oracle: groups of many
+lengths, empty ones, every tile size, fp32 and bf16 outputs, strided operands
+and a malformed table.  Tolerances are the GEMM's (tests/gpu_util.py)."""
+
+import numpy as np
+import pytest
+import torch
+
+import blockwise_scaled_fp8_amd as fp8
+from oracle import moe
+from tests.gpu_util import check_gemm_output, host_f32, say
+
+pytestmark = pytest.mark.gpu
+
+
+def _codes(rng, shape):
+    c = rng.integers(0, 256, size=shape).astype(np.uint8)
+    c[(c & 0x7F) == 0x7F] = 0x7E
+    return c
+
+
+def _operands(M, N, K, seed):
+    rng = np.random.default_rng(seed)
+    return (_codes(rng, (M, K)), rng.uniform(1e-3, 2e-3, (M, K // 128)).astype(np.float32),
+            _codes(rng, (N, K)), rng.uniform(1e-3, 2e-3, (N, K // 128)).astype(np.float32))
+
+
+def _colmajor(r, gpu):
+    return torch.from_numpy(np.ascontiguousarray(r.T)).to(gpu).t()
+
+
+def _case(gpu, M, N, K, ends, od="f32", seed=0, rows=None):
+    a, ra, b, rb = _operands(M, N, K, seed)
+    dt = torch.bfloat16 if od == "bf16" else torch.float32
+    out = torch.full((len(ends), M, N), float("nan"), dtype=dt, device=gpu)
+    say("grouped wgrad", M, N, K, od, list(ends)[:10])
+    got = fp8.fp8_scaled_grouped_gemm_blockwise_wgrad(
+        torch.from_numpy(a).to(gpu), _colmajor(ra, gpu), torch.from_numpy(b).to(gpu), _colmajor(rb, gpu),
+        torch.tensor(ends, dtype=torch.int32, device=gpu), out=out)
+    torch.cuda.synchronize()
+    assert got is out
+    rows = np.arange(M) if rows is None else np.asarray(rows)
+    ref, size = moe.grouped_wgrad(a[rows], ra[rows], b, rb, ends)
+    check_gemm_output(host_f32(out)[:, rows].reshape(-1, N), ref.reshape(-1, N), size.reshape(-1, N), K // 128, od,
+                      f"wgrad {len(ends)}x{M}x{N}x{K}")
+    return host_f32(out)
+
+
+# small tiles; both 128-row kinds; whole and ragged large tiles; many groups
+@pytest.mark.parametrize("od", ["bf16", "f32"])
+@pytest.mark.parametrize("M, N, K, ends", [
+    (16, 16, 128, [128]), (1, 33, 256, [128, 256]), (64, 64, 640, [0, 128, 128, 512, 640]),
+    (200, 136, 512, [256, 512]), (512, 256, 1024, [128, 128, 640, 640, 1024, 1024, 1024, 1024])])
+def test_small(gpu, M, N, K, ends, od):
+    _case(gpu, M, N, K, ends, od, seed=M + N)
+
+
+def test_tiles_of_128(gpu):
+    # 17 groups x 4 x 4 tiles of 128 x 128, too few for larger ones
+    _case(gpu, 392, 400, 512, [128 * (i // 5) for i in range(1, 18)], "bf16", seed=3, rows=np.r_[0:20, 120:140, 380:392])
+
+
+def test_tiles_of_256_by_128(gpu):
+    # N below 256: 256 x 128 tiles, ragged in both directions
+    _case(gpu, 1040, 144, 384, [128 * min(3, i % 4) for i in np.sort(np.arange(64) % 4)], "f32", seed=4,
+          rows=np.r_[0:8, 250:262, 1030:1040])
+
+
+@pytest.mark.parametrize("od", ["bf16", "f32"])
+def test_large_tiles(gpu, od):
+    # 16 groups x 5 x 5 ragged tiles of 256 x 256
+    ends = np.cumsum([1, 0, 2, 3, 0, 0, 1, 1, 4, 0, 1, 2, 1, 0, 1, 0]) * 128
+    _case(gpu, 1168, 1136, int(ends[-1]) + 256, [int(e) for e in ends], od, seed=5,
+          rows=np.r_[0:6, 253:259, 1022:1030, 1160:1168])
+
+
+def test_codes_behind_the_last_end_are_not_used(gpu):
+    a, ra, b, rb = _operands(256, 256, 512, 6)
+    a[:, 256:] = 0x7F          # NaN
+    rb[:, 2:] = np.inf
+    out = fp8.fp8_scaled_grouped_gemm_blockwise_wgrad(
+        torch.from_numpy(a).to(gpu), _colmajor(ra, gpu), torch.from_numpy(b).to(gpu), _colmajor(rb, gpu),
+        torch.tensor([128, 256], dtype=torch.int32, device=gpu), out_dtype=torch.float32)
+    assert out.isfinite().all()
+
+
+def test_a_malformed_table_stays_inside(gpu):
+    """Ends past the last column, negative or falling: clamped, an empty group's
+    output is zero."""
+    got = _case(gpu, 320, 272, 512, [128, 384, 10 ** 6, 2 ** 31 - 1], seed=7)
+    assert not got[3].any()
+    a, ra, b, rb = _operands(320, 272, 512, 8)
+    out = fp8.fp8_scaled_grouped_gemm_blockwise_wgrad(
+        torch.from_numpy(a).to(gpu), _colmajor(ra, gpu), torch.from_numpy(b).to(gpu), _colmajor(rb, gpu),
+        torch.tensor([-2 ** 31, 256, 128, -5], dtype=torch.int32, device=gpu), out_dtype=torch.float32)
+    assert not out[0].any() and not out[2].any() and not out[3].any()
+    ref, size = moe.grouped_wgrad(a, ra, b, rb, [0, 256])
+    check_gemm_output(host_f32(out[1]), ref[1], size[1], 4, "f32", "after a negative end")
+
+
+def test_strides(gpu):
+    """Operands out of wider buffers, row-major scales, an output of padded
+    rows and groups whose gaps stay as they were."""
+    M, N, K = 272, 288, 384
+    a, ra, b, rb = _operands(M, N, K, 9)
+    wide = torch.zeros(M, K + 64, dtype=torch.uint8, device=gpu)
+    wide[:, :K] = torch.from_numpy(a).to(gpu)
+    out = torch.full((2, M + 3, N + 5), 7.0, device=gpu)
+    fp8.fp8_scaled_grouped_gemm_blockwise_wgrad(
+        wide[:, :K], torch.from_numpy(ra).to(gpu), torch.from_numpy(b).to(gpu), torch.from_numpy(rb).to(gpu),
+        torch.tensor([256, 384], dtype=torch.int32, device=gpu), out=out[:, :M, :N])
+    ref, size = moe.grouped_wgrad(a, ra, b, rb, [256, 384])
+    check_gemm_output(host_f32(out[:, :M, :N]).reshape(-1, N), ref.reshape(-1, N), size.reshape(-1, N), 3, "f32", "strided")
+    assert (out[:, M:] == 7.0).all() and (out[:, :, N:] == 7.0).all()
+
+
+def test_no_groups_and_no_columns(gpu):
+    a, ra, b, rb = _operands(32, 48, 128, 10)
+    t = [torch.from_numpy(a).to(gpu), _colmajor(ra, gpu), torch.from_numpy(b).to(gpu), _colmajor(rb, gpu)]
+    assert fp8.fp8_scaled_grouped_gemm_blockwise_wgrad(*t, torch.empty(0, dtype=torch.int32, device=gpu)).shape == (0, 32, 48)
+    none = [t[0][:, :0], t[1][:, :0], t[2][:, :0], t[3][:, :0]]
+    out = fp8.fp8_scaled_grouped_gemm_blockwise_wgrad(*none, torch.zeros(3, dtype=torch.int32, device=gpu))
+    assert out.shape == (3, 32, 48) and not out.any()
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("G, rows, cols", [(1, 128, 128), (3, 256, 384), (5, 144, 272)])
+def test_grouped_quantizer_is_the_quantizer(gpu, G, rows, cols, transpose):
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn(G, rows + 4, cols + 8, generator=g).bfloat16().to(gpu)[:, :rows, :cols]
+    say("quant grouped", G, rows, cols, transpose)
+    q, recip = fp8.fp8_blockwise_quant_grouped(x, transpose)
+    for i in range(G):
+        want, want_recip = fp8.fp8_blockwise_quant(x[i], "128x128", transpose)
+        assert torch.equal(q[i], want) and torch.equal(recip[i], want_recip)
