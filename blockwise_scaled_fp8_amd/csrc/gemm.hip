@@ -86,7 +86,7 @@ struct GemmArgs {
   // Weight gradients of a grouped GEMM (KGROUP kernels): `groups` row-major
   // [M, N] outputs out_s_group elements apart, group g contracting the K
   // blocks [group_end[g-1] / 128, group_end[g] / 128); `groups` stays 0 in the
-  // kernels that split rows.
+  // kernels that split rows.  A persistent launch's tiles number tail_base.
   int64_t out_s_group;
 };
 
@@ -890,8 +890,10 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_v2_kernel(const GemmArgs 
     // One group's tiles after the other, each group dealt over all XCDs: with
     // a run of groups per XCD, the XCD of the longest ones finished last.
     const int tiles = p.tiles_m * p.tiles_n;
-    kgroup = blockIdx.x / tiles;
-    wg = xcd_remap(blockIdx.x - kgroup * tiles, tiles);
+    const int id = blockIdx.x + rnd * gridDim.x;
+    if (PERSIST && id >= p.tail_base) return;   // all tiles
+    kgroup = id / tiles;
+    wg = xcd_remap(id - kgroup * tiles, tiles);
   } else if (p.groups > 0) {
     if (p.group_part == 1 && !grouped_split_pays(p)) p.group_part = 0;
     const int T = grouped_tile_count<BM>(p);
@@ -1845,6 +1847,13 @@ bool grouped_wgrad_ok(const GemmProblem& p, int groups) {
 template <int OUT>
 static void launch_wgrad_cfg(int cfg, const GemmArgs& a, dim3 grid, hipStream_t stream) {
   constexpr int MODE = kBlockB1x128;
+  if constexpr (OUT == kOutBf16) {
+    if (a.rounds > 1) {
+      hipLaunchKernelGGL((gemm_v2_kernel<256, 256, 2, 4, 2, MODE, OUT, false, false, true, true>), grid, dim3(512), 0,
+                         stream, a);
+      return;
+    }
+  }
   switch (cfg) {
     case 3:
       hipLaunchKernelGGL((gemm_v2_kernel<256, 256, 2, 4, 2, MODE, OUT, false, false, false, true>), grid, dim3(512), 0,
@@ -1888,7 +1897,17 @@ hipError_t launch_grouped_wgrad(const GemmProblem& p, int groups, const int* gro
   a.rounds = 1;
   a.group_end = group_end;
   a.out_s_group = out_s_group;
-  const dim3 grid((unsigned)(groups * a.tiles_m * a.tiles_n));
+  const int tiles = groups * a.tiles_m * a.tiles_n, cus = num_cus();
+  // Two or more rounds of interior tiles: one workgroup per CU runs every cus-th
+  // tile, its stores draining under the next tile's contraction, which is as
+  // short as one group's rows.
+  const bool persist = cfg == 3 && p.out_kind == kOutBf16 && tiles >= 2 * cus && p.M % 256 == 0 && p.N % 256 == 0 &&
+                       p.ldo % 8 == 0 && out_s_group % 8 == 0 && ((size_t)p.out & 15) == 0;
+  if (persist) {
+    a.rounds = (tiles + cus - 1) / cus;
+    a.tail_base = tiles;
+  }
+  const dim3 grid((unsigned)(persist ? cus : tiles));
   if (p.out_kind == kOutBf16) launch_wgrad_cfg<kOutBf16>(cfg, a, grid, stream);
   else launch_wgrad_cfg<kOutF32>(cfg, a, grid, stream);
   return hipGetLastError();

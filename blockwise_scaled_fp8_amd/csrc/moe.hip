@@ -23,12 +23,16 @@ namespace fp8bw {
 // Sort.  A workgroup takes a run of slots, a wave a run of its run, 64 slots at
 // a time: the lanes that hold the same expert are found by one ballot per bit
 // of the expert's number, so a slot's rank is its wave's count so far (LDS)
-// plus the matching lanes below it, in slot order and without atomics.  Up to
+// plus the matching lanes below it, in slot order and without atomics.  Ranks
+// stay in registers until the first row of every (wave, expert) is known.  Up to
 // kSortOne slots take one workgroup and one launch (the latency of a decoding
-// step); more take a counting launch and a placing one, whose workgroups each
-// add up the counts of those before them.
-constexpr int64_t kSortOne = 4096;
-constexpr int kSortWaves = 4, kSortOneWaves = 8;
+// step, 5 us); more take a counting launch and a placing one, whose workgroups
+// each add up the counts of those before them.  Bound by latency: 33280 slots of
+// 16 experts are 0.4 MB.
+constexpr int kSortOneWaves = 16;        // 8 for more than 512 experts (LDS)
+constexpr int kSortOneRuns = 8;          // times 64 slots a wave
+constexpr int kSortWaves = 4, kSortRuns = 4;
+constexpr int64_t kSortOne = 64 * kSortOneWaves * kSortOneRuns;
 
 __device__ __forceinline__ int slot_expert(const MoeSortArgs& p, int64_t i, int64_t end) {
   if (i >= end) return p.experts;
@@ -38,50 +42,58 @@ __device__ __forceinline__ int slot_expert(const MoeSortArgs& p, int64_t i, int6
 
 // Lanes with this lane's expert.
 __device__ __forceinline__ uint64_t same_expert(int e, int bits) {
-  uint64_t m = ~0ull;
+  uint32_t lo = ~0u, hi = ~0u;
   for (int b = 0; b < bits; ++b) {
-    const bool set = (e >> b) & 1;
-    const uint64_t has = __ballot(set);
-    m &= set ? has : ~has;
+    const uint32_t set = (uint32_t)((int)((uint32_t)e << (31 - b)) >> 31);   // the bit, in every bit
+    const uint64_t has = __ballot(set != 0);
+    lo &= ~((uint32_t)has ^ set);
+    hi &= ~((uint32_t)(has >> 32) ^ set);
   }
-  return m;
+  return (uint64_t)hi << 32 | lo;
 }
 
-// Slots of each expert among [begin, end), which this wave alone counts in
-// `count`; visit(i, e, rank) for every slot with an expert.
-template <class F>
-__device__ __forceinline__ void rank_run(const MoeSortArgs& p, int64_t begin, int64_t end, int bits,
-                                         volatile int* count, F visit) {
+// Counts this lane's slot of expert e among the wave's: its rank there (of no
+// meaning without an expert).
+__device__ __forceinline__ int count_slot(int e, int experts, int bits, volatile int* count) {
   const int lane = threadIdx.x & 63;
-  const uint64_t below = (1ull << lane) - 1;
-  for (int64_t i0 = begin; i0 < end; i0 += 64) {
-    const int e = slot_expert(p, i0 + lane, end);
-    const uint64_t same = same_expert(e, bits);
-    if (e < p.experts) {
-      const int rank = count[e] + __popcll(same & below);
-      visit(i0 + lane, e, rank);
-      // the wave runs in step: every lane has read before the last one writes
-      __builtin_amdgcn_wave_barrier();
-      if ((same >> lane) == 1) count[e] = rank + 1;
-    } else {
-      visit(i0 + lane, e, 0);
-    }
+  const uint64_t same = same_expert(e, bits);
+  int rank = 0;
+  if (e < experts) {
+    rank = count[e] + __popcll(same & ((1ull << lane) - 1));
+    // the wave runs in step: every lane has read before the last one writes
+    __builtin_amdgcn_wave_barrier();
+    if ((same >> lane) == 1) count[e] = rank + 1;
   }
+  return rank;
 }
 
 __device__ __forceinline__ int expert_bits(int experts) { return 32 - __clz(experts); }
 
-template <int WAVES>
+// Experts and ranks of `runs` <= RUNS times 64 slots of a wave, all loads first.
+template <int RUNS>
+struct SlotRanks {
+  int expert[RUNS], rank[RUNS];
+  __device__ __forceinline__ SlotRanks(const MoeSortArgs& p, int64_t begin, int runs, int bits, int* count) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k)
+      if (k < runs) expert[k] = slot_expert(p, begin + 64 * k + lane, p.n);
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k)
+      if (k < runs) rank[k] = count_slot(expert[k], p.experts, bits, count);
+  }
+};
+
+// The counts of one workgroup's run, a multiple of what its waves take at a time.
+template <int WAVES, int RUNS>
 __global__ __launch_bounds__(64 * WAVES) void moe_count_kernel(const MoeSortArgs p, int64_t run) {
   extern __shared__ int lds[];
   int* const count = lds;   // [WAVES][experts]
   const int tid = threadIdx.x, wave = tid >> 6;
-  const int64_t per = run / WAVES;
   for (int k = tid; k < WAVES * p.experts; k += 64 * WAVES) count[k] = 0;
   __syncthreads();
-  const int64_t begin = blockIdx.x * run + wave * per;
-  rank_run(p, begin, min(begin + per, p.n), expert_bits(p.experts), count + wave * p.experts,
-           [](int64_t, int, int) {});
+  for (int64_t r = 0; r < run; r += 64 * RUNS * WAVES)
+    SlotRanks<RUNS>(p, blockIdx.x * run + r + wave * 64 * RUNS, RUNS, expert_bits(p.experts), count + wave * p.experts);
   __syncthreads();
   for (int e = tid; e < p.experts; e += 64 * WAVES) {
     int n = 0;
@@ -91,23 +103,25 @@ __global__ __launch_bounds__(64 * WAVES) void moe_count_kernel(const MoeSortArgs
   }
 }
 
-// Workgroup b of `groups` places the slots [b run, (b + 1) run).
-template <int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void moe_place_kernel(const MoeSortArgs p, int64_t run, int groups) {
+// Workgroup b of `groups` places the slots [b run, (b + 1) run), 64 `runs` of each
+// wave at a time.
+template <int WAVES, int RUNS>
+__global__ __launch_bounds__(64 * WAVES) void moe_place_kernel(const MoeSortArgs p, int64_t run, int runs, int groups) {
   constexpr int N = 64 * WAVES;
   extern __shared__ int lds[];
-  int* const count = lds;                        // [WAVES][experts], then each wave's next row
-  int* const first = lds + WAVES * p.experts;    // [experts] first row of an expert
-  int* const total = first + p.experts;          // [experts] its slots
+  int* const count = lds;                        // [WAVES][experts], then each wave's first row
+  int* const next = lds + WAVES * p.experts;     // [experts] this workgroup's next row of an expert
+  int* const total = next + p.experts;           // [experts] an expert's slots
   __shared__ int wave_rows[WAVES];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, E = p.experts;
   const int bits = expert_bits(E);
-  const int64_t per = run / WAVES;
-  for (int k = tid; k < WAVES * E; k += N) count[k] = 0;
-  __syncthreads();
-  const int64_t begin = blockIdx.x * run + wave * per, end = min(begin + per, p.n);
-  rank_run(p, begin, end, bits, count + wave * E, [](int64_t, int, int) {});
-  __syncthreads();
+  // Slots of this workgroup's first part, while the counts are on their way.
+  auto clear = [&]() {
+    for (int k = tid; k < WAVES * E; k += N) count[k] = 0;
+    __syncthreads();
+  };
+  clear();
+  SlotRanks<RUNS> s(p, blockIdx.x * run + wave * 64 * runs, runs, bits, count + wave * E);
   // Each expert's slots in all, and those of the workgroups before this one.
   // Few experts: several threads share an expert's list of counts.
   if (groups > 1) {
@@ -118,7 +132,7 @@ __global__ __launch_bounds__(64 * WAVES) void moe_place_kernel(const MoeSortArgs
       const int part = parts > 1 ? tid / E : 0, e = parts > 1 ? tid % E : e0 + tid;
       int all = 0, mine = 0;
       if (part < parts && e < E) {
-#pragma unroll 4
+#pragma unroll 8
         for (int b = part; b < groups; b += parts) {
           const int c = p.counts[(int64_t)b * E + e];
           all += c;
@@ -136,15 +150,16 @@ __global__ __launch_bounds__(64 * WAVES) void moe_place_kernel(const MoeSortArgs
         all += before[(parts + k) * E + e];
       }
       total[e] = all;
-      first[e] = mine;   // for now
+      next[e] = mine;   // for now
     }
   } else {
+    __syncthreads();
     for (int e = tid; e < E; e += N) {
       int all = 0;
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) all += count[w * E + e];
       total[e] = all;
-      first[e] = 0;
+      next[e] = 0;
     }
   }
   __syncthreads();
@@ -152,7 +167,8 @@ __global__ __launch_bounds__(64 * WAVES) void moe_place_kernel(const MoeSortArgs
   int base = 0;
   for (int e0 = 0; e0 < E; e0 += N) {
     const int e = e0 + tid;
-    const int padded = e < E ? (total[e] + p.align - 1) / p.align * p.align : 0;
+    const int slots = e < E ? total[e] : 0;
+    const int padded = (slots + p.align - 1) / p.align * p.align;
     int sum = padded;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -169,73 +185,94 @@ __global__ __launch_bounds__(64 * WAVES) void moe_place_kernel(const MoeSortArgs
     }
     if (e < E) {
       if (blockIdx.x == 0) p.group_end[e] = base + sum;
-      int row = base + sum - padded + first[e];   // this workgroup's first row of the expert
-      first[e] = base + sum - padded;
+      next[e] += base + sum - padded;
+      total[e] = base + sum - padded + slots;   // from here on: the expert's last row + 1
+    }
+    base += all;
+    __syncthreads();
+  }
+  for (int64_t part = 0;;) {
+    for (int e = tid; e < E; e += N) {
+      int row = next[e];
 #pragma unroll
       for (int w = 0; w < WAVES; ++w) {
         const int n = count[w * E + e];
         count[w * E + e] = row;
         row += n;
       }
+      next[e] = row;
     }
-    base += all;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k) {
+      const int64_t i = blockIdx.x * run + part + (wave * runs + k) * 64 + lane;
+      if (k >= runs || i >= p.n) continue;
+      int r = -1;
+      if (s.expert[k] < E) {
+        r = count[wave * E + s.expert[k]] + s.rank[k];
+        p.source[r] = (int)i;
+      }
+      p.row[i] = r;
+    }
+    part += (int64_t)runs * N;
+    if (part >= run) break;
+    __syncthreads();
+    clear();
+    s = SlotRanks<RUNS>(p, blockIdx.x * run + part + wave * 64 * runs, runs, bits, count + wave * E);
     __syncthreads();
   }
-  rank_run(p, begin, end, bits, count + wave * E, [&](int64_t i, int e, int r) {
-    if (e < E) {
-      p.row[i] = r;
-      p.source[r] = (int)i;
-    } else if (i < end) {
-      p.row[i] = -1;
-    }
-  });
-  // Rows without a slot: an expert's padding (one wave an expert), then what
-  // lies behind the last end.
+  // Rows without a slot: from an expert's last row to the next multiple of align
+  // (its first row is one), and what lies behind the last end.
   for (int e = (int)blockIdx.x * WAVES + wave; e < E; e += groups * WAVES) {
-    const int n = total[e], padded = (n + p.align - 1) / p.align * p.align;
-    for (int k = n + lane; k < padded; k += 64) p.source[first[e] + k] = -1;
+    const int last = (total[e] + p.align - 1) / p.align * p.align;
+    for (int k = total[e] + lane; k < last; k += 64) p.source[k] = -1;
   }
   for (int64_t r = base + (int64_t)blockIdx.x * N + tid; r < p.rows; r += (int64_t)groups * N) p.source[r] = -1;
 }
 
-// Workgroups and slots of each; the runs are whole multiples of what the waves
-// take at a time, and at most 256 workgroups read each other's counts.
-static int sort_groups(int64_t n, int64_t* run) {
-  if (n <= kSortOne) {
-    *run = (n + 64 * kSortOneWaves - 1) / (64 * kSortOneWaves) * (64 * kSortOneWaves);
+// Workgroups and slots of each; with several, their runs are whole multiples of
+// what the waves take at a time, and at most 256 read each other's counts.
+static int sort_groups(int64_t n, int experts, int64_t* run) {
+  if (n <= (experts > 512 ? kSortOne / 2 : kSortOne)) {
+    *run = n;
     return 1;
   }
-  const int64_t unit = 64 * kSortWaves;
+  const int64_t unit = 64 * kSortWaves * kSortRuns;
   int64_t r = (n + 255) / 256;
   r = (r + unit - 1) / unit * unit;
-  if (r < 4 * unit) r = 4 * unit;
   *run = r;
   return (int)((n + r - 1) / r);
 }
 
 size_t moe_sort_ws_bytes(int64_t n, int experts) {
   int64_t run;
-  const int groups = sort_groups(n, &run);
+  const int groups = sort_groups(n, experts, &run);
   return groups > 1 ? (size_t)groups * (size_t)experts * sizeof(int) : 0;
 }
 
 hipError_t launch_moe_sort(const MoeSortArgs& p, hipStream_t stream) {
   int64_t run;
-  const int groups = sort_groups(p.n, &run);
+  const int groups = sort_groups(p.n, p.experts, &run);
   const size_t E = (size_t)p.experts;
   if (groups == 1) {
-    hipLaunchKernelGGL(moe_place_kernel<kSortOneWaves>, dim3(1), dim3(64 * kSortOneWaves),
-                       (kSortOneWaves + 2) * E * sizeof(int), stream, p, run, 1);
+    constexpr int R = kSortOneRuns;
+    const int waves = E > 512 ? kSortOneWaves / 2 : kSortOneWaves;
+    const int runs = p.n > 64 * waves ? (int)((p.n + 64 * waves - 1) / (64 * waves)) : 1;
+    const size_t lds = (waves + 2) * E * sizeof(int);
+    if (E > 512)
+      hipLaunchKernelGGL((moe_place_kernel<kSortOneWaves / 2, R>), dim3(1), dim3(64 * waves), lds, stream, p, run, runs, 1);
+    else
+      hipLaunchKernelGGL((moe_place_kernel<kSortOneWaves, R>), dim3(1), dim3(64 * waves), lds, stream, p, run, runs, 1);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(moe_count_kernel<kSortWaves>, dim3(groups), dim3(64 * kSortWaves),
-                     kSortWaves * E * sizeof(int), stream, p, run);
+  constexpr int W = kSortWaves, R = kSortRuns;
+  hipLaunchKernelGGL((moe_count_kernel<W, R>), dim3(groups), dim3(64 * W), W * E * sizeof(int), stream, p, run);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   int parts = 1;
-  while (parts * 2 * p.experts <= 64 * kSortWaves) parts *= 2;
-  hipLaunchKernelGGL(moe_place_kernel<kSortWaves>, dim3(groups), dim3(64 * kSortWaves),
-                     (kSortWaves + 2 + 2 * parts) * E * sizeof(int), stream, p, run, groups);
+  while (parts * 2 * p.experts <= 64 * W) parts *= 2;
+  hipLaunchKernelGGL((moe_place_kernel<W, R>), dim3(groups), dim3(64 * W), (W + 2 + 2 * parts) * E * sizeof(int), stream,
+                     p, run, R, groups);
   return hipGetLastError();
 }
 
@@ -283,21 +320,21 @@ __device__ __forceinline__ void fill_empty_rows(const MoeTable& t, const Layouts
 }
 
 template <int P>
-__global__ __launch_bounds__(256) void moe_gather_rows_kernel(const MoeGatherArgs p, int64_t pieces, int fill) {
+__global__ __launch_bounds__(256) void moe_gather_rows_kernel(const MoeGatherArgs p, uint32_t pieces, int fill) {
   if ((int)blockIdx.x < fill) {
     fill_empty_rows(p.table, p.out, p.cols, (int64_t)blockIdx.x * 16);
     return;
   }
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63;
   const MoeTable& t = p.table;
+  const Pieces<P> at(blockIdx.x - fill, pieces);
   uint4 u[P];
   int64_t tok[P], col[P];
   bool in[P];
 #pragma unroll
   for (int k = 0; k < P; ++k) {
-    const int64_t item = ((int64_t)blockIdx.x - fill) * 4 * P + 4 * k + wave;
-    tok[k] = item / pieces;
-    col[k] = (item - tok[k] * pieces) * 512 + lane * 8;
+    tok[k] = at.row[k];
+    col[k] = at.col[k] + lane * 8;
     in[k] = tok[k] < t.tokens && col[k] < p.cols;
     u[k] = load_stream(p.x + (in[k] ? tok[k] * p.ld_x + col[k] : 0));
     if (!in[k]) u[k] = make_uint4(0, 0, 0, 0);
@@ -330,72 +367,73 @@ __global__ __launch_bounds__(256) void moe_gather_rows_kernel(const MoeGatherArg
 }
 
 // Gather with transposed codes: 128 x 128 tiles of the sorted rows, from which
-// every layout is written.
+// every layout is written.  A tile's corner is in scalar registers and a thread's
+// offsets from it in 32 bits (the host keeps 128 leading dimensions below 2^31
+// bytes).
 __global__ __launch_bounds__(512, 4) void moe_gather_tile_kernel(const MoeGatherArgs p, int col_tiles) {
   __shared__ TileLds<1> L;
   __shared__ int token[128];
   __shared__ float factor[128];
-  const int tid = threadIdx.x, g = tid & 15, j = tid >> 4;
+  const int tid = threadIdx.x, lane16 = tid & 15, row0 = (tid >> 4) * 4, col = lane16 * 8;
   const int64_t rb = blockIdx.x / col_tiles, cb = blockIdx.x - rb * col_tiles;
-  const int64_t col = cb * 128 + g * 8;
-  const bool col_in = col < p.cols;
+  const int rows = (int)min(p.table.rows - rb * 128, (int64_t)128);   // of the tile
+  const int cols = (int)min(p.cols - cb * 128, (int64_t)128);
   const LayoutsOut& o = p.out;
   if (tid < 128) {
-    const int64_t r = rb * 128 + tid;
-    const int slot = r < p.table.rows ? p.table.source[r] : -1;
-    const int tk = slot < 0 ? -1 : slot / p.table.topk;
-    token[tid] = tk < p.table.tokens ? tk : -1;
-    factor[tid] = tk < 0 || tk >= p.table.tokens ? 0.f : slot_weight(p.weight, slot);
+    const int slot = tid < rows ? p.table.source[rb * 128 + tid] : -1;
+    const bool has = slot >= 0 && slot < p.table.tokens * p.table.topk;
+    token[tid] = has ? slot / p.table.topk : -1;
+    factor[tid] = has ? slot_weight(p.weight, slot) : 0.f;
   }
   __syncthreads();
+  const uint16_t* const x = p.x + cb * 128;
   uint4 u[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int tk = token[4 * j + k];
-    const bool in = col_in && tk >= 0;
-    u[k] = *(const uint4*)(p.x + (in ? tk * p.ld_x + col : 0));
+    const int tk = token[row0 + k];
+    const bool in = col < cols && tk >= 0;
+    u[k] = *(const uint4*)(x + (in ? tk * p.ld_x + col : 0));
     if (!in) u[k] = make_uint4(0, 0, 0, 0);
   }
+  // (Without weights the factor is 1; the product spares the maxima the step
+  // that quiets a value of unknown origin.)
   float v[4][8];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     unpack8(u[k], v[k]);
-    if (p.weight.p) {
-      const float w = factor[4 * j + k];
+    const float w = factor[row0 + k];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) v[k][c] *= w;
-    }
+    for (int c = 0; c < 8; ++c) v[k][c] *= w;
   }
   tile_column_max(L, 0, v);
+  if (o.y) {
+    uint16_t* const corner = o.y + rb * 128 * o.ld_y + cb * 128;
+    uint32_t at = row0 * (uint32_t)o.ld_y + col;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int64_t r = rb * 128 + 4 * j + k;
-    const bool in = col_in && r < p.table.rows;
-    if (o.y && in) store_row8(o, r, col, v[k]);
-    if (o.q) {
-      float recip;
-      const uint2 code = block_codes(v[k], &recip);
-      if (in) store_codes8(o, r, col, code, recip);
-    }
+    for (int k = 0; k < 4; ++k, at += (uint32_t)o.ld_y)
+      if (row0 + k < rows && col < cols) *(uint4*)(corner + at) = pack8(v[k]);
+  }
+  if (o.q) {
+    float amax[4], scale[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) amax[k] = row16_max(absmax8(v[k]));
+    const float recip = row16_scales(amax, scale);
+    uint8_t* const corner = o.q + rb * 128 * o.ld_q + cb * 128;
+    uint32_t at = row0 * (uint32_t)o.ld_q + col;
+#pragma unroll
+    for (int k = 0; k < 4; ++k, at += (uint32_t)o.ld_q)
+      if (row0 + k < rows && col < cols) *(uint2*)(corner + at) = codes8(v[k], scale[k]);
+    if (lane16 < 4 && row0 + lane16 < rows) o.recip[(rb * 128 + row0 + lane16) * o.rs_row + cb * o.rs_kb] = recip;
   }
   __syncthreads();
   if (tid < 128) {
     const float s = tile_column_scale(L, 0, tid);
-    if (cb * 128 + tid < p.cols) o.recip_t[(cb * 128 + tid) * o.rst_row + rb * o.rst_kb] = recip_of_scale(s);
+    if (tid < cols) o.recip_t[(cb * 128 + tid) * o.rst_row + rb * o.rst_kb] = recip_of_scale(s);
   }
   __syncthreads();
   tile_codes(L, 0, v);
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int id = tid + 512 * i, oc = id >> 3, seg = id & 7;
-    const uint4 w = tile_piece(L, 0, oc, seg);
-    const int64_t orow = cb * 128 + oc, ocol = rb * 128 + 16 * seg;
-    if (orow < p.cols && ocol < p.table.rows) {
-      const u32x4 t = {w.x, w.y, w.z, w.w};
-      __builtin_nontemporal_store(t, (u32x4*)(o.qt + orow * o.ld_qt + ocol));
-    }
-  }
+  store_transposed(L, 0, o.qt + cb * 128 * o.ld_qt + rb * 128, o.ld_qt, rows, cols);
 }
 
 // The router's weights' gradient: one workgroup a token, which reads its row of
@@ -463,10 +501,10 @@ hipError_t launch_moe_gather(const MoeGatherArgs& p, hipStream_t stream) {
   const int64_t pieces = (p.cols + 511) / 512, items = t.tokens * pieces, fill = (t.rows + 15) / 16;
   if (items >= 4096)
     hipLaunchKernelGGL(moe_gather_rows_kernel<4>, dim3((unsigned)(fill + (items + 15) / 16)), dim3(256), 0, stream, p,
-                       pieces, (int)fill);
+                       (uint32_t)pieces, (int)fill);
   else
     hipLaunchKernelGGL(moe_gather_rows_kernel<1>, dim3((unsigned)(fill + (items + 3) / 4)), dim3(256), 0, stream, p,
-                       pieces, (int)fill);
+                       (uint32_t)pieces, (int)fill);
   return hipGetLastError();
 }
 
@@ -474,17 +512,17 @@ hipError_t launch_moe_gather(const MoeGatherArgs& p, hipStream_t stream) {
 // Combine: a wave takes P pieces of 512 columns of tokens, and of each the
 // token's rows, two slots in flight; fp32 sums in the slots' order.
 template <int P>
-__global__ __launch_bounds__(256) void moe_combine_kernel(const MoeCombineArgs p, int64_t pieces) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+__global__ __launch_bounds__(256) void moe_combine_kernel(const MoeCombineArgs p, uint32_t pieces) {
+  const int lane = threadIdx.x & 63;
   const MoeTable& t = p.table;
+  const Pieces<P> at(blockIdx.x, pieces);
   int64_t tok[P], col[P];
   bool in[P];
   float sum[P][8] = {};
 #pragma unroll
   for (int k = 0; k < P; ++k) {
-    const int64_t item = (int64_t)blockIdx.x * 4 * P + 4 * k + wave;
-    tok[k] = item / pieces;
-    col[k] = (item - tok[k] * pieces) * 512 + lane * 8;
+    tok[k] = at.row[k];
+    col[k] = at.col[k] + lane * 8;
     in[k] = tok[k] < t.tokens && col[k] < p.cols;
   }
   constexpr int J = P == 1 ? 8 : 2;   // slots in flight
@@ -529,9 +567,9 @@ hipError_t launch_moe_combine(const MoeCombineArgs& p, hipStream_t stream) {
   const int64_t pieces = (p.cols + 511) / 512, items = p.table.tokens * pieces;
   if (items == 0) return hipSuccess;
   if (items >= 4096)
-    hipLaunchKernelGGL(moe_combine_kernel<4>, dim3((unsigned)((items + 15) / 16)), dim3(256), 0, stream, p, pieces);
+    hipLaunchKernelGGL(moe_combine_kernel<4>, dim3((unsigned)((items + 15) / 16)), dim3(256), 0, stream, p, (uint32_t)pieces);
   else
-    hipLaunchKernelGGL(moe_combine_kernel<1>, dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, p, pieces);
+    hipLaunchKernelGGL(moe_combine_kernel<1>, dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, p, (uint32_t)pieces);
   return hipGetLastError();
 }
 

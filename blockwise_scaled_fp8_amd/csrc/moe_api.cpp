@@ -2,6 +2,8 @@
 // gated activation, the grouped weight gradient and the grouped quantizer.
 // Validation and dispatch only; the contracts are in include/fp8bw.h.
 
+#include <initializer_list>
+
 #include "check.h"
 #include "launch.h"
 
@@ -47,6 +49,15 @@ fp8bw::LayoutsOut layouts(const fp8bw_layouts& o, int64_t rows, int64_t cols, in
   r.recip_t = o.recip_t; r.rst_row = used_stride(cols, o.rst_row);
   r.rst_kb = used_stride(cdiv(rows, 128), o.rst_kb);
   return r;
+}
+
+// A tile's 128 rows are addressed with 32-bit byte offsets from its corner.
+int check_tile_strides(std::initializer_list<int64_t> bf16_or_f32, std::initializer_list<int64_t> codes) {
+  for (int64_t s : bf16_or_f32)
+    if (s >= ((int64_t)1 << 22)) return fail(FP8BW_ERR_LAYOUT, "transposed codes need strides below 2^22 (%lld)", (long long)s);
+  for (int64_t s : codes)
+    if (s >= ((int64_t)1 << 24)) return fail(FP8BW_ERR_LAYOUT, "transposed codes need strides of codes below 2^24 (%lld)", (long long)s);
+  return FP8BW_OK;
 }
 
 // Launch sizes of a [rows, cols] result and, with them, `tokens` rows read or written.
@@ -228,6 +239,7 @@ FP8BW_API int fp8bw_swiglu_fwd(const void* h, int64_t ld_h, int64_t rows, int64_
   p.out = layouts(*out, rows, ffn, blocks);
   p.hq = (uint8_t*)hq; p.ld_hq = used_stride(rows, ld_hq);
   p.h_recip = h_recip; p.hr_row = used_stride(rows, hr_row); p.hr_kb = hr_kb;
+  if (p.out.qt && (st = check_tile_strides({p.ld_h}, {p.out.ld_qt})) != FP8BW_OK) return st;
   return hip_status(fp8bw::launch_swiglu_fwd(p, (hipStream_t)stream), "fp8bw_swiglu_fwd");
 }
 
@@ -261,6 +273,11 @@ FP8BW_API int fp8bw_swiglu_bwd(const void* dy, int64_t ld_dy, const void* h, int
   p.dh = layouts(*dh, rows, 2 * ffn, 2 * blocks);
   p.act_qt = (uint8_t*)act_qt; p.ld_act_qt = ld_act_qt;
   p.act_recip_t = act_recip_t; p.art_row = art_row; p.art_kb = used_stride(cdiv(rows, 128), art_kb);
+  if ((p.dh.qt || act_qt) &&
+      (st = check_tile_strides({p.ld_dy, h_recip ? 0 : p.ld_h, h_recip ? p.hr_row : 0, p.dh.y ? p.dh.ld_y : 0},
+                               {h_recip ? p.ld_h : 0, p.dh.q ? p.dh.ld_q : 0, p.dh.qt ? p.dh.ld_qt : 0,
+                                act_qt ? ld_act_qt : 0})) != FP8BW_OK)
+    return st;
   return hip_status(fp8bw::launch_swiglu_bwd(p, (hipStream_t)stream), "fp8bw_swiglu_bwd");
 }
 

@@ -24,13 +24,19 @@ __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
 }
 
-// Writes one 16-lane row's 1x128 block of codes of f and its reciprocal scale.
-__device__ __forceinline__ void put_codes8(const float (&f)[8], uint8_t* q, float* recip, bool in) {
-  const float s = scale_from_amax(row16_max(absmax8(f)));
-  const uint2 code = codes8(f, s);
-  if (in) {
+// KEPT: codes that nothing reads before the backward, which pass the caches by and
+// leave them to the next product's operand (33280 rows of 2 x 5120, this kernel
+// after itself 243 -> 237 us; the operand's own codes written that way cost the
+// product behind more than they save here).
+template <bool KEPT = false>
+__device__ __forceinline__ void put_codes8(const float (&f)[8], float scale, uint8_t* q, bool in) {
+  const uint2 code = codes8(f, scale);
+  if (!in) return;
+  if constexpr (KEPT) {
+    const u32x2 c = {code.x, code.y};
+    __builtin_nontemporal_store(c, (u32x2*)q);
+  } else {
     *(uint2*)q = code;
-    if ((threadIdx.x & 15) == 0) *recip = recip_of_scale(s);
   }
 }
 
@@ -67,16 +73,16 @@ __device__ __forceinline__ void half_values(const HalfIn& x, float (&f)[8]) {
 // Rows: a wave takes P pieces of 512 columns of a row of v, all loads in flight
 // first; a 16-lane DPP row holds one 1x128 block of each half.
 template <int P>
-__global__ __launch_bounds__(256) void swiglu_fwd_rows_kernel(const SwigluFwdArgs p, int64_t pieces) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+__global__ __launch_bounds__(256) void swiglu_fwd_rows_kernel(const SwigluFwdArgs p, uint32_t pieces) {
+  const int lane = threadIdx.x & 63;
+  const Pieces<P> at(blockIdx.x, pieces);
   HalfIn gate[P], up[P];
   int64_t row[P], col[P];
   bool in[P];
 #pragma unroll
   for (int k = 0; k < P; ++k) {
-    const int64_t item = (int64_t)blockIdx.x * 4 * P + 4 * k + wave;
-    row[k] = item / pieces;
-    col[k] = (item - row[k] * pieces) * 512 + lane * 8;
+    row[k] = at.row[k];
+    col[k] = at.col[k] + lane * 8;
     in[k] = row[k] < p.rows && col[k] < p.ffn;
     gate[k] = load_half<false>(p.h, p.ld_h, nullptr, 0, 0, p.ffn, row[k], col[k], 0, in[k]);
     up[k] = load_half<false>(p.h, p.ld_h, nullptr, 0, 0, p.ffn, row[k], col[k], 1, in[k]);
@@ -92,12 +98,23 @@ __global__ __launch_bounds__(256) void swiglu_fwd_rows_kernel(const SwigluFwdArg
 #pragma unroll
     for (int c = 0; c < 8; ++c) v[c] = g[c] * sigmoid(g[c]) * u[c];
     if (p.out.y && in[k]) *(uint4*)(p.out.y + r * p.out.ld_y + c0) = pack8(v);
-    if (p.out.q) put_codes8(v, p.out.q + r * p.out.ld_q + c0, p.out.recip + r * p.out.rs_row + kb * p.out.rs_kb, in[k]);
+    if (!p.out.q && !p.hq) continue;
+    // three blocks: v, g, u
+    const float amax[3] = {row16_max(absmax8(v)), row16_max(absmax8(g)), row16_max(absmax8(u))};
+    float scale[3];
+    const float recip = row16_scales(amax, scale);
+    const int i = lane & 15;   // writes the scale of block i
+    if (p.out.q) {
+      put_codes8(v, scale[0], p.out.q + r * p.out.ld_q + c0, in[k]);
+      if (in[k] && i == 0) p.out.recip[r * p.out.rs_row + kb * p.out.rs_kb] = recip;
+    }
     if (p.hq) {
       uint8_t* const hq = p.hq + r * p.ld_hq + c0;
-      float* const hr = p.h_recip + r * p.hr_row + kb * p.hr_kb;
-      put_codes8(g, hq, hr, in[k]);
-      put_codes8(u, hq + p.ffn, hr + blocks * p.hr_kb, in[k]);
+      put_codes8<true>(g, scale[1], hq, in[k]);
+      put_codes8<true>(u, scale[2], hq + p.ffn, in[k]);
+      const int64_t first = c0 - 8 * i;   // the block's first column: in range where the block has any
+      if (first < p.ffn && (i == 1 || i == 2))
+        p.h_recip[r * p.hr_row + ((i - 1) * blocks + (first >> 7)) * p.hr_kb] = recip;
     }
   }
 }
@@ -113,17 +130,17 @@ __device__ __forceinline__ void swiglu_grad(float& g, float& u, float& d) {
 }
 
 template <int P, bool CODES>
-__global__ __launch_bounds__(256) void swiglu_bwd_rows_kernel(const SwigluBwdArgs p, int64_t pieces) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+__global__ __launch_bounds__(256) void swiglu_bwd_rows_kernel(const SwigluBwdArgs p, uint32_t pieces) {
+  const int lane = threadIdx.x & 63;
+  const Pieces<P> at(blockIdx.x, pieces);
   HalfIn gate[P], up[P];
   uint4 dy[P];
   int64_t row[P], col[P];
   bool in[P];
 #pragma unroll
   for (int k = 0; k < P; ++k) {
-    const int64_t item = (int64_t)blockIdx.x * 4 * P + 4 * k + wave;
-    row[k] = item / pieces;
-    col[k] = (item - row[k] * pieces) * 512 + lane * 8;
+    row[k] = at.row[k];
+    col[k] = at.col[k] + lane * 8;
     in[k] = row[k] < p.rows && col[k] < p.ffn;
     dy[k] = load_stream(p.dy + (in[k] ? row[k] * p.ld_dy + col[k] : 0));
     gate[k] = load_half<CODES>(p.h, p.ld_h, p.h_recip, p.hr_row, p.hr_kb, p.ffn, row[k], col[k], 0, in[k]);
@@ -134,7 +151,7 @@ __global__ __launch_bounds__(256) void swiglu_bwd_rows_kernel(const SwigluBwdArg
 #pragma unroll
   for (int k = 0; k < P; ++k) {
     if (row[k] >= p.rows) return;
-    const int64_t r = row[k], c0 = col[k], kb = c0 >> 7;
+    const int64_t r = row[k], c0 = col[k];
     float g[8], u[8], d[8];
     half_values<CODES>(gate[k], g);
     half_values<CODES>(up[k], u);
@@ -148,146 +165,212 @@ __global__ __launch_bounds__(256) void swiglu_bwd_rows_kernel(const SwigluBwdArg
     }
     if (p.dh.q) {
       uint8_t* const q = p.dh.q + r * p.dh.ld_q + c0;
-      float* const recip = p.dh.recip + r * p.dh.rs_row + kb * p.dh.rs_kb;
-      put_codes8(g, q, recip, in[k]);
-      put_codes8(u, q + p.ffn, recip + blocks * p.dh.rs_kb, in[k]);
+      const float amax[2] = {row16_max(absmax8(g)), row16_max(absmax8(u))};
+      float scale[2];
+      const float recip = row16_scales(amax, scale);
+      put_codes8(g, scale[0], q, in[k]);
+      put_codes8(u, scale[1], q + p.ffn, in[k]);
+      const int i = lane & 15;
+      const int64_t first = c0 - 8 * i;
+      if (first < p.ffn && i < 2) p.dh.recip[r * p.dh.rs_row + (i * blocks + (first >> 7)) * p.dh.rs_kb] = recip;
     }
   }
 }
 
 // ---------------------------------------------------------------------------
 // Tiles: 128 rows x 128 columns of v (and of both halves), from which the
-// transposed codes and every other layout are written.
-__device__ __forceinline__ void store_transposed(uint8_t* qt, int64_t ld_qt, int64_t cols, int64_t rows, int64_t cb,
-                                                 int64_t rb, int oc, int seg, const uint4& w) {
-  const int64_t orow = cb * 128 + oc, ocol = rb * 128 + 16 * seg;
-  if (orow < cols && ocol < rows) {
-    const u32x4 t = {w.x, w.y, w.z, w.w};
-    __builtin_nontemporal_store(t, (u32x4*)(qt + orow * ld_qt + ocol));
+// transposed codes and every other layout are written.  A tile's corner is in
+// scalar registers and a thread's offsets from it in 32 bits (the host keeps
+// 128 leading dimensions below 2^31 bytes): with 64-bit addresses a lane the
+// backward spilled.
+struct Tile {
+  int64_t rb, cb;     // row and column block
+  int row, col;       // this thread's first row and column, of 4 and of 8
+  int rows, cols;     // of the tile that exist
+};
+__device__ __forceinline__ Tile tile_of(int64_t rows, int64_t ffn, int col_tiles) {
+  Tile t;
+  t.rb = blockIdx.x / col_tiles;
+  t.cb = blockIdx.x - t.rb * col_tiles;
+  t.row = (threadIdx.x >> 4) * 4;
+  t.col = (threadIdx.x & 15) * 8;
+  t.rows = (int)min(rows - t.rb * 128, (int64_t)128);
+  t.cols = (int)min(ffn - t.cb * 128, (int64_t)128);
+  return t;
+}
+
+// Both halves of h's rows, as the row kernels hold them.
+template <bool CODES>
+__device__ __forceinline__ void load_tile_halves(const Tile& t, const void* h, int64_t ld_h, const float* recip,
+                                                 int64_t hr_row, int64_t hr_kb, int64_t ffn, HalfIn (&gate)[4],
+                                                 HalfIn (&up)[4]) {
+  const int64_t corner = t.rb * 128 * ld_h + t.cb * 128, blocks = (ffn + 127) >> 7;
+  const float* const gr = CODES ? recip + t.rb * 128 * hr_row + t.cb * hr_kb : nullptr;
+  const float* const ur = CODES ? gr + blocks * hr_kb : nullptr;
+  const uint32_t row_at = t.row * (uint32_t)ld_h + t.col, recip_at = t.row * (uint32_t)hr_row;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const bool in = t.row + k < t.rows && t.col < t.cols;
+    const uint32_t at = in ? row_at + (uint32_t)k * (uint32_t)ld_h : 0;
+    if constexpr (CODES) {
+      const uint8_t* const g = (const uint8_t*)h + corner;
+      const u32x2 a = __builtin_nontemporal_load((const u32x2*)(g + at));
+      const u32x2 b = __builtin_nontemporal_load((const u32x2*)(g + ffn + at));
+      gate[k].raw = in ? make_uint4(a.x, a.y, 0, 0) : make_uint4(0, 0, 0, 0);
+      up[k].raw = in ? make_uint4(b.x, b.y, 0, 0) : make_uint4(0, 0, 0, 0);
+      const uint32_t ar = in ? recip_at + (uint32_t)k * (uint32_t)hr_row : 0;
+      gate[k].recip = gr[ar];
+      up[k].recip = ur[ar];
+    } else {
+      const uint16_t* const g = (const uint16_t*)h + corner;
+      gate[k].raw = load_stream(g + at);
+      up[k].raw = load_stream(g + ffn + at);
+      if (!in) gate[k].raw = up[k].raw = make_uint4(0, 0, 0, 0);
+    }
   }
 }
 
 __global__ __launch_bounds__(512, 4) void swiglu_fwd_tile_kernel(const SwigluFwdArgs p, int col_tiles) {
   __shared__ TileLds<1> L;
-  const int tid = threadIdx.x, g16 = tid & 15, j = tid >> 4;
-  const int64_t rb = blockIdx.x / col_tiles, cb = blockIdx.x - rb * col_tiles;
-  const int64_t col = cb * 128 + g16 * 8, blocks = (p.ffn + 127) >> 7;
+  const Tile t = tile_of(p.rows, p.ffn, col_tiles);
+  const int tid = threadIdx.x, lane16 = tid & 15;
+  const int64_t blocks = (p.ffn + 127) >> 7;
   const LayoutsOut& o = p.out;
   HalfIn gate[4], up[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int64_t r = rb * 128 + 4 * j + k;
-    const bool in = col < p.ffn && r < p.rows;
-    gate[k] = load_half<false>(p.h, p.ld_h, nullptr, 0, 0, p.ffn, r, col, 0, in);
-    up[k] = load_half<false>(p.h, p.ld_h, nullptr, 0, 0, p.ffn, r, col, 1, in);
-  }
+  load_tile_halves<false>(t, p.h, p.ld_h, nullptr, 0, 0, p.ffn, gate, up);
   float v[4][8];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int64_t r = rb * 128 + 4 * j + k;
-    const bool in = col < p.ffn && r < p.rows;
+    const int64_t r = t.rb * 128 + t.row + k;
+    const bool row_in = t.row + k < t.rows, in = row_in && t.col < t.cols;
     float g[8], u[8];
     half_values<false>(gate[k], g);
     half_values<false>(up[k], u);
 #pragma unroll
     for (int c = 0; c < 8; ++c) v[k][c] = g[c] * sigmoid(g[c]) * u[c];
+    const int64_t col = t.cb * 128 + t.col;
     if (o.y && in) *(uint4*)(o.y + r * o.ld_y + col) = pack8(v[k]);
-    if (o.q) put_codes8(v[k], o.q + r * o.ld_q + col, o.recip + r * o.rs_row + cb * o.rs_kb, in);
+    if (!o.q && !p.hq) continue;
+    const float amax[3] = {row16_max(absmax8(v[k])), row16_max(absmax8(g)), row16_max(absmax8(u))};
+    float scale[3];
+    const float recip = row16_scales(amax, scale);
+    if (o.q) {
+      put_codes8(v[k], scale[0], o.q + r * o.ld_q + col, in);
+      if (lane16 == 0 && row_in) o.recip[r * o.rs_row + t.cb * o.rs_kb] = recip;
+    }
     if (p.hq) {
       uint8_t* const hq = p.hq + r * p.ld_hq + col;
-      float* const hr = p.h_recip + r * p.hr_row + cb * p.hr_kb;
-      put_codes8(g, hq, hr, in);
-      put_codes8(u, hq + p.ffn, hr + blocks * p.hr_kb, in);
+      put_codes8<true>(g, scale[1], hq, in);
+      put_codes8<true>(u, scale[2], hq + p.ffn, in);
+      if ((lane16 == 1 || lane16 == 2) && row_in)
+        p.h_recip[r * p.hr_row + ((lane16 - 1) * blocks + t.cb) * p.hr_kb] = recip;
     }
   }
   tile_column_max(L, 0, v);
   __syncthreads();
   if (tid < 128) {
     const float s = tile_column_scale(L, 0, tid);
-    if (cb * 128 + tid < p.ffn) o.recip_t[(cb * 128 + tid) * o.rst_row + rb * o.rst_kb] = recip_of_scale(s);
+    if (tid < t.cols) o.recip_t[(t.cb * 128 + tid) * o.rst_row + t.rb * o.rst_kb] = recip_of_scale(s);
   }
   __syncthreads();
   tile_codes(L, 0, v);
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int id = tid + 512 * i, oc = id >> 3, seg = id & 7;
-    store_transposed(o.qt, o.ld_qt, p.ffn, p.rows, cb, rb, oc, seg, tile_piece(L, 0, oc, seg));
-  }
+  store_transposed(L, 0, o.qt + t.cb * 128 * o.ld_qt + t.rb * 128, o.ld_qt, t.rows, t.cols);
 }
 
 // Arrays of a tile: 0 dg, 1 du, 2 v.
 template <bool CODES>
 __global__ __launch_bounds__(512, 4) void swiglu_bwd_tile_kernel(const SwigluBwdArgs p, int col_tiles) {
   __shared__ TileLds<3> L;
-  const int tid = threadIdx.x, g16 = tid & 15, j = tid >> 4;
-  const int64_t rb = blockIdx.x / col_tiles, cb = blockIdx.x - rb * col_tiles;
-  const int64_t col = cb * 128 + g16 * 8, blocks = (p.ffn + 127) >> 7;
+  const Tile t = tile_of(p.rows, p.ffn, col_tiles);
+  const int tid = threadIdx.x, lane16 = tid & 15;
+  const int64_t blocks = (p.ffn + 127) >> 7;
+  const LayoutsOut& o = p.dh;
   HalfIn gate[4], up[4];
   uint4 dy[4];
+  load_tile_halves<CODES>(t, p.h, p.ld_h, p.h_recip, p.hr_row, p.hr_kb, p.ffn, gate, up);
+  const uint16_t* const dy_corner = p.dy + t.rb * 128 * p.ld_dy + t.cb * 128;
+  const uint32_t dy_at = t.row * (uint32_t)p.ld_dy + t.col;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int64_t r = rb * 128 + 4 * j + k;
-    const bool in = col < p.ffn && r < p.rows;
-    gate[k] = load_half<CODES>(p.h, p.ld_h, p.h_recip, p.hr_row, p.hr_kb, p.ffn, r, col, 0, in);
-    up[k] = load_half<CODES>(p.h, p.ld_h, p.h_recip, p.hr_row, p.hr_kb, p.ffn, r, col, 1, in);
-    dy[k] = load_stream(p.dy + (in ? r * p.ld_dy + col : 0));
+    const bool in = t.row + k < t.rows && t.col < t.cols;
+    dy[k] = load_stream(dy_corner + (in ? dy_at + (uint32_t)k * (uint32_t)p.ld_dy : 0));
     if (!in) dy[k] = make_uint4(0, 0, 0, 0);
   }
   float g[4][8], u[4][8], d[4][8];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int64_t r = rb * 128 + 4 * j + k;
-    const bool in = col < p.ffn && r < p.rows;
     half_values<CODES>(gate[k], g[k]);
     half_values<CODES>(up[k], u[k]);
     unpack8(dy[k], d[k]);
 #pragma unroll
     for (int c = 0; c < 8; ++c) swiglu_grad(g[k][c], u[k][c], d[k][c]);
-    if (p.dh.y && in) {
-      uint16_t* const y = p.dh.y + r * p.dh.ld_y + col;
-      *(uint4*)y = pack8(g[k]);
-      *(uint4*)(y + p.ffn) = pack8(u[k]);
-    }
-    if (p.dh.q) {
-      uint8_t* const q = p.dh.q + r * p.dh.ld_q + col;
-      float* const recip = p.dh.recip + r * p.dh.rs_row + cb * p.dh.rs_kb;
-      put_codes8(g[k], q, recip, in);
-      put_codes8(u[k], q + p.ffn, recip + blocks * p.dh.rs_kb, in);
-    }
+    __builtin_amdgcn_sched_barrier(0);
   }
   tile_column_max(L, 0, g);
   tile_column_max(L, 1, u);
   tile_column_max(L, 2, d);
+  if (o.y) {
+    uint16_t* const corner = o.y + t.rb * 128 * o.ld_y + t.cb * 128;
+    uint32_t at = t.row * (uint32_t)o.ld_y + t.col;
+#pragma unroll
+    for (int k = 0; k < 4; ++k, at += (uint32_t)o.ld_y) {
+      if (t.row + k < t.rows && t.col < t.cols) {
+        *(uint4*)(corner + at) = pack8(g[k]);
+        *(uint4*)(corner + p.ffn + at) = pack8(u[k]);
+      }
+    }
+  }
+  if (o.q) {
+    // the blocks of 4 rows of both halves: block i = 4 half + row
+    float amax[8], scale[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      amax[k] = row16_max(absmax8(g[k]));
+      amax[4 + k] = row16_max(absmax8(u[k]));
+    }
+    const float recip = row16_scales(amax, scale);
+    uint8_t* const corner = o.q + t.rb * 128 * o.ld_q + t.cb * 128;
+    uint32_t at = t.row * (uint32_t)o.ld_q + t.col;
+#pragma unroll
+    for (int k = 0; k < 4; ++k, at += (uint32_t)o.ld_q) {
+      const bool in = t.row + k < t.rows && t.col < t.cols;
+      put_codes8(g[k], scale[k], corner + at, in);
+      put_codes8(u[k], scale[4 + k], corner + p.ffn + at, in);
+    }
+    if (lane16 < 8 && t.row + (lane16 & 3) < t.rows)
+      o.recip[(t.rb * 128 + t.row + (lane16 & 3)) * o.rs_row + ((lane16 >> 2) * blocks + t.cb) * o.rs_kb] = recip;
+  }
   __syncthreads();
   if (tid < 384) {
     const int a = tid >> 7, c = tid & 127;
     const float recip = recip_of_scale(tile_column_scale(L, a, c));
-    if (cb * 128 + c < p.ffn) {
-      if (a < 2 && p.dh.qt) p.dh.recip_t[(a * p.ffn + cb * 128 + c) * p.dh.rst_row + rb * p.dh.rst_kb] = recip;
-      if (a == 2 && p.act_qt) p.act_recip_t[(cb * 128 + c) * p.art_row + rb * p.art_kb] = recip;
+    if (c < t.cols) {
+      if (a < 2 && o.qt) o.recip_t[(a * p.ffn + t.cb * 128 + c) * o.rst_row + t.rb * o.rst_kb] = recip;
+      if (a == 2 && p.act_qt) p.act_recip_t[(t.cb * 128 + c) * p.art_row + t.rb * p.art_kb] = recip;
     }
   }
   __syncthreads();
   tile_codes(L, 0, g);
+  __builtin_amdgcn_sched_barrier(0);
   tile_codes(L, 1, u);
+  __builtin_amdgcn_sched_barrier(0);
   tile_codes(L, 2, d);
   __syncthreads();
-#pragma unroll
-  for (int a = 0; a < 3; ++a) {
-    if (a < 2 ? !p.dh.qt : !p.act_qt) continue;
-    uint8_t* const qt = a < 2 ? p.dh.qt + a * p.ffn * p.dh.ld_qt : p.act_qt;
-    const int64_t ld = a < 2 ? p.dh.ld_qt : p.ld_act_qt;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int id = tid + 512 * i, oc = id >> 3, seg = id & 7;
-      store_transposed(qt, ld, p.ffn, p.rows, cb, rb, oc, seg, tile_piece(L, a, oc, seg));
-    }
+  if (o.qt) {
+    uint8_t* const corner = o.qt + t.cb * 128 * o.ld_qt + t.rb * 128;
+    store_transposed(L, 0, corner, o.ld_qt, t.rows, t.cols);
+    store_transposed(L, 1, corner + p.ffn * o.ld_qt, o.ld_qt, t.rows, t.cols);
   }
+  if (p.act_qt)
+    store_transposed(L, 2, p.act_qt + t.cb * 128 * p.ld_act_qt + t.rb * 128, p.ld_act_qt, t.rows, t.cols);
 }
 
-// Four pieces a wave once that still leaves several workgroups per compute unit.
+// Two pieces a wave once that still leaves several workgroups per compute unit
+// (forward, 33280 rows of 2 x 5120 with a checkpoint: 254 us with one, 233 with
+// two, 245 with four, 251 with eight).
 constexpr int64_t kManyPieces = 8192;
+constexpr int kPieces = 2;
 
 hipError_t launch_swiglu_fwd(const SwigluFwdArgs& p, hipStream_t stream) {
   if (p.out.qt) {
@@ -297,9 +380,9 @@ hipError_t launch_swiglu_fwd(const SwigluFwdArgs& p, hipStream_t stream) {
   }
   const int64_t pieces = (p.ffn + 511) / 512, items = p.rows * pieces;
   if (items >= kManyPieces)
-    hipLaunchKernelGGL(swiglu_fwd_rows_kernel<4>, dim3((unsigned)((items + 15) / 16)), dim3(256), 0, stream, p, pieces);
+    hipLaunchKernelGGL(swiglu_fwd_rows_kernel<kPieces>, dim3((unsigned)((items + 4 * kPieces - 1) / (4 * kPieces))), dim3(256), 0, stream, p, (uint32_t)pieces);
   else
-    hipLaunchKernelGGL(swiglu_fwd_rows_kernel<1>, dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, p, pieces);
+    hipLaunchKernelGGL(swiglu_fwd_rows_kernel<1>, dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, p, (uint32_t)pieces);
   return hipGetLastError();
 }
 
@@ -314,13 +397,13 @@ hipError_t launch_swiglu_bwd(const SwigluBwdArgs& p, hipStream_t stream) {
   }
   const int64_t pieces = (p.ffn + 511) / 512, items = p.rows * pieces;
   const bool many = items >= kManyPieces;
-  const dim3 grid((unsigned)(many ? (items + 15) / 16 : (items + 3) / 4));
-#define FP8BW_K(P, C) hipLaunchKernelGGL((swiglu_bwd_rows_kernel<P, C>), grid, dim3(256), 0, stream, p, pieces)
+  const dim3 grid((unsigned)(many ? (items + 4 * kPieces - 1) / (4 * kPieces) : (items + 3) / 4));
+#define FP8BW_K(P, C) hipLaunchKernelGGL((swiglu_bwd_rows_kernel<P, C>), grid, dim3(256), 0, stream, p, (uint32_t)pieces)
   if (p.h_recip) {
-    if (many) FP8BW_K(4, true);
+    if (many) FP8BW_K(kPieces, true);
     else FP8BW_K(1, true);
   } else {
-    if (many) FP8BW_K(4, false);
+    if (many) FP8BW_K(kPieces, false);
     else FP8BW_K(1, false);
   }
 #undef FP8BW_K

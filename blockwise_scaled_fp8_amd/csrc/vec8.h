@@ -19,10 +19,10 @@ __device__ __forceinline__ uint4 load_stream(const uint16_t* p) {
 // Sum over the 16 lanes of a DPP row, then over the wavefront; every lane
 // receives the same value.
 __device__ __forceinline__ float row16_sum(float v) {
-  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false));
-  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x4E, 0xF, 0xF, false));
-  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x141, 0xF, 0xF, false));
-  v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x140, 0xF, 0xF, false));
+  v += dpp_move<0xB1>(v);
+  v += dpp_move<0x4E>(v);
+  v += dpp_move<0x141>(v);
+  v += dpp_move<0x140>(v);
   return v;
 }
 __device__ __forceinline__ float wave_sum(float v) {
@@ -53,10 +53,49 @@ __device__ __forceinline__ float absmax8(const float (&f)[8]) {
   return m;
 }
 
+// Four E4M3 codes of values scaled by their own block's scale.  These need no
+// clamp: |f| <= amax and s = 448 / max(amax, 1e-12) rounded give |f s| <= 448
+// (1 + 2^-23), and what lies between 448 and 464 rounds to 448.
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+}
 // Eight E4M3 codes of f * s.
 __device__ __forceinline__ uint2 codes8(const float (&f)[8], float s) {
-  return make_uint2(cvt4_e4m3(f[0] * s, f[1] * s, f[2] * s, f[3] * s),
-                    cvt4_e4m3(f[4] * s, f[5] * s, f[6] * s, f[7] * s));
+  return make_uint2(codes4(f[0] * s, f[1] * s, f[2] * s, f[3] * s),
+                    codes4(f[4] * s, f[5] * s, f[6] * s, f[7] * s));
+}
+
+// Lane I of each DPP row, to all its lanes (row_newbcast).
+template <int I>
+__device__ __forceinline__ float row16_lane(float v) {
+  return dpp_move<0x150 + I>(v);
+}
+
+// Scales of N <= 16 blocks whose amaxes every lane of a DPP row holds.  Lane i
+// divides for block i alone, 448 / amax and its reciprocal being the most
+// expensive part of a block's codes (two IEEE divisions, 8 values a lane), and
+// its scale is broadcast.  Returns, in lane i < N, block i's reciprocal.
+template <int N, int I = 0>
+__device__ __forceinline__ void row16_spread(float s, float (&scale)[N]) {
+  if constexpr (I < N) {
+    scale[I] = row16_lane<I>(s);
+    row16_spread<N, I + 1>(s, scale);
+  }
+}
+// amax[l] for a lane's own l < N, by selects (a loop over i would be turned into
+// an array in memory indexed by l).
+template <int N, int I = 1>
+__device__ __forceinline__ float row16_pick(const float (&amax)[N], int l, float m) {
+  if constexpr (I < N) return row16_pick<N, I + 1>(amax, l, l == I ? +amax[I] : m);
+  else return m;
+}
+template <int N>
+__device__ __forceinline__ float row16_scales(const float (&amax)[N], float (&scale)[N]) {
+  static_assert(N <= 16, "one lane a block");
+  const float s = scale_from_amax(row16_pick(amax, threadIdx.x & 15, amax[0]));
+  row16_spread(s, scale);
+  return recip_of_scale(s);
 }
 
 // Eight E4M3 codes' values times r.
@@ -70,6 +109,28 @@ __device__ __forceinline__ void values8(const uint2& q, float r, float (&f)[8]) 
     f[4 * h + 2] = hi.x * r; f[4 * h + 3] = hi.y * r;
   }
 }
+
+// P consecutive pieces of 512 columns of a wave, rows one after the other; `pieces`
+// to a row, fewer than 2^30 in all.  One division, the rest by counting: P 64-bit
+// divisions were most of a row kernel's scalar instructions.
+template <int P>
+struct Pieces {
+  int row[P];
+  int col[P];   // first column
+  __device__ __forceinline__ Pieces(uint32_t workgroup, uint32_t pieces) {
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t first = (workgroup * 4 + wave) * P;
+    uint32_t r = first / pieces, c = first - r * pieces;
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      row[k] = (int)r;
+      col[k] = (int)c * 512;
+      const bool next = ++c == pieces;
+      r += next ? 1u : 0u;
+      c = next ? 0u : c;
+    }
+  }
+};
 
 // ---------------------------------------------------------------------------
 // Transposed codes of NA 128 x 128 tiles of fp32 values held by a workgroup of
@@ -90,17 +151,31 @@ struct TileLds {
   __attribute__((aligned(16))) uint32_t tile[NA][128 * 32];
 };
 
-// The column maxima of array a, into LDS.  Before the first barrier.
+// The column maxima of array a, into LDS.  Before the first barrier.  The wave's
+// four row quads are joined two columns at a time: exchanging halves (then 16-lane
+// rows) of two registers leaves in each lane pair one column's two values, so one
+// exchange and one maximum serve both columns, and every lane writes.
+__device__ __forceinline__ uint32_t max_halves(uint32_t x, uint32_t y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+  return max(r[0], r[1]);   // x's maximum in lanes 0 .. 31, y's in 32 .. 63
+}
+__device__ __forceinline__ uint32_t max_rows(uint32_t x, uint32_t y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+  return max(r[0], r[1]);   // rows 0, 2: x's, rows 1, 3: y's
+}
 template <int NA>
 __device__ __forceinline__ void tile_column_max(TileLds<NA>& L, int a, const float (&v)[4][8]) {
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = tid & 15;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  uint32_t m[8];   // as integers: magnitudes in the same order
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    float m = fmaxf(fmaxf(fabsf(v[0][c]), fabsf(v[1][c])), fmaxf(fabsf(v[2][c]), fabsf(v[3][c])));
-    m = fmaxf(m, __shfl_xor(m, 16));
-    m = fmaxf(m, __shfl_xor(m, 32));
-    if (lane < 16) L.red[wave][a][8 * g + c] = m;
-  }
+  for (int c = 0; c < 8; ++c)
+    m[c] = __float_as_uint(fmaxf(fmaxf(fabsf(v[0][c]), fabsf(v[1][c])), fmaxf(fabsf(v[2][c]), fabsf(v[3][c]))));
+  // 16-lane rows 0 .. 3 end with columns 0, 2, 1, 3 (and 4 further)
+  const uint32_t lo = max_rows(max_halves(m[0], m[1]), max_halves(m[2], m[3]));
+  const uint32_t hi = max_rows(max_halves(m[4], m[5]), max_halves(m[6], m[7]));
+  float* const red = &L.red[wave][a][8 * (lane & 15) + ((lane >> 3) & 2) + (lane >> 5)];
+  red[0] = __uint_as_float(lo);
+  red[4] = __uint_as_float(hi);
 }
 
 // After a barrier: the scale of column c of array a, for one thread of each.
@@ -122,14 +197,25 @@ __device__ __forceinline__ void tile_codes(TileLds<NA>& L, int a, const float (&
   for (int c = 0; c < 8; ++c) {
     const float s = L.scale[a][8 * g + c];
     L.tile[a][(8 * g + c) * 32 + (j ^ (4 * (g & 7)))] =
-        cvt4_e4m3(v[0][c] * s, v[1][c] * s, v[2][c] * s, v[3][c] * s);
+        codes4(v[0][c] * s, v[1][c] * s, v[2][c] * s, v[3][c] * s);
   }
 }
 
-// After the last: 16 codes of output row (tile column) oc, rows 16 seg .. + 15.
+// After the last: array a's tile of `rows` x `cols` existing values, to the
+// transposed matrix whose rows 0 .. cols - 1 start at `corner` (rows % 16 == 0).
+// Nothing reads these codes before the backward or its weight gradient: they pass
+// the caches by.
 template <int NA>
-__device__ __forceinline__ uint4 tile_piece(const TileLds<NA>& L, int a, int oc, int seg) {
-  return *(const uint4*)&L.tile[a][oc * 32 + ((4 * seg) ^ (4 * ((oc >> 3) & 7)))];
+__device__ __forceinline__ void store_transposed(const TileLds<NA>& L, int a, uint8_t* corner, int64_t ld, int rows,
+                                                 int cols) {
+  const int oc = threadIdx.x >> 3, seg = threadIdx.x & 7;
+  uint32_t at = oc * (uint32_t)ld + 16 * seg;
+#pragma unroll
+  for (int i = 0; i < 2; ++i, at += 64 * (uint32_t)ld) {
+    const int c = oc + 64 * i;
+    const u32x4 w = *(const u32x4*)&L.tile[a][c * 32 + ((4 * seg) ^ (4 * ((c >> 3) & 7)))];
+    if (c < cols && 16 * seg < rows) __builtin_nontemporal_store(w, (u32x4*)(corner + at));
+  }
 }
 
 }  // namespace fp8bw

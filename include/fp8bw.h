@@ -659,7 +659,8 @@ int fp8bw_moe_combine_bwd(const void* dout, int64_t ld_dout, const void* y, int6
  *        operand of its weight gradient.
  *
  * Both: ffn % 16 == 0, ffn <= 2^20, rows < 2^27, fewer than 2^26 pieces of 512 columns
- * and 2^23 tiles of 128 x 128 of v.  Transposed codes need rows % 16 == 0.
+ * and 2^23 tiles of 128 x 128 of v.  Transposed codes need rows % 16 == 0, leading
+ * dimensions of bf16 and row strides of h_recip below 2^22, and of codes below 2^24.
  */
 int fp8bw_swiglu_fwd(const void* h, int64_t ld_h, int64_t rows, int64_t ffn, const fp8bw_layouts* out,
                      void* hq, int64_t ld_hq, float* h_recip, int64_t hr_row, int64_t hr_kb,
