@@ -54,7 +54,11 @@ from .ops import (  # noqa: F401
 from .torch_ops import (  # noqa: E402,F401  (registers torch.ops.fp8bw.*)
     AdamW,
     Float8BlockwiseLinear,
+    Float8BlockwiseMoE,
     RMSNorm,
     RMSNormLinear,
     linear_cross_entropy,
+    moe_dispatch,
+    moe_join,
+    swiglu,
 )

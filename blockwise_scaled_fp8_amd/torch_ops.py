@@ -25,7 +25,11 @@ add bench script", Summary).  Here that is:
   * around it, what the rest of a training step needs: ``RMSNorm`` (with the
     residual's addition), ``RMSNormLinear`` (the norm writes the linear's
     operand codes itself), ``linear_cross_entropy`` (a head and its loss
-    without the logits) and ``AdamW`` (fp32 or 8-bit states).
+    without the logits) and ``AdamW`` (fp32 or 8-bit states);
+  * ``Float8BlockwiseMoE``, the experts of a mixture-of-experts layer on the
+    grouped GEMM, trained from E4M3 operands and 8-bit checkpoints, and its
+    parts with gradients of their own: ``moe_dispatch``, ``moe_join``,
+    ``swiglu``.
 
 Shapes follow the ABI's rules: in_features and out_features multiples of
 128 (they are contraction axes in fwd and dgrad) and a token count that is a
@@ -243,8 +247,10 @@ def _empty(like, dtype=None):
 def _aligned(t):
     """t where it is laid out as the kernels read it (16-byte aligned rows of
     unit column stride), else a copy that is."""
-    if t is None or t.numel() == 0:
+    if t is None:
         return t
+    if t.numel() == 0:
+        return t if t.stride(-1) == 1 else t.new_empty(t.shape)   # an expanded gradient of nothing
     rows_fit = t.dim() < 2 or t.shape[0] == 1 or (t.stride(0) >= t.shape[1] and t.stride(0) % 8 == 0)
     if t.data_ptr() % 16 == 0 and t.stride(-1) == 1 and rows_fit:
         return t
@@ -503,6 +509,295 @@ def linear_cross_entropy(h, w, target, ignore_index=-100, reduction="mean"):
     if reduction == "sum":
         return loss.sum()
     return loss.sum() / (flat != ignore_index).sum()
+
+
+# ---------------------------------------------------------------------------
+# Mixture of experts: rows to experts and back, the gated activation, and the
+# whole layer on the grouped GEMM.
+
+@torch.library.custom_op("fp8bw::moe_sort", mutates_args=())
+def moe_sort(expert: torch.Tensor, experts: int,
+             align: int) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(row, source, group_end) of ops.moe_sort."""
+    return tuple(ops.moe_sort(expert.contiguous(), experts, align))
+
+
+@moe_sort.register_fake
+def _moe_sort_fake(expert, experts, align):
+    rows = ops.moe_rows(expert.shape[0], expert.shape[1], experts, align)
+    return tuple(expert.new_empty(shape, dtype=torch.int32) for shape in (expert.shape, (rows,), (experts,)))
+
+
+@torch.library.custom_op("fp8bw::moe_gather", mutates_args=())
+def moe_gather(x: torch.Tensor, row: torch.Tensor, source: torch.Tensor,
+               group_end: torch.Tensor) -> torch.Tensor:
+    """bf16 rows of ops.moe_gather."""
+    return ops.moe_gather(_aligned(x), ops.MoeTable(row, source, group_end)).y
+
+
+@moe_gather.register_fake
+def _moe_gather_fake(x, row, source, group_end):
+    _check_2d_bf16(x)
+    return x.new_empty((source.shape[0], x.shape[1]))
+
+
+@torch.library.custom_op("fp8bw::moe_combine", mutates_args=())
+def moe_combine(y: torch.Tensor, weight: Optional[torch.Tensor], row: torch.Tensor, source: torch.Tensor,
+                group_end: torch.Tensor) -> torch.Tensor:
+    """ops.moe_combine."""
+    return ops.moe_combine(_aligned(y), ops.MoeTable(row, source, group_end),
+                           None if weight is None else weight.contiguous())
+
+
+@moe_combine.register_fake
+def _moe_combine_fake(y, weight, row, source, group_end):
+    _check_2d_bf16(y)
+    return y.new_empty((row.shape[0], y.shape[1]))
+
+
+@torch.library.custom_op("fp8bw::moe_combine_bwd", mutates_args=())
+def moe_combine_bwd(dout: torch.Tensor, y: torch.Tensor, weight: torch.Tensor, row: torch.Tensor,
+                    source: torch.Tensor, group_end: torch.Tensor, need_dy: bool,
+                    need_dweight: bool) -> tuple[torch.Tensor, torch.Tensor]:
+    """(dy, dweight) of ops.moe_combine_bwd; one not asked for comes back empty."""
+    o, dw = ops.moe_combine_bwd(_aligned(dout), _aligned(y) if need_dweight else None,
+                                ops.MoeTable(row, source, group_end), weight.contiguous(), dy=need_dy,
+                                need_dweight=need_dweight)
+    return (o.y if need_dy else _empty(dout)), (dw if need_dweight else _empty(weight))
+
+
+@moe_combine_bwd.register_fake
+def _moe_combine_bwd_fake(dout, y, weight, row, source, group_end, need_dy, need_dweight):
+    return (dout.new_empty((source.shape[0], dout.shape[1])) if need_dy else _empty(dout),
+            weight.new_empty(weight.shape) if need_dweight else _empty(weight))
+
+
+class _MoeDispatch(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, row, source, group_end):
+        ctx.save_for_backward(row, source, group_end)
+        return torch.ops.fp8bw.moe_gather(x, row, source, group_end)
+
+    @staticmethod
+    def backward(ctx, dy):
+        return torch.ops.fp8bw.moe_combine(dy, None, *ctx.saved_tensors), None, None, None
+
+
+class _MoeJoin(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, weight, row, source, group_end):
+        ctx.save_for_backward(y if weight is not None and ctx.needs_input_grad[1] else None, weight, row, source,
+                              group_end)
+        return torch.ops.fp8bw.moe_combine(y, weight, row, source, group_end)
+
+    @staticmethod
+    def backward(ctx, dout):
+        y, weight, *table = ctx.saved_tensors
+        need = ctx.needs_input_grad[:2]
+        if weight is None:
+            return torch.ops.fp8bw.moe_gather(dout, *table), None, None, None, None
+        dy, dweight = torch.ops.fp8bw.moe_combine_bwd(dout, dout if y is None else y, weight, *table, *need)
+        return (dy if need[0] else None), (dweight if need[1] else None), None, None, None
+
+
+def moe_dispatch(x, table):
+    """Rows of x bf16 [..., features] in the order of a moe_sort table over its
+    tokens, bf16 [rows, features], zeros in rows without a slot; differentiable
+    in x."""
+    return _MoeDispatch.apply(x.reshape(-1, x.shape[-1]), *table)
+
+
+def moe_join(y, table, weight=None):
+    """bf16 [tokens, features]: every token's rows of y, times weight (fp32 or
+    bf16, as many as the table has slots) if given, summed; differentiable in y
+    and weight."""
+    if weight is not None:
+        weight = weight.reshape(table.row.shape)
+    return _MoeJoin.apply(y, weight, *table)
+
+
+@torch.library.custom_op("fp8bw::swiglu_fwd", mutates_args=())
+def swiglu_fwd(h: torch.Tensor, save: bool) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(y, hq, h_recip) of ops.swiglu_fwd; the checkpoint empty unless save."""
+    o = ops.swiglu_fwd(_aligned(h), save=save)
+    return o.y, (o.hq if save else _empty(h, torch.uint8)), (o.h_recip if save else _empty(h, torch.float32))
+
+
+@swiglu_fwd.register_fake
+def _swiglu_fwd_fake(h, save):
+    _check_2d_bf16(h)
+    rows, ffn = h.shape[0], h.shape[1] // 2
+    if not save:
+        return h.new_empty((rows, ffn)), _empty(h, torch.uint8), _empty(h, torch.float32)
+    return (h.new_empty((rows, ffn)), h.new_empty(h.shape, dtype=torch.uint8),
+            h.new_empty((2 * ((ffn + 127) // 128), rows), dtype=torch.float32).t())
+
+
+@torch.library.custom_op("fp8bw::swiglu_bwd", mutates_args=())
+def swiglu_bwd(dy: torch.Tensor, h: torch.Tensor, h_recip: Optional[torch.Tensor]) -> torch.Tensor:
+    """dh of ops.swiglu_bwd."""
+    return ops.swiglu_bwd(_aligned(dy), h if h_recip is not None else _aligned(h), h_recip).dh
+
+
+@swiglu_bwd.register_fake
+def _swiglu_bwd_fake(dy, h, h_recip):
+    return dy.new_empty((dy.shape[0], 2 * dy.shape[1]))
+
+
+class _Swiglu(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, h, checkpoint):
+        keep = checkpoint and ctx.needs_input_grad[0]
+        y, hq, h_recip = torch.ops.fp8bw.swiglu_fwd(h, keep)
+        ctx.save_for_backward(*((hq, h_recip) if keep else (h, None)))
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        return torch.ops.fp8bw.swiglu_bwd(dy, *ctx.saved_tensors), None
+
+
+def swiglu(h, checkpoint=False):
+    """silu(gate) * up of h = [gate | up] bf16 [..., 2 ffn] -> [..., ffn].
+    checkpoint: the backward keeps h as E4M3 codes with a scale per 1x128 block
+    of each half, half its bytes, and computes with their values."""
+    y = _Swiglu.apply(h.reshape(-1, h.shape[-1]), checkpoint)
+    return y.reshape(*h.shape[:-1], h.shape[-1] // 2)
+
+
+@torch.library.custom_op("fp8bw::moe_fwd", mutates_args=())
+def moe_fwd(x: torch.Tensor, expert: torch.Tensor, weight: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor,
+            align: int, keep_x: bool, keep_h: bool, keep_y: bool
+            ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor,
+                       torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(out, row, source, group_end, x_qt, x_recip_t, hq, h_recip, y): the experts'
+    MLPs on sorted rows, out[t] = sum_j weight[t, j] W2_e swiglu(W13_e x[t]); what
+    the backward needs and is not kept comes back empty."""
+    table = ops.moe_sort(expert.contiguous(), w13.shape[0], align)
+    rows = ops.moe_gather(_aligned(x), table, y=False, q=True, qt=keep_x)
+    h = ops.fp8_scaled_grouped_gemm_blockwise(rows.q, rows.recip, *ops.fp8_blockwise_quant_grouped(w13),
+                                              table.group_end)
+    a = ops.swiglu_fwd(h, y=False, q=True, save=keep_h)
+    y = ops.fp8_scaled_grouped_gemm_blockwise(a.q, a.recip, *ops.fp8_blockwise_quant_grouped(w2), table.group_end)
+    out = ops.moe_combine(y, table, weight.contiguous())
+    codes, scales = _empty(x, torch.uint8), _empty(x, torch.float32)
+    return (out, *table, rows.qt if keep_x else codes, rows.recip_t if keep_x else scales,
+            a.hq if keep_h else codes.clone(), a.h_recip if keep_h else scales.clone(), y if keep_y else _empty(x))
+
+
+@moe_fwd.register_fake
+def _moe_fwd_fake(x, expert, weight, w13, w2, align, keep_x, keep_h, keep_y):
+    _check_2d_bf16(x)
+    (E, _, H), F = w13.shape, w2.shape[2]
+    R = ops.moe_rows(expert.shape[0], expert.shape[1], E, align)
+
+    def codes(keep, rows, cols, blocks):
+        if not keep:
+            return _empty(x, torch.uint8), _empty(x, torch.float32)
+        return (x.new_empty((rows, cols), dtype=torch.uint8),
+                x.new_empty((blocks, rows), dtype=torch.float32).t())
+    return (x.new_empty(x.shape), *_moe_sort_fake(expert, E, align), *codes(keep_x, H, R, (R + 127) // 128),
+            *codes(keep_h, R, 2 * F, 2 * F // 128), x.new_empty((R, H)) if keep_y else _empty(x))
+
+
+@torch.library.custom_op("fp8bw::moe_bwd", mutates_args=())
+def moe_bwd(dout: torch.Tensor, row: torch.Tensor, source: torch.Tensor, group_end: torch.Tensor,
+            x_qt: torch.Tensor, x_recip_t: torch.Tensor, hq: torch.Tensor, h_recip: torch.Tensor, y: torch.Tensor,
+            weight: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, need_dx: bool, need_dweight: bool,
+            need_dw13: bool, need_dw2: bool) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dx, dweight, dW13, dW2) of moe_fwd; one not asked for comes back empty.
+    Every product is an FP8 one: the joined gradient and the activation's are
+    quantized into both layouts by the kernels that make them."""
+    table = ops.MoeTable(row, source, group_end)
+    through = need_dx or need_dw13
+    dy, dweight = ops.moe_combine_bwd(_aligned(dout), y if need_dweight else None, table, weight.contiguous(), dy=False,
+                                      q=through or need_dw2, qt=need_dw2, need_dweight=need_dweight)
+    dx = dw13 = dw2 = None
+    if through or need_dw2:
+        da = ops.fp8_scaled_grouped_gemm_blockwise(dy.q, dy.recip, *ops.fp8_blockwise_quant_grouped(w2, transpose=True),
+                                                   group_end)
+        g = ops.swiglu_bwd(da, hq, h_recip, dh=False, q=need_dx, qt=need_dw13, act_qt=need_dw2)
+    if need_dw2:
+        dw2 = ops.fp8_scaled_grouped_gemm_blockwise_wgrad(dy.qt, dy.recip_t, g.act_qt, g.act_recip_t, group_end)
+    if need_dw13:
+        dw13 = ops.fp8_scaled_grouped_gemm_blockwise_wgrad(g.qt, g.recip_t, x_qt, x_recip_t, group_end)
+    if need_dx:
+        dx = ops.moe_combine(ops.fp8_scaled_grouped_gemm_blockwise(
+            g.q, g.recip, *ops.fp8_blockwise_quant_grouped(w13, transpose=True), group_end), table)
+    return (_empty(dout) if dx is None else dx, _empty(weight) if dweight is None else dweight,
+            _empty(w13) if dw13 is None else dw13, _empty(w2) if dw2 is None else dw2)
+
+
+@moe_bwd.register_fake
+def _moe_bwd_fake(dout, row, source, group_end, x_qt, x_recip_t, hq, h_recip, y, weight, w13, w2, need_dx,
+                  need_dweight, need_dw13, need_dw2):
+    return tuple(like.new_empty(like.shape) if need else _empty(like) for like, need in (
+        (dout, need_dx), (weight, need_dweight), (w13, need_dw13), (w2, need_dw2)))
+
+
+class _MoE(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, expert, weight, w13, w2):
+        need_x, _, need_weight, need_w13, need_w2 = ctx.needs_input_grad
+        out, *kept = torch.ops.fp8bw.moe_fwd(x, expert, weight, w13, w2, 128, need_w13, need_x or need_w13 or need_w2,
+                                             need_weight)
+        ctx.save_for_backward(*kept, weight, w13, w2)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        n = ctx.needs_input_grad
+        need = (n[0], *n[2:])
+        grads = torch.ops.fp8bw.moe_bwd(dout, *ctx.saved_tensors, *need)
+        dx, dweight, dw13, dw2 = (g if wanted else None for g, wanted in zip(grads, need))
+        return dx, None, dweight, dw13, dw2
+
+
+class Float8BlockwiseMoE(torch.nn.Module):
+    """The experts of a mixture-of-experts layer: expert e maps x to
+    ``W2_e swiglu(W13_e x)`` with every product in the FP8 blockwise recipe, and
+    a token's output is the weighted sum over the experts that a router chose.
+
+    ``m(x, expert, weight)``: x bf16 [..., hidden]; expert int32 or int64 [...,
+    topk], a number outside [0, experts) being no expert; weight fp32 or bf16
+    [..., topk].  Any number of tokens, training included: each expert's rows
+    are padded to blocks of 128 on the device.  Weights are bf16 parameters w13
+    [experts, 2 ffn, hidden] (gate, then up) and w2 [experts, hidden, ffn].
+
+    The forward keeps the sorted rows' transposed codes, the experts' first
+    products as 8-bit checkpoints and, for the router's gradient, their outputs
+    in bf16."""
+
+    def __init__(self, hidden, ffn, experts, device=None):
+        super().__init__()
+        if hidden % 128 or ffn % 128:
+            raise ValueError("hidden and ffn must be multiples of 128")
+        if not 1 <= experts <= 1024:
+            raise ValueError("experts must be in [1, 1024]")
+        self.hidden, self.ffn, self.experts = hidden, ffn, experts
+        self.w13 = torch.nn.Parameter(torch.empty(experts, 2 * ffn, hidden, device=device, dtype=torch.bfloat16))
+        self.w2 = torch.nn.Parameter(torch.empty(experts, hidden, ffn, device=device, dtype=torch.bfloat16))
+        self.reset_parameters()
+
+    def reset_parameters(self):
+        with torch.no_grad():
+            for w in (self.w13, self.w2):
+                w.uniform_(-1.0 / math.sqrt(w.shape[2]), 1.0 / math.sqrt(w.shape[2]))
+
+    def forward(self, x, expert, weight):
+        if expert.shape != weight.shape or expert.shape[:-1] != x.shape[:-1]:
+            raise ValueError("expert and weight must be [..., topk] over x's leading dimensions")
+        topk = expert.shape[-1]
+        x2 = x.reshape(-1, self.hidden)
+        e2, s2 = expert.reshape(-1, topk), weight.reshape(-1, topk)
+        if torch.is_grad_enabled() and any(t.requires_grad for t in (x2, s2, self.w13, self.w2)):
+            out = _MoE.apply(x2, e2, s2, self.w13, self.w2)
+        else:
+            out = torch.ops.fp8bw.moe_fwd(x2, e2, s2, self.w13, self.w2, 1, False, False, False)[0]
+        return out.reshape(x.shape)
+
+    def extra_repr(self):
+        return f"{self.experts} experts, {self.hidden}, ffn={self.ffn}"
 
 
 # ---------------------------------------------------------------------------

@@ -1,9 +1,10 @@
 """Trains a small language model with every operator of the package: blocks of
 RMSNormLinear (the norm adds the residual and writes the FP8 operand), a
-nonlinearity and a Float8BlockwiseLinear, a final RMSNorm, the vocabulary cross
-entropy without logits, and AdamW with 8-bit states.
+nonlinearity and a Float8BlockwiseLinear (or, with --experts, of RMSNorm, a
+router and Float8BlockwiseMoE), a final RMSNorm, the vocabulary cross entropy
+without logits, and AdamW with 8-bit states.
 
-    python examples/train_small_lm.py [--steps 60] [--bits 8]
+    python examples/train_small_lm.py [--steps 60] [--bits 8] [--experts 0]
 
 The text is synthetic: token t + 1 is a fixed function of token t, nine times
 out of ten, so the loss falls from log(vocabulary) towards that rule's entropy.
@@ -31,11 +32,28 @@ class Block(torch.nn.Module):
         return self.down(torch.nn.functional.silu(y)), residual
 
 
+class ExpertBlock(torch.nn.Module):
+    """Each token's two likeliest experts out of a router's softmax."""
+
+    def __init__(self, width, inner, experts, device):
+        super().__init__()
+        self.norm = fp8.RMSNorm(width, device=device)
+        self.router = torch.nn.Linear(width, experts, bias=False, device=device)
+        self.experts = fp8.Float8BlockwiseMoE(width, inner, experts, device=device)
+
+    def forward(self, x, residual):
+        y, residual = self.norm(x, residual)
+        top = torch.topk(torch.softmax(self.router(y.float()), -1), 2)
+        return self.experts(y, top.indices, top.values / top.values.sum(-1, keepdim=True)), residual
+
+
 class SmallLM(torch.nn.Module):
-    def __init__(self, vocab, width, inner, blocks, device):
+    def __init__(self, vocab, width, inner, blocks, device, experts=0):
         super().__init__()
         self.embed = torch.nn.Parameter(torch.randn(vocab, width, device=device).bfloat16())
-        self.blocks = torch.nn.ModuleList(Block(width, inner, device) for _ in range(blocks))
+        self.blocks = torch.nn.ModuleList(
+            ExpertBlock(width, inner, experts, device) if experts else Block(width, inner, device)
+            for _ in range(blocks))
         self.norm = fp8.RMSNorm(width, device=device)
         self.head = torch.nn.Parameter((torch.randn(vocab, width, device=device) / width ** 0.5).bfloat16())
 
@@ -59,12 +77,13 @@ def batch(vocab, tokens, generator, device):
     return t, target
 
 
-def train(steps=60, bits=8, vocab=1000, width=256, inner=512, blocks=2, tokens=1024, lr=3e-3, say=print):
+def train(steps=60, bits=8, vocab=1000, width=256, inner=512, blocks=2, tokens=1024, lr=3e-3, say=print,
+          experts=0):
     device = torch.device("cuda", 0)
     torch.manual_seed(0)
     generator = torch.Generator(device=device)
     generator.manual_seed(1)
-    model = SmallLM(vocab, width, inner, blocks, device)
+    model = SmallLM(vocab, width, inner, blocks, device, experts)
     opt = fp8.AdamW(model.parameters(), lr=lr, weight_decay=0.01, state_bits=bits)
     losses = []
     for step in range(steps):
@@ -84,5 +103,6 @@ if __name__ == "__main__":
     parser = argparse.ArgumentParser()
     parser.add_argument("--steps", type=int, default=60)
     parser.add_argument("--bits", type=int, default=8, choices=(8, 32))
+    parser.add_argument("--experts", type=int, default=0)
     args = parser.parse_args()
-    train(args.steps, args.bits)
+    train(args.steps, args.bits, experts=args.experts)
