@@ -86,8 +86,9 @@ struct GemmArgs {
   // Weight gradients of a grouped GEMM (KGROUP kernels): `groups` row-major
   // [M, N] outputs out_s_group elements apart, group g contracting the K
   // blocks [group_end[g-1] / 128, group_end[g] / 128); `groups` stays 0 in the
-  // kernels that split rows.  A persistent launch's tiles number tail_base.
+  // kernels that split rows.
   int64_t out_s_group;
+  int kgroups;
 };
 
 // The K blocks of group g of a weight gradient, clamped so that no table can
@@ -890,10 +891,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_v2_kernel(const GemmArgs 
     // One group's tiles after the other, each group dealt over all XCDs: with
     // a run of groups per XCD, the XCD of the longest ones finished last.
     const int tiles = p.tiles_m * p.tiles_n;
-    const int id = blockIdx.x + rnd * gridDim.x;
-    if (PERSIST && id >= p.tail_base) return;   // all tiles
-    kgroup = id / tiles;
-    wg = xcd_remap(id - kgroup * tiles, tiles);
+    kgroup = blockIdx.x / tiles;
+    wg = xcd_remap(blockIdx.x - kgroup * tiles, tiles);
   } else if (p.groups > 0) {
     if (p.group_part == 1 && !grouped_split_pays(p)) p.group_part = 0;
     const int T = grouped_tile_count<BM>(p);
@@ -1827,6 +1826,276 @@ hipError_t launch_grouped_gemm(const GemmProblem& p, int groups, const int* grou
 // ---------------------------------------------------------------------------
 // Weight gradients of a grouped GEMM: one [M, N] product per group over the
 // group's K blocks (GemmArgs::out_s_group), all in one launch.
+//
+// wgrad_stream_kernel: one workgroup per CU runs its share of all groups' 256x256
+// tiles as one stream of K blocks.  A group's contraction is short (a training
+// batch of 33280 tokens over 16 experts: 17 K blocks), so what a tile costs beside
+// its K blocks decides: run tile by tile (gemm_v2_kernel, one workgroup each, or
+// its persistent form) that was 6.5 to 7 us, as much as three K blocks: the first
+// loads' latency, a last stage loaded for nothing, and the epilogue.  Here the
+// next tile's first block is on its way while a tile ends: the epilogue leaves
+// through the 64 KB of one stage, in two halves, and the other receives it.
+//
+// Order: groups by falling length, so that the tiles every cus-th of which a
+// workgroup takes grow shorter towards its end, and empty groups' zeros come
+// last; within a group as everywhere (tile_to_mn).  Roles as in a persistent
+// launch: waves 0 and 1 issue the direct loads and wait for them, the others
+// store, and nothing waits for stores.
+constexpr int kStreamGroups = 1024;
+
+struct WgradTile {
+  const uint8_t *a, *b;    // of the next K block
+  const float *ra, *rb;
+  uint16_t* out;           // the window's corner
+  int left;                // K blocks
+  int row_lo, col_lo;      // first row and column of the window that are the tile's
+};
+
+__device__ __forceinline__ WgradTile wgrad_tile(const GemmArgs& p, int id, const int* group, const int* begin,
+                                                const int* length) {
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int r = id / tiles;
+  int tm, tn;
+  tile_to_mn(xcd_remap(id - r * tiles, tiles), p.tiles_m, p.tiles_n, &tm, &tn);
+  const int g = __builtin_amdgcn_readfirstlane(group[r]);
+  const int64_t kb = __builtin_amdgcn_readfirstlane(begin[r]);
+  const int ml = min(tm * 256, p.M - 256), nl = min(tn * 256, p.N - 256);
+  WgradTile t;
+  t.left = __builtin_amdgcn_readfirstlane(length[r]);
+  t.a = p.a + (int64_t)ml * p.lda + kb * 128;
+  t.b = p.b + (int64_t)nl * p.ldb + kb * 128;
+  t.ra = p.ra + (int64_t)ml * p.ra_s_row + kb * p.ra_s_kb;
+  t.rb = p.rb + (int64_t)nl * p.rb_s_row + kb * p.rb_s_kb;
+  t.out = (uint16_t*)p.out + g * p.out_s_group + (int64_t)ml * p.ldo + nl;
+  t.row_lo = tm * 256 - ml;
+  t.col_lo = tn * 256 - nl;
+  return t;
+}
+
+__global__ __launch_bounds__(512) void wgrad_stream_kernel(const GemmArgs p) {
+  constexpr int TM = 8, TN = 4, LW = 2;
+  [[maybe_unused]] constexpr int AI = 16;   // loads of a loading wave: AI of A and of B,
+  constexpr int SI = 2;                     // SI of the scales of each
+  __shared__ __attribute__((aligned(1024))) uint8_t sA0[32768], sA1[32768], sB0[32768], sB1[32768];
+  __shared__ __attribute__((aligned(16))) float sRa0[256], sRa1[256], sRb0[256], sRb1[256];
+  __shared__ int group[kStreamGroups], begin[kStreamGroups], length[kStreamGroups], unsorted[kStreamGroups];
+  uint8_t* const sA[2] = {sA0, sA1};
+  uint8_t* const sB[2] = {sB0, sB1};
+  float* const sRa[2] = {sRa0, sRa1};
+  float* const sRb[2] = {sRb0, sRb1};
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int wmi = wave / 4, wni = wave % 4;
+  const int frow = lane & 15, fhalf = lane >> 4;
+
+  // Groups by falling length, ties by number.
+  for (int g = tid; g < p.kgroups; g += 512) {
+    int kb, end;
+    group_kblocks(p, g, &kb, &end);
+    unsorted[g] = end - kb;
+  }
+  __syncthreads();
+  for (int g = tid; g < p.kgroups; g += 512) {
+    const int n = unsorted[g];
+    int rank = 0;
+    for (int h = 0; h < p.kgroups; ++h) rank += unsorted[h] > n || (unsorted[h] == n && h < g) ? 1 : 0;
+    int kb, end;
+    group_kblocks(p, g, &kb, &end);
+    group[rank] = g;
+    begin[rank] = kb;
+    length[rank] = n;
+  }
+  __syncthreads();
+
+  const int total = p.kgroups * p.tiles_m * p.tiles_n;
+  int id = blockIdx.x;
+
+  // Lane offsets of the loads (see gemm_v2_kernel).
+  const int lrow = lane >> 3;
+  const int lchunk = (lane & 7) ^ ((4 * (wave & 1) + (lrow >> 1)) & 5);
+  [[maybe_unused]] const uint32_t a_voff = (uint32_t)((8 * wave + lrow) * p.lda + lchunk * 16);
+  [[maybe_unused]] const uint32_t b_voff = (uint32_t)((8 * wave + lrow) * p.ldb + lchunk * 16);
+  uint32_t ra_voff[SI], rb_voff[SI];
+#pragma unroll
+  for (int i = 0; i < SI; ++i) {
+    const int k = 64 * ((wave + LW * i) % 4) + lane, kb16 = k % 128;
+    ra_voff[i] = (uint32_t)((k / 128 * 128 + 16 * (4 * (kb16 / 64) + kb16 % 4) + kb16 % 64 / 4) * p.ra_s_row * 4);
+    rb_voff[i] = (uint32_t)(k * p.rb_s_row * 4);
+  }
+  auto issue = [&](const WgradTile& t, uint8_t* sa, uint8_t* sb, float* sra, float* srb) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const __amdgpu_buffer_rsrc_t ars = buffer_rsrc(t.a, 256 * p.lda), brs = buffer_rsrc(t.b, 256 * p.ldb);
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ars, (lds_void_t*)(sa + (wave + LW * i) * 1024), 16, a_voff,
+                                               8 * LW * i * (int)p.lda, 0, 0);
+#pragma unroll
+    for (int i = 0; i < AI; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(brs, (lds_void_t*)(sb + (wave + LW * i) * 1024), 16, b_voff,
+                                               8 * LW * i * (int)p.ldb, 0, 0);
+    const __amdgpu_buffer_rsrc_t rars = buffer_rsrc(t.ra, (255 * p.ra_s_row + 1) * 4);
+    const __amdgpu_buffer_rsrc_t rbrs = buffer_rsrc(t.rb, (255 * p.rb_s_row + 1) * 4);
+#pragma unroll
+    for (int i = 0; i < SI; ++i) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rars, (lds_void_t*)(sra + 64 * ((wave + LW * i) % 4)), 4, ra_voff[i], 0,
+                                               0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rbrs, (lds_void_t*)(srb + 64 * ((wave + LW * i) % 4)), 4, rb_voff[i], 0,
+                                               0, 0);
+    }
+#endif
+  };
+
+  // One K block out of LDS, as in gemm_v2_kernel: partials transposed (lane: one
+  // row, four columns), folded two MFMAs later.
+  auto block = [&](const uint8_t* tA, const uint8_t* tB, const float* tRa, const float* tRb, v4f (&acc)[TM][TN]) {
+    uint32_t a_lo = (wmi * 128 + frow) * 128 + (((2 * fhalf) ^ swz(frow)) << 4);
+    uint32_t a_hi = (wmi * 128 + frow) * 128 + (((2 * fhalf + 1) ^ swz(frow)) << 4);
+    uint32_t b_lo = (wni * 64 + frow) * 128 + (((2 * fhalf) ^ swz(frow)) << 4);
+    uint32_t b_hi = (wni * 64 + frow) * 128 + (((2 * fhalf + 1) ^ swz(frow)) << 4);
+    uint32_t ra_off = (wmi * 128 + 4 * frow) * 4, rb_off = (wni * 64 + 4 * fhalf) * 4;
+    asm volatile("" : "+v"(a_lo), "+v"(a_hi), "+v"(b_lo), "+v"(b_hi), "+v"(ra_off), "+v"(rb_off));
+    v8i bf[TN], af[2];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) bf[j] = load_frag_at(tB, b_lo + 2048 * j, b_hi + 2048 * j);
+    float sa[TM];
+    v4f sbc[TN];
+#pragma unroll
+    for (int q = 0; q < TM / 4; ++q) {
+      const v4f s4 = *(const v4f*)((const uint8_t*)tRa + ra_off + 256 * q);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) sa[4 * q + v] = s4[v];
+    }
+#pragma unroll
+    for (int j = 0; j < TN; ++j) sbc[j] = *(const v4f*)((const uint8_t*)tRb + rb_off + 64 * j);
+    af[0] = load_frag_at(tA, a_lo, a_hi);
+    v4f ring[kRingDelay + 1];
+#pragma unroll
+    for (int t = 0; t < TM * TN + kRingDelay; ++t) {
+      const int i = t / TN, j = t % TN;
+      if (t < TM * TN && j == 0 && i + 1 < TM)
+        af[(i + 1) % 2] = load_frag_at(tA, a_lo + 2048 * (i + 1), a_hi + 2048 * (i + 1));
+      if (t < TM * TN) ring[t % (kRingDelay + 1)] = mfma_fp8(bf[j], af[i % 2], v4f{0.f, 0.f, 0.f, 0.f});
+      if (t >= kRingDelay) {
+        const int u = t - kRingDelay, iu = u / TN, ju = u % TN;
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          acc[iu][ju][v] = __builtin_fmaf(ring[u % (kRingDelay + 1)][v] * sbc[ju][v], sa[iu], acc[iu][ju][v]);
+      }
+    }
+  };
+
+  // The tile's bf16 values through stage 1, rows 64 h .. 64 h + 63 of both halves
+  // of the tile at a time (LDS row 16 ii + frow of array wmi; 16-byte chunk c at
+  // c ^ (row & 15)), out as whole 512-byte rows by the waves that do not load.
+  // Every wave has passed a barrier behind the stage's last read.
+  auto epilogue = [&](const WgradTile& t, const v4f (&acc)[TM][TN]) {
+    typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+    typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint8_t* const mine = wmi ? sB1 : sA1;
+#pragma unroll
+      for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const v4f& x = acc[4 * h + ii][j];
+          u32x2 w;
+          w.x = pack_bf16x2_rne(x[0], x[1]);
+          w.y = pack_bf16x2_rne(x[2], x[3]);
+          const int chunk = 8 * wni + 2 * j + (fhalf >> 1);
+          *(u32x2*)(mine + (16 * ii + frow) * 512 + 16 * (chunk ^ frow) + 8 * (fhalf & 1)) = w;
+        }
+      __syncthreads();
+      if (wave >= LW) {
+        const int c = lane & 31;
+        for (int pr = wave - LW; pr < 64; pr += 8 - LW) {
+          const int lr = 2 * pr + (lane >> 5), rq = lr & 63;   // row of both arrays
+          const int row = 128 * (lr >> 6) + 64 * h + rq;
+          const u32x4 d = *(const u32x4*)((lr >> 6 ? sB1 : sA1) + rq * 512 + 16 * (c ^ (rq & 15)));
+          if (row >= t.row_lo && 8 * c >= t.col_lo)
+            __builtin_nontemporal_store(d, (u32x4*)(t.out + (int64_t)row * p.ldo + 8 * c));
+        }
+      } else if (h == 1) {
+        wait_vmcnt<0>();   // the next tile's first block has landed
+      }
+      __syncthreads();
+    }
+  };
+
+  // The next block to load.
+  WgradTile next;
+  int next_id = id;
+  auto advance = [&]() {
+    if (next.left > 1) {
+      --next.left;
+      next.a += 128;
+      next.b += 128;
+      next.ra += p.ra_s_kb;
+      next.rb += p.rb_s_kb;
+    } else if (next_id + (int)gridDim.x < total) {
+      next_id += gridDim.x;
+      const WgradTile t = wgrad_tile(p, next_id, group, begin, length);
+      if (t.left > 0) next = t;   // else the last block again, which nobody reads
+    }
+  };
+  auto load = [&](int st) {
+    issue(next, sA[st], sB[st], sRa[st], sRb[st]);
+    advance();
+  };
+  if (id < total) {
+    next = wgrad_tile(p, id, group, begin, length);
+    if (next.left > 0) {
+      if (wave < LW) {
+        load(0);
+        wait_vmcnt<0>();
+      }
+      __syncthreads();
+    }
+  }
+#pragma nounroll
+  for (; id < total; id += gridDim.x) {
+    const WgradTile t = wgrad_tile(p, id, group, begin, length);
+    if (t.left == 0) break;
+    v4f acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    // The tile's blocks take stages 0, 1, 0, ..; the next tile's first block goes
+    // to stage 0 under the last block where that is in stage 1, else behind it.
+    auto kloop = [&](auto role) {
+      constexpr bool kLoader = decltype(role)::value == 1;
+      for (int it0 = 0; it0 < t.left; it0 += 2) {
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const int it = it0 + st;
+          if (it >= t.left) break;
+          if (kLoader && (st == 1 || it + 1 < t.left)) load(st ^ 1);
+          block(sA[st], sB[st], sRa[st], sRb[st], acc);
+          if constexpr (kLoader) stage_sync<0>();
+          else stage_sync_noload();
+        }
+      }
+      if (kLoader && (t.left & 1)) load(0);
+    };
+    if (wave < LW) kloop(kloop_role<1>{});
+    else kloop(kloop_role<2>{});
+    epilogue(t, acc);
+  }
+  // Empty groups, last in the order: zeros.
+  for (; id < total; id += gridDim.x) {
+    const WgradTile t = wgrad_tile(p, id, group, begin, length);
+    const int c = 8 * (tid & 31);
+    for (int row = tid >> 5; row < 256; row += 16)
+      if (row >= t.row_lo && c >= t.col_lo) *(uint4*)(t.out + (int64_t)row * p.ldo + c) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+static bool wgrad_stream_ok(const GemmProblem& p, int groups, int64_t out_s_group) {
+  return groups <= kStreamGroups && p.out_kind == kOutBf16 && p.N % 8 == 0 && p.ldo % 8 == 0 && out_s_group % 8 == 0 &&
+         ((size_t)p.out & 15) == 0;
+}
+
 static int grouped_wgrad_config(const GemmProblem& p, int groups) {
   const int64_t cus = num_cus();
   auto fills = [&](int c) {
@@ -1847,13 +2116,6 @@ bool grouped_wgrad_ok(const GemmProblem& p, int groups) {
 template <int OUT>
 static void launch_wgrad_cfg(int cfg, const GemmArgs& a, dim3 grid, hipStream_t stream) {
   constexpr int MODE = kBlockB1x128;
-  if constexpr (OUT == kOutBf16) {
-    if (a.rounds > 1) {
-      hipLaunchKernelGGL((gemm_v2_kernel<256, 256, 2, 4, 2, MODE, OUT, false, false, true, true>), grid, dim3(512), 0,
-                         stream, a);
-      return;
-    }
-  }
   switch (cfg) {
     case 3:
       hipLaunchKernelGGL((gemm_v2_kernel<256, 256, 2, 4, 2, MODE, OUT, false, false, false, true>), grid, dim3(512), 0,
@@ -1897,17 +2159,13 @@ hipError_t launch_grouped_wgrad(const GemmProblem& p, int groups, const int* gro
   a.rounds = 1;
   a.group_end = group_end;
   a.out_s_group = out_s_group;
+  a.kgroups = groups;
   const int tiles = groups * a.tiles_m * a.tiles_n, cus = num_cus();
-  // Two or more rounds of interior tiles: one workgroup per CU runs every cus-th
-  // tile, its stores draining under the next tile's contraction, which is as
-  // short as one group's rows.
-  const bool persist = cfg == 3 && p.out_kind == kOutBf16 && tiles >= 2 * cus && p.M % 256 == 0 && p.N % 256 == 0 &&
-                       p.ldo % 8 == 0 && out_s_group % 8 == 0 && ((size_t)p.out & 15) == 0;
-  if (persist) {
-    a.rounds = (tiles + cus - 1) / cus;
-    a.tail_base = tiles;
+  if (cfg == 3 && wgrad_stream_ok(p, groups, out_s_group) && tiles > cus) {
+    hipLaunchKernelGGL(wgrad_stream_kernel, dim3((unsigned)cus), dim3(512), 0, stream, a);
+    return hipGetLastError();
   }
-  const dim3 grid((unsigned)(persist ? cus : tiles));
+  const dim3 grid((unsigned)tiles);
   if (p.out_kind == kOutBf16) launch_wgrad_cfg<kOutBf16>(cfg, a, grid, stream);
   else launch_wgrad_cfg<kOutF32>(cfg, a, grid, stream);
   return hipGetLastError();

@@ -133,3 +133,43 @@ def test_grouped_quantizer_is_the_quantizer(gpu, G, rows, cols, transpose):
     for i in range(G):
         want, want_recip = fp8.fp8_blockwise_quant(x[i], "128x128", transpose)
         assert torch.equal(q[i], want) and torch.equal(recip[i], want_recip)
+
+
+def _stream_case(gpu, M, N, ends, K, rows, seed):
+    """More 256x256 tiles than compute units: workgroups that run several tiles."""
+    return _case(gpu, M, N, K, ends, "bf16", seed=seed, rows=rows)
+
+
+def test_streams_of_whole_tiles(gpu):
+    # 64 groups x 2 x 3 tiles; odd and even lengths, equal ones, empty groups
+    lengths = [(7 * i) % 6 for i in range(64)]
+    ends = [int(e) * 128 for e in np.cumsum(lengths)]
+    got = _stream_case(gpu, 512, 768, ends, ends[-1] + 128, np.r_[0:4, 254:258, 508:512], 20)
+    for g, n in enumerate(lengths):
+        assert (not got[g].any()) == (n == 0)
+
+
+def test_streams_of_ragged_tiles(gpu):
+    # 2 x 2 tiles a group whose windows overlap; one long group among many short
+    lengths = [1] * 40 + [37] + [2] * 30 + [0] * 9
+    ends = [int(e) * 128 for e in np.cumsum(lengths)]
+    _stream_case(gpu, 360, 264, ends, ends[-1], np.r_[0:3, 100:108, 252:260, 356:360], 21)
+
+
+def test_streams_of_empty_groups_only(gpu):
+    out = _case(gpu, 512, 512, 256, [0] * 80, "bf16", seed=22, rows=[0, 511])
+    assert not out.any()
+
+
+def test_stream_leaves_gaps_alone(gpu):
+    """Strided outputs: rows and groups with gaps between them."""
+    M, N, K, G = 264, 520, 384, 100
+    a, ra, b, rb = _operands(M, N, K, 23)
+    ends = [min(3, i // 20) * 128 for i in range(1, G + 1)]
+    out = torch.full((G, M + 1, N + 8), 7.0, dtype=torch.bfloat16, device=gpu)
+    fp8.fp8_scaled_grouped_gemm_blockwise_wgrad(
+        torch.from_numpy(a).to(gpu), _colmajor(ra, gpu), torch.from_numpy(b).to(gpu), _colmajor(rb, gpu),
+        torch.tensor(ends, dtype=torch.int32, device=gpu), out=out[:, :M, :N])
+    ref, size = moe.grouped_wgrad(a[:40], ra[:40], b, rb, ends)
+    check_gemm_output(host_f32(out[:, :40, :N]).reshape(-1, N), ref.reshape(-1, N), size.reshape(-1, N), 3, "bf16", "stream")
+    assert (out[:, M:] == 7.0).all() and (out[:, :, N:] == 7.0).all()
