@@ -114,7 +114,9 @@ PROTOTYPES = {
                                  ctypes.POINTER(Layouts), c_ptr, c_i64, c_ptr, c_i64, c_i64, c_ptr]),
     "fp8_scaled_grouped_gemm_blockwise_wgrad": (c_int, [c_ptr, c_i64, c_ptr, c_i64, c_i64, c_ptr, c_i64,
                                                         c_ptr, c_i64, c_i64, c_int, c_ptr, c_i64, c_i64,
-                                                        c_i64, c_ptr, c_i64, c_i64, c_int, c_ptr]),
+                                                        c_i64, c_ptr, c_i64, c_i64, c_int, c_ptr,
+                                                        c_size, c_ptr]),
+    "fp8bw_grouped_wgrad_ws_bytes": (c_size, [c_i64, c_i64, c_i64, c_int]),
     "fp8_blockwise_quant_grouped": (c_int, [c_ptr, c_i64, c_i64, c_i64, c_i64, c_int, c_int, c_ptr,
                                             c_i64, c_i64, c_ptr, c_i64, c_i64, c_i64, c_ptr]),
 }

@@ -28,7 +28,9 @@
 //  * Split-K writes fp32 partials [split, M, N]; a separate kernel sums them
 //    in split order (deterministic, no atomics).
 
+#include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "device_common.h"
@@ -97,6 +99,14 @@ __device__ __forceinline__ void group_kblocks(const GemmArgs& p, int g, int* beg
   const int b = g == 0 ? 0 : p.group_end[g - 1] / 128;
   *begin = max(0, min(b, p.kblocks));
   *end = max(*begin, min(p.group_end[g] / 128, p.kblocks));
+}
+// Piece `split` of `splits` of them; pieces behind a short group's end are empty.
+__device__ __forceinline__ void group_kblocks_piece(const GemmArgs& p, int g, int split, int splits, int* begin,
+                                                    int* end) {
+  group_kblocks(p, g, begin, end);
+  const int per = (*end - *begin + splits - 1) / splits;
+  *begin = min(*end, *begin + split * per);
+  *end = min(*end, *begin + per);
 }
 
 // A grouped GEMM on the large tiles runs as two launches: the large-tile
@@ -260,8 +270,14 @@ __global__ __launch_bounds__(256) void gemm_kernel(const GemmArgs p_in) {
   int kb_end = min(p.kblocks, kb_begin + p.kb_per_split);
   if constexpr (KGROUP) {
     const int g = blockIdx.x / (p.tiles_m * p.tiles_n);
-    group_kblocks(p, g, &kb_begin, &kb_end);
-    p.out = (uint8_t*)p.out + g * p.out_s_group * (OUT == kOutBf16 ? 2 : 4);
+    if constexpr (SPLIT) {
+      group_kblocks_piece(p, g, blockIdx.y, gridDim.y, &kb_begin, &kb_end);
+      // [split][group][M][N]; the store below adds blockIdx.y matrices itself
+      p.partial += ((int64_t)blockIdx.y * (p.kgroups - 1) + g) * p.M * p.N;
+    } else {
+      group_kblocks(p, g, &kb_begin, &kb_end);
+      p.out = (uint8_t*)p.out + g * p.out_s_group * (OUT == kOutBf16 ? 2 : 4);
+    }
   }
 
   // Loader mapping: chunk (row = tid/8 + 32 i, 16-byte column tid%8).
@@ -933,8 +949,12 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_v2_kernel(const GemmArgs 
   int kb_begin = split * p.kb_per_split;
   int kb_end = min(p.kblocks, kb_begin + p.kb_per_split);
   if constexpr (KGROUP) {
-    group_kblocks(p, kgroup, &kb_begin, &kb_end);
-    p.out = (uint8_t*)p.out + kgroup * p.out_s_group * (OUT == kOutBf16 ? 2 : 4);
+    if constexpr (SPLIT) {
+      group_kblocks_piece(p, kgroup, blockIdx.y, gridDim.y, &kb_begin, &kb_end);
+    } else {
+      group_kblocks(p, kgroup, &kb_begin, &kb_end);
+      p.out = (uint8_t*)p.out + kgroup * p.out_s_group * (OUT == kOutBf16 ? 2 : 4);
+    }
   }
 
   // Per-lane byte offsets of this wave's first row octets of A and B.  Lane
@@ -1204,7 +1224,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_v2_kernel(const GemmArgs 
       pm0 = m0;
       pn0 = n0;
     } else {
-      pbase = p.partial + (int64_t)split * p.M * p.N;
+      const int64_t matrix = KGROUP ? (int64_t)blockIdx.y * p.kgroups + kgroup : split;
+      pbase = p.partial + matrix * p.M * p.N;
       pld = p.N;
     }
   }
@@ -2096,52 +2117,141 @@ static bool wgrad_stream_ok(const GemmProblem& p, int groups, int64_t out_s_grou
          ((size_t)p.out & 15) == 0;
 }
 
-static int grouped_wgrad_config(const GemmProblem& p, int groups) {
-  const int64_t cus = num_cus();
-  auto fills = [&](int c) {
-    return groups * ((p.M + kCfgs[c].bm - 1) / kCfgs[c].bm) * ((p.N + kCfgs[c].bn - 1) / kCfgs[c].bn) >= cus;
-  };
-  if (gemm_config_ok(p, 3) && fills(3)) return 3;
-  if (gemm_config_ok(p, 2) && fills(2)) return 2;
-  return p.M >= 128 && p.N >= 128 && fills(0) ? 0 : 1;
+// How a call runs: the tile configuration and the pieces every group's
+// contraction is cut into (fp32 partials [splits][groups][M][N], joined in order).
+// By the sizes alone, so that the workspace query needs no strides; operands whose
+// strides the large tiles do not take run on 64x64 tiles in as many pieces.
+struct WgradPlan {
+  int cfg, splits;
+};
+
+static int64_t wgrad_tiles(const GemmProblem& p, int groups, int c) {
+  return groups * ((p.M + kCfgs[c].bm - 1) / kCfgs[c].bm) * ((p.N + kCfgs[c].bn - 1) / kCfgs[c].bn);
+}
+
+// Microseconds of `n` tiles of configuration c (all groups and pieces) over kb K
+// blocks each, as measured (one MI355X, 256 CUs): a round of 256x256 tiles takes
+// 2.0 us a K block and 6 beside them; 128x128 tiles, two to a CU, 1.05 us a block
+// alone and 1.5 together; 64x64 tiles, four to a CU, 0.45 to 1.0.  (256x128 tiles
+// lost to one of these at every size: 4 groups of 256 x 4096, 64 blocks: 66.7 us
+// against 58.1.)
+static double wgrad_cost(int c, double n, double kb, double cus) {
+  const double r = n / (cus * (c == 3 ? 1 : c == 0 ? 2 : 4));
+  // Many rounds run into each other, and groups' lengths differ.
+  const double rounds = r < 2 ? std::ceil(r) : r + 0.25;
+  if (c == 3) return rounds * (2.0 * kb + 6) + 5;
+  if (c == 0) return rounds * ((1.05 + 0.45 * std::min(1.0, std::max(0.0, 2 * r - 1))) * kb + 3) + 3;
+  return rounds * ((0.45 + 0.55 * std::min(1.0, r)) * kb + 2) + 6;
+}
+
+// The cheapest by that estimate for groups of equal length; a further launch joins
+// pieces (4 us) and the fp32 partials, at most 256 MB, are written and read (8 TB/s
+// out of the memory-side cache).  1 group, 512 x 512, 256 blocks: 149 us in one
+// piece, 33 in eight; 2048 x 2048: 220 to 149 us (256x256 tiles, four pieces).
+static WgradPlan wgrad_plan(const GemmProblem& p, int groups) {
+  const double cus = num_cus(), kb = std::max(1.0, (double)(p.K / 128) / groups);
+  const double matrix = (double)groups * p.M * p.N;
+  WgradPlan best = {1, 1};
+  double least = 1e30;
+  for (int c : {3, 0, 1}) {
+    // (the large tiles need a whole one; half of a smaller one may be empty)
+    if (c == 3 && (p.M < 256 || p.N < 256)) continue;
+    if (c == 0 && (p.M < 64 || p.N < 64)) continue;
+    const double n = (double)wgrad_tiles(p, groups, c);
+    for (int s = 1; s <= 32; s *= 2) {
+      if (s > 1 && (s > kb || 4 * s * matrix > 256e6)) break;
+      const double t = wgrad_cost(c, n * s, kb / s, cus) + (s > 1 ? 4 + s * matrix / 1e6 : 0);
+      if (t < least) {
+        least = t;
+        best = {c, s};
+      }
+    }
+  }
+  return best;
+}
+
+static int wgrad_config(const GemmProblem& p, int planned) { return gemm_config_ok(p, planned) ? planned : 1; }
+
+size_t grouped_wgrad_ws_bytes(const GemmProblem& p, int groups) {
+  const WgradPlan w = wgrad_plan(p, groups);
+  return w.splits > 1 ? (size_t)w.splits * (size_t)groups * (size_t)p.M * (size_t)p.N * sizeof(float) : 0;
 }
 
 bool grouped_wgrad_ok(const GemmProblem& p, int groups) {
-  const int cfg = grouped_wgrad_config(p, groups);
+  const WgradPlan w = wgrad_plan(p, groups);
   // fewer than 2^32 threads a launch, at most 512 a workgroup
-  return groups * ((p.M + kCfgs[cfg].bm - 1) / kCfgs[cfg].bm) * ((p.N + kCfgs[cfg].bn - 1) / kCfgs[cfg].bn) <
-         (int64_t)1 << 23;
+  return wgrad_tiles(p, groups, wgrad_config(p, w.cfg)) * w.splits < (int64_t)1 << 23;
 }
 
+// out_g = the sum of the group's partials in order, four columns a thread where
+// rows have whole quads.
 template <int OUT>
+__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* __restrict__ part, int splits, int groups, int M,
+                                                         int N, void* __restrict__ out, int64_t ldo,
+                                                         int64_t out_s_group) {
+  const int64_t total = (int64_t)groups * M * N;
+  const int q = (N & 3) == 0 ? 4 : 1;
+  const bool vec = q == 4 && (ldo & 3) == 0 && (out_s_group & 3) == 0;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * q; i < total; i += (int64_t)gridDim.x * 256 * q) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < splits; ++k) {
+      if (q == 4) {
+        const float4 v = *(const float4*)(part + k * total + i);
+        s[0] += v.x;
+        s[1] += v.y;
+        s[2] += v.z;
+        s[3] += v.w;
+      } else {
+        s[0] += part[k * total + i];
+      }
+    }
+    const int64_t row = i / N, g = row / M;
+    const int64_t at = g * out_s_group + (row - g * M) * ldo + (i - row * N);
+    if (vec) {
+      if (OUT == kOutBf16)
+        *(uint2*)((uint16_t*)out + at) = make_uint2(pack_bf16x2_rne(s[0], s[1]), pack_bf16x2_rne(s[2], s[3]));
+      else
+        *(float4*)((float*)out + at) = make_float4(s[0], s[1], s[2], s[3]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        if (v >= q) break;
+        if (OUT == kOutBf16) ((uint16_t*)out)[at + v] = (uint16_t)f32_to_bf16_rne(s[v]);
+        else ((float*)out)[at + v] = s[v];
+      }
+    }
+  }
+}
+
+template <int OUT, bool SPLIT>
 static void launch_wgrad_cfg(int cfg, const GemmArgs& a, dim3 grid, hipStream_t stream) {
   constexpr int MODE = kBlockB1x128;
   switch (cfg) {
     case 3:
-      hipLaunchKernelGGL((gemm_v2_kernel<256, 256, 2, 4, 2, MODE, OUT, false, false, false, true>), grid, dim3(512), 0,
-                         stream, a);
-      break;
-    case 2:
-      hipLaunchKernelGGL((gemm_v2_kernel<256, 128, 2, 2, 3, MODE, OUT, false, false, false, true>), grid, dim3(256), 0,
+      hipLaunchKernelGGL((gemm_v2_kernel<256, 256, 2, 4, 2, MODE, OUT, SPLIT, false, false, true>), grid, dim3(512), 0,
                          stream, a);
       break;
     case 0:
-      hipLaunchKernelGGL((gemm_kernel<128, 128, MODE, OUT, false, true>), grid, dim3(256), 0, stream, a);
+      hipLaunchKernelGGL((gemm_kernel<128, 128, MODE, OUT, SPLIT, true>), grid, dim3(256), 0, stream, a);
       break;
     default:
-      hipLaunchKernelGGL((gemm_kernel<64, 64, MODE, OUT, false, true>), grid, dim3(256), 0, stream, a);
+      hipLaunchKernelGGL((gemm_kernel<64, 64, MODE, OUT, SPLIT, true>), grid, dim3(256), 0, stream, a);
   }
 }
 
-hipError_t launch_grouped_wgrad(const GemmProblem& p, int groups, const int* group_end, int64_t out_s_group,
+hipError_t launch_grouped_wgrad(const GemmProblem& p, int groups, const int* group_end, int64_t out_s_group, void* ws,
                                 hipStream_t stream) {
-  const int cfg = grouped_wgrad_config(p, groups);
+  const WgradPlan w = wgrad_plan(p, groups);
+  const int cfg = wgrad_config(p, w.cfg);
+  const int64_t tiles = wgrad_tiles(p, groups, cfg);
+  const int bm = kCfgs[cfg].bm, bn = kCfgs[cfg].bn;
   GemmArgs a = {};
   a.a = (const uint8_t*)p.a;
   a.b = (const uint8_t*)p.b;
   a.ra = p.ra;
   a.rb = p.rb;
   a.out = p.out;
+  a.partial = (float*)ws;
   a.lda = p.lda;
   a.ldb = p.ldb;
   a.ldo = p.ldo;
@@ -2154,20 +2264,34 @@ hipError_t launch_grouped_wgrad(const GemmProblem& p, int groups, const int* gro
   a.K = (int)p.K;
   a.kblocks = (int)(p.K / 128);
   a.kb_per_split = a.kblocks;
-  a.tiles_m = (int)((p.M + kCfgs[cfg].bm - 1) / kCfgs[cfg].bm);
-  a.tiles_n = (int)((p.N + kCfgs[cfg].bn - 1) / kCfgs[cfg].bn);
+  a.tiles_m = (int)((p.M + bm - 1) / bm);
+  a.tiles_n = (int)((p.N + bn - 1) / bn);
   a.rounds = 1;
   a.group_end = group_end;
   a.out_s_group = out_s_group;
   a.kgroups = groups;
-  const int tiles = groups * a.tiles_m * a.tiles_n, cus = num_cus();
-  if (cfg == 3 && wgrad_stream_ok(p, groups, out_s_group) && tiles > cus) {
+  const int cus = num_cus();
+  if (w.splits == 1 && cfg == 3 && tiles > cus && wgrad_stream_ok(p, groups, out_s_group)) {
     hipLaunchKernelGGL(wgrad_stream_kernel, dim3((unsigned)cus), dim3(512), 0, stream, a);
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)tiles);
-  if (p.out_kind == kOutBf16) launch_wgrad_cfg<kOutBf16>(cfg, a, grid, stream);
-  else launch_wgrad_cfg<kOutF32>(cfg, a, grid, stream);
+  const dim3 grid((unsigned)tiles, (unsigned)w.splits);
+  if (w.splits == 1) {
+    if (p.out_kind == kOutBf16) launch_wgrad_cfg<kOutBf16, false>(cfg, a, grid, stream);
+    else launch_wgrad_cfg<kOutF32, false>(cfg, a, grid, stream);
+    return hipGetLastError();
+  }
+  launch_wgrad_cfg<kOutF32, true>(cfg, a, grid, stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t quads = (groups * p.M * p.N + 3) / 4;
+  const dim3 join((unsigned)std::min<int64_t>((quads + 255) / 256, 4096));
+  if (p.out_kind == kOutBf16)
+    hipLaunchKernelGGL(wgrad_join_kernel<kOutBf16>, join, dim3(256), 0, stream, a.partial, w.splits, groups, a.M, a.N,
+                       a.out, a.ldo, out_s_group);
+  else
+    hipLaunchKernelGGL(wgrad_join_kernel<kOutF32>, join, dim3(256), 0, stream, a.partial, w.splits, groups, a.M, a.N,
+                       a.out, a.ldo, out_s_group);
   return hipGetLastError();
 }
 

@@ -99,7 +99,8 @@ hipError_t launch_grouped_gemm(const GemmProblem& p, int groups, const int* grou
 // Weight gradients: out + g*out_s_group = A . B^T over the K blocks
 // [group_end[g-1] / 128, group_end[g] / 128), mode kBlockB1x128.
 bool grouped_wgrad_ok(const GemmProblem& p, int groups);
-hipError_t launch_grouped_wgrad(const GemmProblem& p, int groups, const int* group_end, int64_t out_s_group,
+size_t grouped_wgrad_ws_bytes(const GemmProblem& p, int groups);
+hipError_t launch_grouped_wgrad(const GemmProblem& p, int groups, const int* group_end, int64_t out_s_group, void* ws,
                                 hipStream_t stream);
 // Fill a contiguous bf16 [rows, cols] matrix with +0.
 hipError_t launch_zero_bf16(void* out, int64_t rows, int64_t cols, hipStream_t stream);

@@ -291,11 +291,20 @@ int check_wgrad_operand(const void* q, int64_t rows, int64_t K, int64_t ld, cons
 
 }  // namespace
 
+FP8BW_API size_t fp8bw_grouped_wgrad_ws_bytes(int64_t M, int64_t N, int64_t K, int groups) {
+  if (groups < 1 || groups > (1 << 20) || M <= 0 || N <= 0 || K <= 0 || K % 128 || M > kMaxDim || N > kMaxDim ||
+      K > kMaxDim)
+    return 0;
+  fp8bw::GemmProblem p = {};
+  p.M = M; p.N = N; p.K = K;
+  return align_up(fp8bw::grouped_wgrad_ws_bytes(p, groups));
+}
+
 FP8BW_API int fp8_scaled_grouped_gemm_blockwise_wgrad(
     const void* a, int64_t lda, const float* ra, int64_t ra_s_row, int64_t ra_s_kb, const void* b,
     int64_t ldb, const float* rb, int64_t rb_s_row, int64_t rb_s_kb, int groups, const int* group_end,
     int64_t M, int64_t N, int64_t K, void* out, int64_t ldo, int64_t out_s_group, int out_dtype,
-    void* stream) {
+    void* ws, size_t ws_bytes, void* stream) {
   if (groups < 1 || groups > (1 << 20)) return fail(FP8BW_ERR_SHAPE, "groups=%d must be in [1, 2^20]", groups);
   if (M < 0 || N < 0 || K < 0) return fail(FP8BW_ERR_SHAPE, "negative dimension");
   if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return fail(FP8BW_ERR_SHAPE, "dimension too large");
@@ -328,7 +337,9 @@ FP8BW_API int fp8_scaled_grouped_gemm_blockwise_wgrad(
   if (!fp8bw::grouped_wgrad_ok(p, groups))
     return fail(FP8BW_ERR_UNSUPPORTED, "%d groups of [%lld, %lld] are more output tiles than one launch takes", groups,
                 (long long)M, (long long)N);
-  return hip_status(fp8bw::launch_grouped_wgrad(p, groups, group_end, groups > 1 ? out_s_group : 0,
+  const size_t need = align_up(fp8bw::grouped_wgrad_ws_bytes(p, groups));
+  if (need > 0 && (st = check_ws(ws, ws_bytes, need)) != FP8BW_OK) return st;
+  return hip_status(fp8bw::launch_grouped_wgrad(p, groups, group_end, groups > 1 ? out_s_group : 0, ws,
                                                 (hipStream_t)stream),
                     "fp8_scaled_grouped_gemm_blockwise_wgrad");
 }

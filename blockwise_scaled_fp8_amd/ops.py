@@ -1033,10 +1033,12 @@ def fp8_scaled_grouped_gemm_blockwise_wgrad(a, ra, b, rb, group_end, out_dtype=t
         raise ValueError("out must be bfloat16 or float32 with unit column stride")
     if G == 0:
         return out
+    nws = lib.fp8bw_grouped_wgrad_ws_bytes(M, N, K, G)
+    ws = torch.empty(nws, dtype=torch.uint8, device=a.device) if nws else None
     check(lib.fp8_scaled_grouped_gemm_blockwise_wgrad(
         a.data_ptr(), a.stride(0), ra.data_ptr(), ra.stride(0), ra.stride(1), b.data_ptr(), b.stride(0),
         rb.data_ptr(), rb.stride(0), rb.stride(1), G, group_end.data_ptr(), M, N, K, out.data_ptr(),
-        out.stride(1), out.stride(0), OUT_DTYPES[out.dtype], _stream(a)))
+        out.stride(1), out.stride(0), OUT_DTYPES[out.dtype], _ptr(ws), nws, _stream(a)))
     return out
 
 

@@ -686,15 +686,20 @@ int fp8bw_swiglu_bwd(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h,
  *              without blocks gives zeros.
  *   out        device [M, N] per group, bf16 or fp32, ldo, out_s_group elements apart
  *              (>= (M - 1) * ldo + N).
+ *   ws         fp8bw_grouped_wgrad_ws_bytes(M, N, K, groups) bytes, 256-byte aligned:
+ *              fp32 partials of few tiles over long contractions, joined in a fixed
+ *              order (0 where there are none: ws may be NULL).
  *   Requires K % 128 == 0, 1 <= groups <= 2^20 and at most 2^23 output tiles; errors as
  *   fp8_scaled_gemm_blockwise.
  */
+size_t fp8bw_grouped_wgrad_ws_bytes(int64_t M, int64_t N, int64_t K, int groups);
 int fp8_scaled_grouped_gemm_blockwise_wgrad(const void* a, int64_t lda, const float* ra,
                                             int64_t ra_s_row, int64_t ra_s_kb, const void* b,
                                             int64_t ldb, const float* rb, int64_t rb_s_row,
                                             int64_t rb_s_kb, int groups, const int* group_end,
                                             int64_t M, int64_t N, int64_t K, void* out, int64_t ldo,
-                                            int64_t out_s_group, int out_dtype, void* stream);
+                                            int64_t out_s_group, int out_dtype, void* ws,
+                                            size_t ws_bytes, void* stream);
 
 /*
  * fp8_blockwise_quant_grouped -- fp8_blockwise_quant with 128x128 blocks of `groups`

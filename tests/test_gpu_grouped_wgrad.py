@@ -173,3 +173,48 @@ def test_stream_leaves_gaps_alone(gpu):
     ref, size = moe.grouped_wgrad(a[:40], ra[:40], b, rb, ends)
     check_gemm_output(host_f32(out[:, :40, :N]).reshape(-1, N), ref.reshape(-1, N), size.reshape(-1, N), 3, "bf16", "stream")
     assert (out[:, M:] == 7.0).all() and (out[:, :, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("od", ["bf16", "f32"])
+@pytest.mark.parametrize("M, N, lengths, tail", [
+    (64, 64, [40], 0), (130, 70, [33, 0, 5], 2), (512, 512, [64], 0), (48, 1001, [17, 30], 1), (256, 256, [9, 60, 0, 3], 4),
+    (1024, 1024, [40], 0), (1100, 900, [64], 3)])
+def test_long_contractions_in_pieces(gpu, M, N, lengths, tail, od):
+    """Few tiles over long contractions: pieces joined in order, some of them
+    empty where a group is short."""
+    ends = [int(e) * 128 for e in np.cumsum(lengths)]
+    K = ends[-1] + 128 * tail
+    assert fp8.load_library().fp8bw_grouped_wgrad_ws_bytes(M, N, K, len(ends)) > 0
+    got = _case(gpu, M, N, K, ends, od, seed=M + N, rows=np.r_[0:min(M, 40), M - 1])
+    again = _case(gpu, M, N, K, ends, od, seed=M + N, rows=[0])
+    assert np.array_equal(got, again)
+
+
+def test_pieces_into_a_strided_output(gpu):
+    M, N, K = 96, 120, 128 * 40
+    a, ra, b, rb = _operands(M, N, K, 30)
+    for N_, od in ((N, torch.bfloat16), (N - 1, torch.float32), (N - 2, torch.bfloat16)):
+        out = torch.full((2, M + 2, N + 3), 7.0, dtype=od, device=gpu)
+        ends = [128 * 7, K]
+        fp8.fp8_scaled_grouped_gemm_blockwise_wgrad(
+            torch.from_numpy(a).to(gpu), _colmajor(ra, gpu), torch.from_numpy(b[:N_].copy()).to(gpu),
+            _colmajor(rb[:N_], gpu), torch.tensor(ends, dtype=torch.int32, device=gpu), out=out[:, :M, :N_])
+        ref, size = moe.grouped_wgrad(a, ra, b[:N_], rb[:N_], ends)
+        check_gemm_output(host_f32(out[:, :M, :N_]).reshape(-1, N_), ref.reshape(-1, N_), size.reshape(-1, N_), 40,
+                          "f32" if od == torch.float32 else "bf16", "pieces, strided")
+        assert (out[:, M:] == 7.0).all() and (out[:, :, N_:] == 7.0).all()
+
+
+def test_strides_that_the_large_tiles_do_not_take(gpu):
+    """A row stride of 2^23 codes: 256 rows pass 2^31 bytes, so that the large
+    tiles' 32-bit offsets do not reach; the small ones run instead."""
+    M, N, K, ld = 272, 256, 256, 1 << 23
+    a, ra, b, rb = _operands(M, N, K, 31)
+    wide = torch.empty(M * ld, dtype=torch.uint8, device=gpu).view(M, ld)
+    wide[:, :K] = torch.from_numpy(a).to(gpu)
+    say("wide stride")
+    out = fp8.fp8_scaled_grouped_gemm_blockwise_wgrad(
+        wide[:, :K], _colmajor(ra, gpu), torch.from_numpy(b).to(gpu), _colmajor(rb, gpu),
+        torch.tensor([128, 256] + [256] * 300, dtype=torch.int32, device=gpu), out_dtype=torch.float32)
+    ref, size = moe.grouped_wgrad(a[-30:], ra[-30:], b, rb, [128, 256])
+    check_gemm_output(host_f32(out[:2, -30:]).reshape(-1, N), ref.reshape(-1, N), size.reshape(-1, N), 2, "f32", "wide")

@@ -150,7 +150,7 @@ def test_swiglu_bwd(lib, want, kw):
 
 
 WGRAD = dict(a=P, lda=256, ra=P, ra_s_row=1, ra_s_kb=64, b=P, ldb=256, rb=P, rb_s_row=1, rb_s_kb=96, groups=4, group_end=P,
-             M=64, N=96, K=256, out=P, ldo=96, out_s_group=64 * 96, out_dtype=0, stream=None)
+             M=64, N=96, K=256, out=P, ldo=96, out_s_group=64 * 96, out_dtype=0, ws=None, ws_bytes=0, stream=None)
 
 
 @pytest.mark.parametrize("want, kw", [
@@ -194,3 +194,15 @@ def test_the_binding_takes_gpu_tensors_only():
                  lambda: fp8.fp8_scaled_grouped_gemm_blockwise_wgrad(codes, scales, codes, scales, t.group_end)):
         with pytest.raises(ValueError, match="HIP"):
             call()
+
+
+def test_grouped_wgrad_workspace(lib):
+    need = lib.fp8bw_grouped_wgrad_ws_bytes(512, 512, 32768, 1)
+    assert need >= 2 * 512 * 512 * 4 and need % 256 == 0
+    assert lib.fp8bw_grouped_wgrad_ws_bytes(8192, 5120, 33280, 16) == 0
+    for bad in ((512, 512, 32768, 0), (0, 512, 32768, 1), (512, 512, 32760, 1), (-1, 512, 32768, 1), (BIG, 1, 128, 1)):
+        assert lib.fp8bw_grouped_wgrad_ws_bytes(*bad) == 0
+    long = dict(WGRAD, groups=1, M=512, N=512, K=32768, lda=32768, ldb=32768, ra_s_kb=512, rb_s_kb=512, ldo=512,
+                ws=P, ws_bytes=need)
+    for want, kw in ((WS, dict(ws=None)), (WS, dict(ws_bytes=need - 1)), (ALIGN, dict(ws=P + 128))):
+        _check(lib, "fp8_scaled_grouped_gemm_blockwise_wgrad", long, want, kw)
