@@ -2139,9 +2139,9 @@ static double wgrad_cost(int c, double n, double kb, double cus) {
   const double r = n / (cus * (c == 3 ? 1 : c == 0 ? 2 : 4));
   // Many rounds run into each other, and groups' lengths differ.
   const double rounds = r < 2 ? std::ceil(r) : r + 0.25;
-  if (c == 3) return rounds * (2.0 * kb + 6) + 5;
-  if (c == 0) return rounds * ((1.05 + 0.45 * std::min(1.0, std::max(0.0, 2 * r - 1))) * kb + 3) + 3;
-  return rounds * ((0.45 + 0.55 * std::min(1.0, r)) * kb + 2) + 6;
+  if (c == 3) return rounds * (2.0 * kb + 6) + 3;
+  if (c == 0) return rounds * ((1.05 + 0.45 * std::min(1.0, std::max(0.0, 2 * r - 1))) * kb + 3) + 4;
+  return rounds * ((0.45 + 0.55 * std::min(1.0, r)) * kb + 2) + 2.5;
 }
 
 // The cheapest by that estimate for groups of equal length; a further launch joins

@@ -293,7 +293,7 @@ __device__ __forceinline__ void store_row8(const LayoutsOut& o, int64_t row, int
 // Codes of a piece; every lane of a DPP row takes part, those past the last
 // column with zeros.
 __device__ __forceinline__ uint2 block_codes(const float (&v)[8], float* recip) {
-  const float s = scale_from_amax(row16_max(absmax8(v)));
+  const float s = scale_from_amax(row16_amax(v));
   *recip = recip_of_scale(s);
   return codes8(v, s);
 }
@@ -370,11 +370,12 @@ __global__ __launch_bounds__(256) void moe_gather_rows_kernel(const MoeGatherArg
 // every layout is written.  A tile's corner is in scalar registers and a thread's
 // offsets from it in 32 bits (the host keeps 128 leading dimensions below 2^31
 // bytes).
-__global__ __launch_bounds__(512, 4) void moe_gather_tile_kernel(const MoeGatherArgs p, int col_tiles) {
-  __shared__ TileLds<1> L;
-  __shared__ int token[128];
-  __shared__ float factor[128];
-  const int tid = threadIdx.x, lane16 = tid & 15, row0 = (tid >> 4) * 4, col = lane16 * 8;
+__global__ __launch_bounds__(256, 4) void moe_gather_tile_kernel(const MoeGatherArgs p, int col_tiles) {
+  constexpr int R = 8;
+  __shared__ TileLds<1, R> L;
+  __shared__ __attribute__((aligned(16))) int token[128];
+  __shared__ __attribute__((aligned(16))) float factor[128];
+  const int tid = threadIdx.x, lane16 = tid & 15, row0 = (tid >> 4) * R, col = lane16 * 8;
   const int64_t rb = blockIdx.x / col_tiles, cb = blockIdx.x - rb * col_tiles;
   const int rows = (int)min(p.table.rows - rb * 128, (int64_t)128);   // of the tile
   const int cols = (int)min(p.cols - cb * 128, (int64_t)128);
@@ -387,19 +388,25 @@ __global__ __launch_bounds__(512, 4) void moe_gather_tile_kernel(const MoeGather
   }
   __syncthreads();
   const uint16_t* const x = p.x + cb * 128;
-  uint4 u[4];
+  uint4 u[R];
+  int tk[R];
+  bool whole = col < cols;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int tk = token[row0 + k];
-    const bool in = col < cols && tk >= 0;
-    u[k] = *(const uint4*)(x + (in ? tk * p.ld_x + col : 0));
-    if (!in) u[k] = make_uint4(0, 0, 0, 0);
+  for (int k = 0; k < R; ++k) {
+    tk[k] = token[row0 + k];
+    whole = whole && tk[k] >= 0;
+    u[k] = *(const uint4*)(x + (tk[k] >= 0 && col < cols ? tk[k] * p.ld_x + col : 0));
+  }
+  if (!__all(whole)) {   // padding or a ragged edge
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (tk[k] < 0 || col >= cols) u[k] = make_uint4(0, 0, 0, 0);
   }
   // (Without weights the factor is 1; the product spares the maxima the step
   // that quiets a value of unknown origin.)
-  float v[4][8];
+  float v[R][8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < R; ++k) {
     unpack8(u[k], v[k]);
     const float w = factor[row0 + k];
 #pragma unroll
@@ -410,20 +417,20 @@ __global__ __launch_bounds__(512, 4) void moe_gather_tile_kernel(const MoeGather
     uint16_t* const corner = o.y + rb * 128 * o.ld_y + cb * 128;
     uint32_t at = row0 * (uint32_t)o.ld_y + col;
 #pragma unroll
-    for (int k = 0; k < 4; ++k, at += (uint32_t)o.ld_y)
+    for (int k = 0; k < R; ++k, at += (uint32_t)o.ld_y)
       if (row0 + k < rows && col < cols) *(uint4*)(corner + at) = pack8(v[k]);
   }
   if (o.q) {
-    float amax[4], scale[4];
+    float amax[R], scale[R];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) amax[k] = row16_max(absmax8(v[k]));
+    for (int k = 0; k < R; ++k) amax[k] = row16_amax(v[k]);
     const float recip = row16_scales(amax, scale);
     uint8_t* const corner = o.q + rb * 128 * o.ld_q + cb * 128;
     uint32_t at = row0 * (uint32_t)o.ld_q + col;
 #pragma unroll
-    for (int k = 0; k < 4; ++k, at += (uint32_t)o.ld_q)
+    for (int k = 0; k < R; ++k, at += (uint32_t)o.ld_q)
       if (row0 + k < rows && col < cols) *(uint2*)(corner + at) = codes8(v[k], scale[k]);
-    if (lane16 < 4 && row0 + lane16 < rows) o.recip[(rb * 128 + row0 + lane16) * o.rs_row + cb * o.rs_kb] = recip;
+    if (lane16 < R && row0 + lane16 < rows) o.recip[(rb * 128 + row0 + lane16) * o.rs_row + cb * o.rs_kb] = recip;
   }
   __syncthreads();
   if (tid < 128) {
@@ -493,9 +500,8 @@ hipError_t launch_moe_gather(const MoeGatherArgs& p, hipStream_t stream) {
   }
   if (t.rows == 0 || (!p.out.y && !p.out.q && !p.out.qt)) return hipSuccess;
   if (p.out.qt) {
-    const int64_t ct = (p.cols + 127) / 128;
-    hipLaunchKernelGGL(moe_gather_tile_kernel, dim3((unsigned)(ct * ((t.rows + 127) / 128))), dim3(512), 0, stream,
-                       p, (int)ct);
+    const int64_t ct = (p.cols + 127) / 128, rt = (t.rows + 127) / 128;
+    hipLaunchKernelGGL(moe_gather_tile_kernel, dim3((unsigned)(ct * rt)), dim3(256), 0, stream, p, (int)ct);
     return hipGetLastError();
   }
   const int64_t pieces = (p.cols + 511) / 512, items = t.tokens * pieces, fill = (t.rows + 15) / 16;

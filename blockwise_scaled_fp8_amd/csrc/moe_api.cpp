@@ -178,6 +178,8 @@ int moe_gather(const void* x, int64_t ld_x, const void* y, int64_t ld_y, const v
   p.out = layouts(*out, rows, cols, blocks);
   p.y = (const uint16_t*)y; p.ld_y = used_stride(rows, ld_y);
   p.dweight = dweight;
+  if (p.out.qt && (st = check_tile_strides({p.out.y ? p.out.ld_y : 0}, {p.out.q ? p.out.ld_q : 0, p.out.ld_qt})) != FP8BW_OK)
+    return st;
   return hip_status(fp8bw::launch_moe_gather(p, (hipStream_t)stream), what);
 }
 

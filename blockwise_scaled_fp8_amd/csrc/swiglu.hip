@@ -100,7 +100,7 @@ __global__ __launch_bounds__(256) void swiglu_fwd_rows_kernel(const SwigluFwdArg
     if (p.out.y && in[k]) *(uint4*)(p.out.y + r * p.out.ld_y + c0) = pack8(v);
     if (!p.out.q && !p.hq) continue;
     // three blocks: v, g, u
-    const float amax[3] = {row16_max(absmax8(v)), row16_max(absmax8(g)), row16_max(absmax8(u))};
+    const float amax[3] = {row16_amax(v), row16_amax(g), row16_amax(u)};
     float scale[3];
     const float recip = row16_scales(amax, scale);
     const int i = lane & 15;   // writes the scale of block i
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(256) void swiglu_bwd_rows_kernel(const SwigluBwdArg
     }
     if (p.dh.q) {
       uint8_t* const q = p.dh.q + r * p.dh.ld_q + c0;
-      const float amax[2] = {row16_max(absmax8(g)), row16_max(absmax8(u))};
+      const float amax[2] = {row16_amax(g), row16_amax(u)};
       float scale[2];
       const float recip = row16_scales(amax, scale);
       put_codes8(g, scale[0], q, in[k]);
@@ -231,7 +231,7 @@ __device__ __forceinline__ void load_tile_halves(const Tile& t, const void* h, i
 }
 
 __global__ __launch_bounds__(512, 4) void swiglu_fwd_tile_kernel(const SwigluFwdArgs p, int col_tiles) {
-  __shared__ TileLds<1> L;
+  __shared__ TileLds<1, 4> L;
   const Tile t = tile_of(p.rows, p.ffn, col_tiles);
   const int tid = threadIdx.x, lane16 = tid & 15;
   const int64_t blocks = (p.ffn + 127) >> 7;
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(512, 4) void swiglu_fwd_tile_kernel(const SwigluFwd
     const int64_t col = t.cb * 128 + t.col;
     if (o.y && in) *(uint4*)(o.y + r * o.ld_y + col) = pack8(v[k]);
     if (!o.q && !p.hq) continue;
-    const float amax[3] = {row16_max(absmax8(v[k])), row16_max(absmax8(g)), row16_max(absmax8(u))};
+    const float amax[3] = {row16_amax(v[k]), row16_amax(g), row16_amax(u)};
     float scale[3];
     const float recip = row16_scales(amax, scale);
     if (o.q) {
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(512, 4) void swiglu_fwd_tile_kernel(const SwigluFwd
 // Arrays of a tile: 0 dg, 1 du, 2 v.
 template <bool CODES>
 __global__ __launch_bounds__(512, 4) void swiglu_bwd_tile_kernel(const SwigluBwdArgs p, int col_tiles) {
-  __shared__ TileLds<3> L;
+  __shared__ TileLds<3, 4> L;
   const Tile t = tile_of(p.rows, p.ffn, col_tiles);
   const int tid = threadIdx.x, lane16 = tid & 15;
   const int64_t blocks = (p.ffn + 127) >> 7;
@@ -326,8 +326,8 @@ __global__ __launch_bounds__(512, 4) void swiglu_bwd_tile_kernel(const SwigluBwd
     float amax[8], scale[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      amax[k] = row16_max(absmax8(g[k]));
-      amax[4 + k] = row16_max(absmax8(u[k]));
+      amax[k] = row16_amax(g[k]);
+      amax[4 + k] = row16_amax(u[k]);
     }
     const float recip = row16_scales(amax, scale);
     uint8_t* const corner = o.q + t.rb * 128 * o.ld_q + t.cb * 128;

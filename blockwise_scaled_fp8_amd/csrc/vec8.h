@@ -3,6 +3,8 @@
 // layouts.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 
 namespace fp8bw {
@@ -53,11 +55,29 @@ __device__ __forceinline__ float absmax8(const float (&f)[8]) {
   return m;
 }
 
+// Largest of the 16 lanes of a DPP row, each holding the magnitude of its own 8
+// values (never a NaN: a maximum from 0 ignores them).  As integers, in the same
+// order: a float maximum of a value that came through a lane exchange takes three
+// instructions, this takes one.
+__device__ __forceinline__ float row16_amax(const float (&f)[8]) {
+  uint32_t m = __float_as_uint(absmax8(f));
+  auto step = [&](auto ctrl) {
+    m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, decltype(ctrl)::value, 0xF, 0xF, true));
+  };
+  step(std::integral_constant<int, 0xB1>{});    // quad_perm [1,0,3,2]
+  step(std::integral_constant<int, 0x4E>{});    // quad_perm [2,3,0,1]
+  step(std::integral_constant<int, 0x141>{});   // row_half_mirror
+  step(std::integral_constant<int, 0x140>{});   // row_mirror
+  return __uint_as_float(m);
+}
+
 // Four E4M3 codes of values scaled by their own block's scale.  These need no
 // clamp: |f| <= amax and s = 448 / max(amax, 1e-12) rounded give |f s| <= 448
 // (1 + 2^-23), and what lies between 448 and 464 rounds to 448.
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  int r;
+  asm("" : "=v"(r));   // any register: the two conversions write all of it
+  r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, r, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
 }
 // Eight E4M3 codes of f * s.
@@ -134,25 +154,29 @@ struct Pieces {
 
 // ---------------------------------------------------------------------------
 // Transposed codes of NA 128 x 128 tiles of fp32 values held by a workgroup of
-// 512 threads: thread (g = tid % 16, j = tid / 16) holds columns 8 g .. 8 g + 7
-// of rows 4 j .. 4 j + 3, so a wave's loads cover 256-byte pieces of 16 rows
-// and a 16-lane DPP row holds one 1x128 block of a row.
+// 2048 / R threads: thread (g = tid % 16, j = tid / 16) holds columns 8 g .. 8 g + 7
+// of rows R j .. R j + R - 1, so a wave's loads cover 256-byte pieces of 4 rows
+// and a 16-lane DPP row holds one 1x128 block of a row.  R = 8 spends the fewest
+// instructions beside those an element needs (these kernels are as near the VALU's
+// bound as HBM's); three arrays leave registers for R = 4 only.
 //
-// One scale per column: each column's 4 rows in registers, the 4 row quads of
-// a wave by two shuffles, the 8 waves through LDS.  A thread then quantizes
-// its 4 rows of a column into one dword of an LDS tile stored [column][row]
-// (32 dwords a column); dword d of column c lies at d ^ 4 ((c / 8) % 8), which
-// spreads a store's 16 column groups over the banks and keeps 16-byte groups
-// whole, and the tile leaves as 16-byte pieces of output rows, 8 lanes a row.
-template <int NA>
+// One scale per column: each column's R rows in registers, the 4 row groups of
+// a wave by lane exchange, the waves through LDS.  A thread then quantizes its
+// rows of a column into dwords of an LDS tile stored [column][row] (32 dwords a
+// column); dword d of column c lies at d ^ 4 ((c / 8) % 8), which spreads a
+// store's 16 column groups over the banks and keeps 16-byte groups whole, and the
+// tile leaves as 16-byte pieces of output rows, 8 lanes a row.
+template <int NA, int R>
 struct TileLds {
-  float red[8][NA][128];
-  float scale[NA][128];
+  static_assert(R == 4 || R == 8, "whole dwords of rows");
+  static constexpr int kWaves = 32 / R;
+  float red[kWaves][NA][128];
+  __attribute__((aligned(16))) float scale[NA][128];
   __attribute__((aligned(16))) uint32_t tile[NA][128 * 32];
 };
 
 // The column maxima of array a, into LDS.  Before the first barrier.  The wave's
-// four row quads are joined two columns at a time: exchanging halves (then 16-lane
+// four row groups are joined two columns at a time: exchanging halves (then 16-lane
 // rows) of two registers leaves in each lane pair one column's two values, so one
 // exchange and one maximum serve both columns, and every lane writes.
 __device__ __forceinline__ uint32_t max_halves(uint32_t x, uint32_t y) {
@@ -163,13 +187,17 @@ __device__ __forceinline__ uint32_t max_rows(uint32_t x, uint32_t y) {
   const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
   return max(r[0], r[1]);   // rows 0, 2: x's, rows 1, 3: y's
 }
-template <int NA>
-__device__ __forceinline__ void tile_column_max(TileLds<NA>& L, int a, const float (&v)[4][8]) {
+template <int NA, int R>
+__device__ __forceinline__ void tile_column_max(TileLds<NA, R>& L, int a, const float (&v)[R][8]) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   uint32_t m[8];   // as integers: magnitudes in the same order
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
-    m[c] = __float_as_uint(fmaxf(fmaxf(fabsf(v[0][c]), fabsf(v[1][c])), fmaxf(fabsf(v[2][c]), fabsf(v[3][c]))));
+  for (int c = 0; c < 8; ++c) {
+    float f = fmaxf(fmaxf(fabsf(v[0][c]), fabsf(v[1][c])), fmaxf(fabsf(v[2][c]), fabsf(v[3][c])));
+#pragma unroll
+    for (int k = 4; k < R; k += 2) f = fmaxf(f, fmaxf(fabsf(v[k][c]), fabsf(v[k + 1][c])));
+    m[c] = __float_as_uint(f);
+  }
   // 16-lane rows 0 .. 3 end with columns 0, 2, 1, 3 (and 4 further)
   const uint32_t lo = max_rows(max_halves(m[0], m[1]), max_halves(m[2], m[3]));
   const uint32_t hi = max_rows(max_halves(m[4], m[5]), max_halves(m[6], m[7]));
@@ -179,25 +207,32 @@ __device__ __forceinline__ void tile_column_max(TileLds<NA>& L, int a, const flo
 }
 
 // After a barrier: the scale of column c of array a, for one thread of each.
-template <int NA>
-__device__ __forceinline__ float tile_column_scale(TileLds<NA>& L, int a, int c) {
+template <int NA, int R>
+__device__ __forceinline__ float tile_column_scale(TileLds<NA, R>& L, int a, int c) {
   float m = 0.f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) m = fmaxf(m, L.red[w][a][c]);
+  for (int w = 0; w < TileLds<NA, R>::kWaves; ++w) m = fmaxf(m, L.red[w][a][c]);
   const float s = scale_from_amax(m);
   L.scale[a][c] = s;
   return s;
 }
 
 // After another: array a's codes, into LDS.
-template <int NA>
-__device__ __forceinline__ void tile_codes(TileLds<NA>& L, int a, const float (&v)[4][8]) {
+template <int NA, int R>
+__device__ __forceinline__ void tile_codes(TileLds<NA, R>& L, int a, const float (&v)[R][8]) {
   const int g = threadIdx.x & 15, j = threadIdx.x >> 4;
+  uint32_t* const column = &L.tile[a][8 * g * 32 + ((R / 4 * j) ^ (4 * (g & 7)))];
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     const float s = L.scale[a][8 * g + c];
-    L.tile[a][(8 * g + c) * 32 + (j ^ (4 * (g & 7)))] =
-        codes4(v[0][c] * s, v[1][c] * s, v[2][c] * s, v[3][c] * s);
+    u32x2 w;
+    w.x = codes4(v[0][c] * s, v[1][c] * s, v[2][c] * s, v[3][c] * s);
+    if constexpr (R == 8) {
+      w.y = codes4(v[4][c] * s, v[5][c] * s, v[6][c] * s, v[7][c] * s);
+      *(u32x2*)(column + 32 * c) = w;
+    } else {
+      column[32 * c] = w.x;
+    }
   }
 }
 
@@ -205,14 +240,15 @@ __device__ __forceinline__ void tile_codes(TileLds<NA>& L, int a, const float (&
 // transposed matrix whose rows 0 .. cols - 1 start at `corner` (rows % 16 == 0).
 // Nothing reads these codes before the backward or its weight gradient: they pass
 // the caches by.
-template <int NA>
-__device__ __forceinline__ void store_transposed(const TileLds<NA>& L, int a, uint8_t* corner, int64_t ld, int rows,
+template <int NA, int R>
+__device__ __forceinline__ void store_transposed(const TileLds<NA, R>& L, int a, uint8_t* corner, int64_t ld, int rows,
                                                  int cols) {
+  constexpr int kColumns = 256 / R;   // a pass
   const int oc = threadIdx.x >> 3, seg = threadIdx.x & 7;
   uint32_t at = oc * (uint32_t)ld + 16 * seg;
 #pragma unroll
-  for (int i = 0; i < 2; ++i, at += 64 * (uint32_t)ld) {
-    const int c = oc + 64 * i;
+  for (int i = 0; i < 128 / kColumns; ++i, at += kColumns * (uint32_t)ld) {
+    const int c = oc + kColumns * i;
     const u32x4 w = *(const u32x4*)&L.tile[a][c * 32 + ((4 * seg) ^ (4 * ((c >> 3) & 7)))];
     if (c < cols && 16 * seg < rows) __builtin_nontemporal_store(w, (u32x4*)(corner + at));
   }

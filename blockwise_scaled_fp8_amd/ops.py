@@ -821,9 +821,15 @@ class SwigluGrads(NamedTuple):
     act_recip_t: Optional[torch.Tensor]  # fp32 [ffn, ceil(rows / 128)], column-major
 
 
+def _matrix_empty(rows, cols, dtype, device):
+    # empty_strided costs 1.4 us, torch.empty 1.75: of a decoding step's calls, each
+    # about 10 us on the host, that is what can be spared
+    return torch.empty_strided((rows, cols), (max(cols, 1), 1), dtype=dtype, device=device)
+
+
 def _codes_empty(rows, cols, blocks, device):
     """(codes [rows, cols], column-major scales [rows, blocks])."""
-    return (torch.empty((rows, cols), dtype=torch.uint8, device=device),
+    return (_matrix_empty(rows, cols, torch.uint8, device),
             torch.empty_strided((rows, blocks), (1, max(rows, 1)), dtype=torch.float32, device=device))
 
 
@@ -831,7 +837,7 @@ def _layouts_empty(rows, cols, blocks, y, q, qt, device):
     """(Rows, the C struct that names its tensors)."""
     ty = tq = tr = tqt = trt = None
     if y:
-        ty = torch.empty((rows, cols), dtype=torch.bfloat16, device=device)
+        ty = _matrix_empty(rows, cols, torch.bfloat16, device)
     if q:
         tq, tr = _codes_empty(rows, cols, blocks, device)
     if qt:
@@ -843,8 +849,9 @@ def _layouts_empty(rows, cols, blocks, y, q, qt, device):
 def _moe_table(table, device):
     """(tokens, topk, rows) of a table on `device`."""
     row, source, group_end = table
+    index = device.index
     for t, dim, name in ((row, 2, "row"), (source, 1, "source"), (group_end, 1, "group_end")):
-        if t.dtype != torch.int32 or t.dim() != dim or not t.is_contiguous() or t.device != device:
+        if t.dtype != torch.int32 or t.dim() != dim or t.get_device() != index or not t.is_contiguous():
             raise ValueError(f"the table's {name} must be a contiguous int32 tensor of {dim} dimension"
                              f"{'s' if dim > 1 else ''} on {device}")
     return row.shape[0], row.shape[1], source.shape[0]
@@ -876,9 +883,9 @@ def moe_sort(expert, experts, align=128):
     experts, align = int(experts), int(align)
     rows = lib.fp8bw_moe_rows(tokens, topk, experts, align)
     dev = expert.device
-    row = torch.empty((tokens, topk), dtype=torch.int32, device=dev)
-    source = torch.empty(rows, dtype=torch.int32, device=dev)
-    group_end = torch.empty(max(experts, 0), dtype=torch.int32, device=dev)
+    row = _matrix_empty(tokens, topk, torch.int32, dev)
+    source = torch.empty_strided((rows,), (1,), dtype=torch.int32, device=dev)
+    group_end = torch.empty_strided((max(experts, 0),), (1,), dtype=torch.int32, device=dev)
     nws = lib.fp8bw_moe_sort_ws_bytes(tokens, topk, experts)
     ws = torch.empty(nws, dtype=torch.uint8, device=dev) if nws else None
     check(lib.fp8bw_moe_sort(expert.data_ptr(), 32 if expert.dtype == torch.int32 else 64, tokens, topk,
@@ -896,10 +903,12 @@ def moe_gather(x, table, y=True, q=False, qt=False):
     lib = load_library()
     _need_cuda(x)
     _bf16_matrix(x, "x")
-    tokens, topk, rows = _moe_table(table, x.device)
+    dev = x.device
+    tokens, topk, rows = _moe_table(table, dev)
     cols = x.shape[1]
-    _check_shape(x, (tokens, cols), "x")
-    out, c = _layouts_empty(rows, cols, _cdiv(cols, 128), y, q, qt, x.device)
+    if x.shape[0] != tokens:
+        _check_shape(x, (tokens, cols), "x")
+    out, c = _layouts_empty(rows, cols, _cdiv(cols, 128), y, q, qt, dev)
     check(lib.fp8bw_moe_gather(x.data_ptr(), x.stride(0), tokens, topk, table.row.data_ptr(),
                                table.source.data_ptr(), rows, cols, c, _stream(x)))
     return out
@@ -917,7 +926,7 @@ def moe_combine(y, table, weight=None):
     _check_shape(y, (rows, cols), "y")
     if weight is not None:
         _moe_weight(weight, tokens, topk)
-    out = torch.empty((tokens, cols), dtype=torch.bfloat16, device=y.device)
+    out = _matrix_empty(tokens, cols, torch.bfloat16, y.device)
     check(lib.fp8bw_moe_combine(y.data_ptr(), y.stride(0), _ptr(weight),
                                 1 if weight is None else OUT_DTYPES[weight.dtype], tokens, topk,
                                 table.row.data_ptr(), rows, cols, out.data_ptr(), out.stride(0), _stream(y)))

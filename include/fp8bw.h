@@ -624,7 +624,8 @@ typedef struct {
  *
  * All three: cols % 16 == 0, cols <= 65536, tokens < 2^24, rows < 2^27, and fewer than
  * 2^26 pieces of 512 columns of tokens and 2^23 tiles of 128 rows x 128 columns.
- * rows >= 1 if tokens >= 1, and no rows without tokens.
+ * rows >= 1 if tokens >= 1, and no rows without tokens.  Transposed codes need rows
+ * % 16 == 0, y's leading dimension below 2^22 and those of codes below 2^24.
  */
 int fp8bw_moe_gather(const void* x, int64_t ld_x, int64_t tokens, int64_t topk, const int32_t* row,
                      const int32_t* source, int64_t rows, int64_t cols, const fp8bw_layouts* out,

@@ -207,3 +207,36 @@ def test_infinities_and_nan_stay_with_their_tokens(gpu):
     out = fp8.moe_combine(y, t)
     assert out[0].isfinite().all() and out[3].isfinite().all()
     assert out[1, 3] == float("inf") and out[1, 4].isnan() and out[2, 5] == -float("inf")
+
+
+def _check_against_quantizer(t, x, o, weight=None):
+    """Every layout of a gather equals the quantizers' of the gathered rows."""
+    has = t.source >= 0
+    slot = t.source.clamp(min=0).long()
+    v = torch.where(has[:, None], x[slot // t.row.shape[1]], 0.0)
+    if weight is not None:
+        return v.float() * weight.reshape(-1)[slot][:, None] * has[:, None]
+    q, recip = fp8.fp8_blockwise_quant(v)
+    qt, recip_t = fp8.fp8_blockwise_quant(v, transpose=True)
+    assert torch.equal(o.q, q) and torch.equal(o.recip, recip)
+    assert torch.equal(o.qt, qt) and torch.equal(o.recip_t, recip_t)
+    return v
+
+
+# many row blocks: even, skewed, empty and single-block experts, one expert, more
+# experts than a wave has lanes, unaligned ends
+@pytest.mark.parametrize("tokens, topk, experts, align, skew", [
+    (4500, 2, 16, 128, 0.0), (4500, 2, 7, 128, 0.8), (3000, 3, 65, 128, 0.5), (9000, 2, 1, 128, 0.0),
+    (1100, 8, 256, 128, 0.3), (1100, 8, 300, 128, 0.0), (4160, 2, 5, 1, 0.4), (16640, 2, 16, 128, 0.2)])
+def test_gather_of_many_row_blocks(gpu, tokens, topk, experts, align, skew):
+    expert = _experts(tokens, topk, experts, 20, 0.05, skew)
+    t = _table(gpu, expert, experts, align)
+    x = _matrix(gpu, tokens, 1168, 21)
+    say("moe_gather, many blocks", tokens, topk, experts, align)
+    o = fp8.moe_gather(x, t, y=True, q=True, qt=True)
+    v = _check_against_quantizer(t, x, o)
+    assert torch.equal(o.y, v)
+    w = torch.rand(tokens, topk, generator=torch.Generator().manual_seed(22)).to(gpu)
+    y = _matrix(gpu, t.source.shape[0], 1168, 23)
+    o, dw = fp8.moe_combine_bwd(x, y, t, w, q=True, qt=True)
+    assert torch.equal(o.y, _check_against_quantizer(t, x, o, w).bfloat16())

@@ -206,3 +206,25 @@ def test_grouped_wgrad_workspace(lib):
                 ws=P, ws_bytes=need)
     for want, kw in ((WS, dict(ws=None)), (WS, dict(ws_bytes=need - 1)), (ALIGN, dict(ws=P + 128))):
         _check(lib, "fp8_scaled_grouped_gemm_blockwise_wgrad", long, want, kw)
+
+
+# A tile of transposed codes is addressed in 32 bits from its corner.
+WIDE = [(LAYOUT, dict(qt=P, recip_t=P, ld_y=1 << 22)), (LAYOUT, dict(qt=P, recip_t=P, q=P, recip=P, ld_q=1 << 24)),
+        (LAYOUT, dict(qt=P, recip_t=P, ld_qt=1 << 24))]
+
+
+@pytest.mark.parametrize("want, kw", WIDE)
+def test_strides_of_transposed_tiles(lib, want, kw):
+    _check(lib, "fp8bw_moe_gather", GATHER, want, dict(out=_layouts(**kw)))
+    _check(lib, "fp8bw_moe_combine_bwd", COMBINE_BWD, want, dict(dy=_layouts(**kw), dweight=None))
+    wide = dict(ld_y=512, ld_q=512, rst_kb=512)
+    _check(lib, "fp8bw_swiglu_bwd", SWIGLU_BWD, want, dict(dh=_layouts(**{**wide, **kw})))
+
+
+def test_strides_of_read_tiles(lib):
+    qt = _layouts(qt=P, recip_t=P)
+    _check(lib, "fp8bw_swiglu_fwd", SWIGLU_FWD, LAYOUT, dict(ld_h=1 << 22, out=qt))
+    qt = _layouts(qt=P, recip_t=P, ld_y=512, ld_q=512, rst_kb=512)
+    for kw in (dict(ld_h=1 << 22), dict(ld_dy=1 << 22), dict(ld_h=1 << 24, h_recip=P), dict(hr_row=1 << 22, hr_kb=1, h_recip=P),
+               dict(act_qt=P, act_recip_t=P, ld_act_qt=1 << 24)):
+        _check(lib, "fp8bw_swiglu_bwd", SWIGLU_BWD, LAYOUT, dict(dh=qt, **kw))
