@@ -1862,6 +1862,14 @@ hipError_t launch_grouped_gemm(const GemmProblem& p, int groups, const int* grou
 // last; within a group as everywhere (tile_to_mn).  Roles as in a persistent
 // launch: waves 0 and 1 issue the direct loads and wait for them, the others
 // store, and nothing waits for stores.
+//
+// Measured: 33280 tokens, 16 groups of 8192 x 5120: 1490 to 1550 us, 1.8 to 1.87
+// PFLOP/s (the dense product of this recipe 2.14); 9001 tokens, 16 groups of
+// 1360 x 2064, three empty: 60 us.  Bound by the vector pipe in the K loop, 2.0 us a
+// block, and by 5 us a tile behind it: without the epilogue 1341 us, without its
+// stores 1453.  An epilogue that stages each wave's values in 2 KB of its own, with
+// no barrier and two blocks loaded ahead of the stores, leaves 0.5 us beside the
+// stores but these then hold up the loads behind them: 1480 to 1487 us.
 constexpr int kStreamGroups = 1024;
 
 struct WgradTile {
