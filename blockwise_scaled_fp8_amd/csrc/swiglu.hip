@@ -70,22 +70,37 @@ __device__ __forceinline__ void half_values(const HalfIn& x, float (&f)[8]) {
 }
 
 // ---------------------------------------------------------------------------
-// Rows: a wave takes P pieces of 512 columns of a row of v, all loads in flight
+// Rows: a wave takes a piece of 512 columns of P rows of v, all loads in flight
 // first; a 16-lane DPP row holds one 1x128 block of each half, and the three scales
-// of v, g and u are divided by three of its lanes at once.  HBM: codes and
-// checkpoint of 33280 rows of 2 x 5120, 212 us for 1.21 GB (5.7 TB/s; with a
-// division in every lane 250); 8 rows of 2 x 8192 2.7 us, the launch.
+// of v, g and u are divided by three of its lanes at once.  A workgroup's 4 P rows
+// follow one another, so that their scales, which lie row by row, leave in whole
+// 32-byte sectors (with the pieces of a row side by side instead 98 MB more are
+// written of 527, and 211 us against 204).  HBM: codes and checkpoint of 33280 rows
+// of 2 x 5120, 204 us for 1.21 GB (5.9 TB/s); 8 rows of 2 x 8192 2.7 us, the launch.
+template <int P>
+struct RowPieces {
+  int row[P];
+  int col;   // first column
+  __device__ __forceinline__ RowPieces(uint32_t workgroup, uint32_t pieces) {
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t r = workgroup / pieces;
+    col = (int)(workgroup - r * pieces) * 512;
+#pragma unroll
+    for (int k = 0; k < P; ++k) row[k] = (int)((4 * r + wave) * P) + k;
+  }
+};
+
 template <int P>
 __global__ __launch_bounds__(256) void swiglu_fwd_rows_kernel(const SwigluFwdArgs p, uint32_t pieces) {
   const int lane = threadIdx.x & 63;
-  const Pieces<P> at(blockIdx.x, pieces);
+  const RowPieces<P> at(blockIdx.x, pieces);
   HalfIn gate[P], up[P];
   int64_t row[P], col[P];
   bool in[P];
 #pragma unroll
   for (int k = 0; k < P; ++k) {
     row[k] = at.row[k];
-    col[k] = at.col[k] + lane * 8;
+    col[k] = at.col + lane * 8;
     in[k] = row[k] < p.rows && col[k] < p.ffn;
     gate[k] = load_half<false>(p.h, p.ld_h, nullptr, 0, 0, p.ffn, row[k], col[k], 0, in[k]);
     up[k] = load_half<false>(p.h, p.ld_h, nullptr, 0, 0, p.ffn, row[k], col[k], 1, in[k]);
@@ -135,7 +150,7 @@ __device__ __forceinline__ void swiglu_grad(float& g, float& u, float& d) {
 template <int P, bool CODES>
 __global__ __launch_bounds__(256) void swiglu_bwd_rows_kernel(const SwigluBwdArgs p, uint32_t pieces) {
   const int lane = threadIdx.x & 63;
-  const Pieces<P> at(blockIdx.x, pieces);
+  const RowPieces<P> at(blockIdx.x, pieces);
   HalfIn gate[P], up[P];
   uint4 dy[P];
   int64_t row[P], col[P];
@@ -143,7 +158,7 @@ __global__ __launch_bounds__(256) void swiglu_bwd_rows_kernel(const SwigluBwdArg
 #pragma unroll
   for (int k = 0; k < P; ++k) {
     row[k] = at.row[k];
-    col[k] = at.col[k] + lane * 8;
+    col[k] = at.col + lane * 8;
     in[k] = row[k] < p.rows && col[k] < p.ffn;
     dy[k] = load_stream(p.dy + (in[k] ? row[k] * p.ld_dy + col[k] : 0));
     gate[k] = load_half<CODES>(p.h, p.ld_h, p.h_recip, p.hr_row, p.hr_kb, p.ffn, row[k], col[k], 0, in[k]);
@@ -373,11 +388,15 @@ __global__ __launch_bounds__(512, 4) void swiglu_bwd_tile_kernel(const SwigluBwd
     store_transposed(L, 2, p.act_qt + t.cb * 128 * p.ld_act_qt + t.rb * 128, p.ld_act_qt, t.rows, t.cols);
 }
 
-// Two pieces a wave once that still leaves several workgroups per compute unit
-// (forward, 33280 rows of 2 x 5120 with a checkpoint: 254 us with one, 233 with
-// two, 245 with four, 251 with eight).
+// Two rows a wave once that still leaves several workgroups per compute unit
+// (forward, 33280 rows of 2 x 5120 with a checkpoint: 204 us with two, 207 with
+// four, 224 with one and as many rows a workgroup as with four).
 constexpr int64_t kManyPieces = 8192;
-constexpr int kPieces = 2;
+constexpr int kRows = 2;
+
+static dim3 rows_grid(int64_t rows, int64_t pieces, int each) {
+  return dim3((unsigned)((rows + 4 * each - 1) / (4 * each) * pieces));
+}
 
 hipError_t launch_swiglu_fwd(const SwigluFwdArgs& p, hipStream_t stream) {
   if (p.out.qt) {
@@ -385,11 +404,11 @@ hipError_t launch_swiglu_fwd(const SwigluFwdArgs& p, hipStream_t stream) {
     hipLaunchKernelGGL(swiglu_fwd_tile_kernel, dim3((unsigned)tiles), dim3(512), 0, stream, p, (int)ct);
     return hipGetLastError();
   }
-  const int64_t pieces = (p.ffn + 511) / 512, items = p.rows * pieces;
-  if (items >= kManyPieces)
-    hipLaunchKernelGGL(swiglu_fwd_rows_kernel<kPieces>, dim3((unsigned)((items + 4 * kPieces - 1) / (4 * kPieces))), dim3(256), 0, stream, p, (uint32_t)pieces);
+  const int64_t pieces = (p.ffn + 511) / 512;
+  if (p.rows * pieces >= kManyPieces)
+    hipLaunchKernelGGL(swiglu_fwd_rows_kernel<kRows>, rows_grid(p.rows, pieces, kRows), dim3(256), 0, stream, p, (uint32_t)pieces);
   else
-    hipLaunchKernelGGL(swiglu_fwd_rows_kernel<1>, dim3((unsigned)((items + 3) / 4)), dim3(256), 0, stream, p, (uint32_t)pieces);
+    hipLaunchKernelGGL(swiglu_fwd_rows_kernel<1>, rows_grid(p.rows, pieces, 1), dim3(256), 0, stream, p, (uint32_t)pieces);
   return hipGetLastError();
 }
 
@@ -402,15 +421,15 @@ hipError_t launch_swiglu_bwd(const SwigluBwdArgs& p, hipStream_t stream) {
       hipLaunchKernelGGL(swiglu_bwd_tile_kernel<false>, dim3((unsigned)tiles), dim3(512), 0, stream, p, (int)ct);
     return hipGetLastError();
   }
-  const int64_t pieces = (p.ffn + 511) / 512, items = p.rows * pieces;
-  const bool many = items >= kManyPieces;
-  const dim3 grid((unsigned)(many ? (items + 4 * kPieces - 1) / (4 * kPieces) : (items + 3) / 4));
-#define FP8BW_K(P, C) hipLaunchKernelGGL((swiglu_bwd_rows_kernel<P, C>), grid, dim3(256), 0, stream, p, (uint32_t)pieces)
+  const int64_t pieces = (p.ffn + 511) / 512;
+  const bool many = p.rows * pieces >= kManyPieces;
+#define FP8BW_K(P, C) \
+  hipLaunchKernelGGL((swiglu_bwd_rows_kernel<P, C>), rows_grid(p.rows, pieces, P), dim3(256), 0, stream, p, (uint32_t)pieces)
   if (p.h_recip) {
-    if (many) FP8BW_K(kPieces, true);
+    if (many) FP8BW_K(kRows, true);
     else FP8BW_K(1, true);
   } else {
-    if (many) FP8BW_K(kPieces, false);
+    if (many) FP8BW_K(kRows, false);
     else FP8BW_K(1, false);
   }
 #undef FP8BW_K
