@@ -766,7 +766,9 @@ class Float8BlockwiseMoE(torch.nn.Module):
 
     The forward keeps the sorted rows' transposed codes, the experts' first
     products as 8-bit checkpoints and, for the router's gradient, their outputs
-    in bf16."""
+    in bf16.  The weights are quantized in every call.  A step may be captured into
+    a graph, routing included, while no earlier autograd graph of its parameters
+    is alive."""
 
     def __init__(self, hidden, ffn, experts, device=None):
         super().__init__()

@@ -195,3 +195,31 @@ def test_a_tokens_nan_stays_with_it(gpu):
     for t in (x, bad):
         m(t, expert, weight).backward(torch.ones_like(x))
     assert torch.equal(x.grad[clean], bad.grad[clean])
+
+
+# enough slots that every workgroup takes several parts of its run
+@pytest.mark.parametrize("tokens, topk, experts, align, wide", [
+    ((1 << 22) + 5, 8, 1000, 128, True), ((1 << 23) + 1, 4, 3, 1, False), ((1 << 24) - 1, 1, 40, 128, True),
+    (300001, 2, 600, 48, False)])
+def test_sort_of_many_slots(gpu, tokens, topk, experts, align, wide):
+    g = torch.Generator(device=gpu)
+    g.manual_seed(tokens)
+    dtype = torch.int64 if wide else torch.int32
+    e = torch.randint(-1, experts + 1, (tokens, topk), device=gpu, generator=g, dtype=dtype)   # some are none
+    say("moe_sort", tokens, topk, experts, align)
+    t = fp8.moe_sort(e, experts, align)
+    flat = e.flatten().long()
+    has = (flat >= 0) & (flat < experts)
+    n = torch.bincount(flat[has], minlength=experts)
+    padded = (n + align - 1) // align * align
+    end = padded.cumsum(0)
+    assert torch.equal(t.group_end.long(), end)
+    order = torch.sort(torch.where(has, flat, experts), stable=True).indices[:int(n.sum())]
+    chosen = flat[order]
+    place = torch.arange(order.numel(), device=gpu) - (n.cumsum(0) - n)[chosen] + (end - padded)[chosen]
+    row = torch.full_like(flat, -1)
+    row[order] = place
+    assert torch.equal(t.row.flatten().long(), row)
+    source = torch.full((t.source.numel(),), -1, dtype=torch.int64, device=gpu)
+    source[place] = order
+    assert torch.equal(t.source.long(), source)
