@@ -193,9 +193,10 @@ __device__ __forceinline__ void tile_column_max(TileLds<NA, R>& L, int a, const 
   uint32_t m[8];   // as integers: magnitudes in the same order
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    float f = fmaxf(fmaxf(fabsf(v[0][c]), fabsf(v[1][c])), fmaxf(fabsf(v[2][c]), fabsf(v[3][c])));
+    // from 0, which ignores NaN: one left here would pass every magnitude below
+    float f = 0.f;
 #pragma unroll
-    for (int k = 4; k < R; k += 2) f = fmaxf(f, fmaxf(fabsf(v[k][c]), fabsf(v[k + 1][c])));
+    for (int k = 0; k < R; ++k) f = fmaxf(f, fabsf(v[k][c]));
     m[c] = __float_as_uint(f);
   }
   // 16-lane rows 0 .. 3 end with columns 0, 2, 1, 3 (and 4 further)
