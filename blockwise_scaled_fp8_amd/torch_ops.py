@@ -522,9 +522,16 @@ def moe_sort(expert: torch.Tensor, experts: int,
     return tuple(ops.moe_sort(expert.contiguous(), experts, align))
 
 
+def _moe_rows(tokens, topk, experts, align):
+    """ops.moe_rows of sizes within its limits, which may be symbolic."""
+    n = tokens * topk
+    filled = torch.sym_min(experts, n)
+    return align * (filled + (n - filled) // align)
+
+
 @moe_sort.register_fake
 def _moe_sort_fake(expert, experts, align):
-    rows = ops.moe_rows(expert.shape[0], expert.shape[1], experts, align)
+    rows = _moe_rows(expert.shape[0], expert.shape[1], experts, align)
     return tuple(expert.new_empty(shape, dtype=torch.int32) for shape in (expert.shape, (rows,), (experts,)))
 
 
@@ -689,7 +696,7 @@ def moe_fwd(x: torch.Tensor, expert: torch.Tensor, weight: torch.Tensor, w13: to
 def _moe_fwd_fake(x, expert, weight, w13, w2, align, keep_x, keep_h, keep_y):
     _check_2d_bf16(x)
     (E, _, H), F = w13.shape, w2.shape[2]
-    R = ops.moe_rows(expert.shape[0], expert.shape[1], E, align)
+    R = _moe_rows(expert.shape[0], expert.shape[1], E, align)
 
     def codes(keep, rows, cols, blocks):
         if not keep:
