@@ -619,7 +619,7 @@ def moe_join(y, table, weight=None):
     bf16, as many as the table has slots) if given, summed; differentiable in y
     and weight."""
     if weight is not None:
-        weight = weight.reshape(table.row.shape)
+        weight = weight.reshape(table[0].shape)
     return _MoeJoin.apply(y, weight, *table)
 
 
