@@ -243,7 +243,8 @@ hipError_t launch_moe_combine(const MoeCombineArgs& p, hipStream_t stream);
 // ---- gated activation (swiglu.hip) ----
 struct SwigluFwdArgs {
   int64_t rows, ffn;
-  const uint16_t* h; int64_t ld_h;                                // [rows, 2 ffn]
+  const void* h; int64_t ld_h;                                    // [rows, 2 ffn]: bf16, or with in_recip codes
+  const float* in_recip; int64_t ir_row, ir_kb;                   // (codes: out.qt alone)
   LayoutsOut out;                                                 // [rows, ffn]
   uint8_t* hq; int64_t ld_hq; float* h_recip; int64_t hr_row, hr_kb;   // codes of h or nullptr
 };

@@ -237,7 +237,7 @@ FP8BW_API int fp8bw_swiglu_fwd(const void* h, int64_t ld_h, int64_t rows, int64_
   if (!out->y && !out->q && !out->qt && !hq) return ok();
   fp8bw::SwigluFwdArgs p = {};
   p.rows = rows; p.ffn = ffn;
-  p.h = (const uint16_t*)h; p.ld_h = used_stride(rows, ld_h);
+  p.h = h; p.ld_h = used_stride(rows, ld_h);
   p.out = layouts(*out, rows, ffn, blocks);
   p.hq = (uint8_t*)hq; p.ld_hq = used_stride(rows, ld_hq);
   p.h_recip = h_recip; p.hr_row = used_stride(rows, hr_row); p.hr_kb = hr_kb;
@@ -253,7 +253,9 @@ FP8BW_API int fp8bw_swiglu_bwd(const void* dy, int64_t ld_dy, const void* h, int
   if (st != FP8BW_OK) return st;
   if (rows == 0 || ffn == 0) return ok();
   const int64_t blocks = cdiv(ffn, 128);
-  if ((st = check_bf16(dy, rows, ffn, ld_dy, "dy")) != FP8BW_OK) return st;
+  // (without an output of dh nothing reads dy)
+  const bool grads = dh && (dh->y || dh->q || dh->qt);
+  if ((dy || grads) && (st = check_bf16(dy, rows, ffn, ld_dy, "dy")) != FP8BW_OK) return st;
   if (h_recip) {
     if (!h) return fail(FP8BW_ERR_NULL, "h must be non-null");
     st = check_codes(h, rows, 2 * ffn, ld_h, h_recip, hr_row, hr_kb, "h", 2 * blocks);
@@ -266,7 +268,7 @@ FP8BW_API int fp8bw_swiglu_bwd(const void* dy, int64_t ld_dy, const void* h, int
     if (rows % 16) return fail(FP8BW_ERR_SHAPE, "transposed codes need rows %% 16 == 0 (rows=%lld)", (long long)rows);
     if ((st = check_codes(act_qt, ffn, rows, ld_act_qt, act_recip_t, art_row, art_kb, "act_qt")) != FP8BW_OK) return st;
   }
-  if (!dh->y && !dh->q && !dh->qt && !act_qt) return ok();
+  if (!grads && !act_qt) return ok();
   fp8bw::SwigluBwdArgs p = {};
   p.rows = rows; p.ffn = ffn;
   p.dy = (const uint16_t*)dy; p.ld_dy = used_stride(rows, ld_dy);
@@ -276,7 +278,7 @@ FP8BW_API int fp8bw_swiglu_bwd(const void* dy, int64_t ld_dy, const void* h, int
   p.act_qt = (uint8_t*)act_qt; p.ld_act_qt = ld_act_qt;
   p.act_recip_t = act_recip_t; p.art_row = art_row; p.art_kb = used_stride(cdiv(rows, 128), art_kb);
   if ((p.dh.qt || act_qt) &&
-      (st = check_tile_strides({p.ld_dy, h_recip ? 0 : p.ld_h, h_recip ? p.hr_row : 0, p.dh.y ? p.dh.ld_y : 0},
+      (st = check_tile_strides({grads ? p.ld_dy : 0, h_recip ? 0 : p.ld_h, h_recip ? p.hr_row : 0, p.dh.y ? p.dh.ld_y : 0},
                                {h_recip ? p.ld_h : 0, p.dh.q ? p.dh.ld_q : 0, p.dh.qt ? p.dh.ld_qt : 0,
                                 act_qt ? ld_act_qt : 0})) != FP8BW_OK)
     return st;

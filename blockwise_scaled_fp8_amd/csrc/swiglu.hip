@@ -252,6 +252,7 @@ __device__ __forceinline__ void load_tile_halves(const Tile& t, const void* h, i
   }
 }
 
+template <bool CODES>
 __global__ __launch_bounds__(512, 4) void swiglu_fwd_tile_kernel(const SwigluFwdArgs p, int col_tiles) {
   __shared__ TileLds<1, 4> L;
   const Tile t = tile_of(p.rows, p.ffn, col_tiles);
@@ -259,17 +260,18 @@ __global__ __launch_bounds__(512, 4) void swiglu_fwd_tile_kernel(const SwigluFwd
   const int64_t blocks = (p.ffn + 127) >> 7;
   const LayoutsOut& o = p.out;
   HalfIn gate[4], up[4];
-  load_tile_halves<false>(t, p.h, p.ld_h, nullptr, 0, 0, p.ffn, gate, up);
+  load_tile_halves<CODES>(t, p.h, p.ld_h, p.in_recip, p.ir_row, p.ir_kb, p.ffn, gate, up);
   float v[4][8];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int64_t r = t.rb * 128 + t.row + k;
     const bool row_in = t.row + k < t.rows, in = row_in && t.col < t.cols;
     float g[8], u[8];
-    half_values<false>(gate[k], g);
-    half_values<false>(up[k], u);
+    half_values<CODES>(gate[k], g);
+    half_values<CODES>(up[k], u);
 #pragma unroll
     for (int c = 0; c < 8; ++c) v[k][c] = g[c] * sigmoid(g[c]) * u[c];
+    if constexpr (CODES) continue;
     const int64_t col = t.cb * 128 + t.col;
     if (o.y && in) *(uint4*)(o.y + r * o.ld_y + col) = pack8(v[k]);
     if (!o.q && !p.hq) continue;
@@ -401,7 +403,10 @@ static dim3 rows_grid(int64_t rows, int64_t pieces, int each) {
 hipError_t launch_swiglu_fwd(const SwigluFwdArgs& p, hipStream_t stream) {
   if (p.out.qt) {
     const int64_t ct = (p.ffn + 127) / 128, tiles = ct * ((p.rows + 127) / 128);
-    hipLaunchKernelGGL(swiglu_fwd_tile_kernel, dim3((unsigned)tiles), dim3(512), 0, stream, p, (int)ct);
+    if (p.in_recip)
+      hipLaunchKernelGGL(swiglu_fwd_tile_kernel<true>, dim3((unsigned)tiles), dim3(512), 0, stream, p, (int)ct);
+    else
+      hipLaunchKernelGGL(swiglu_fwd_tile_kernel<false>, dim3((unsigned)tiles), dim3(512), 0, stream, p, (int)ct);
     return hipGetLastError();
   }
   const int64_t pieces = (p.ffn + 511) / 512;
@@ -413,6 +418,17 @@ hipError_t launch_swiglu_fwd(const SwigluFwdArgs& p, hipStream_t stream) {
 }
 
 hipError_t launch_swiglu_bwd(const SwigluBwdArgs& p, hipStream_t stream) {
+  // v^T alone: no gradient is computed and dy is not read (33280 rows of 2 x 5120: from a
+  // checkpoint 108 us, from bf16 160).
+  if (!p.dh.y && !p.dh.q && !p.dh.qt) {
+    SwigluFwdArgs f = {};
+    f.rows = p.rows; f.ffn = p.ffn;
+    f.h = p.h; f.ld_h = p.ld_h;
+    f.in_recip = p.h_recip; f.ir_row = p.hr_row; f.ir_kb = p.hr_kb;
+    f.out.qt = p.act_qt; f.out.ld_qt = p.ld_act_qt;
+    f.out.recip_t = p.act_recip_t; f.out.rst_row = p.art_row; f.out.rst_kb = p.art_kb;
+    return launch_swiglu_fwd(f, stream);
+  }
   if (p.dh.qt || p.act_qt) {
     const int64_t ct = (p.ffn + 127) / 128, tiles = ct * ((p.rows + 127) / 128);
     if (p.h_recip)

@@ -994,24 +994,31 @@ def swiglu_bwd(dy, h, h_recip=None, dh=True, q=False, qt=False, act_qt=False):
 
     dh, q, qt choose the layouts of the gradient of h (q in 1x128 blocks of each
     half); act_qt makes the activation's transposed codes again, the operand of
-    the weight gradient of the product behind it."""
+    the weight gradient of the product behind it.  For act_qt alone dy is not
+    read and may be None."""
     lib = load_library()
-    _need_cuda(dy, h)
-    _bf16_matrix(dy, "dy")
-    rows, ffn = dy.shape
+    if dy is None and not (dh or q or qt):
+        _need_cuda(h)
+        if h.dim() != 2:
+            raise ValueError("h must be a 2-D tensor")
+        rows, ffn = h.shape[0], _halves(h, "h")
+    else:
+        _need_cuda(dy, h)
+        _bf16_matrix(dy, "dy")
+        rows, ffn = dy.shape
     if h_recip is None:
         _bf16_matrix(h, "h", (rows, 2 * ffn))
     else:
         _check_codes_out(h, (rows, 2 * ffn), "h")
         _check_scales(h_recip, (rows, 2 * _cdiv(ffn, 128)), "h_recip")
-    out, c = _layouts_empty(rows, 2 * ffn, 2 * _cdiv(ffn, 128), dh, q, qt, dy.device)
+    out, c = _layouts_empty(rows, 2 * ffn, 2 * _cdiv(ffn, 128), dh, q, qt, h.device)
     tq = tr = None
     if act_qt:
-        tq, tr = _codes_empty(ffn, rows, _cdiv(rows, 128), dy.device)
-    check(lib.fp8bw_swiglu_bwd(dy.data_ptr(), dy.stride(0), h.data_ptr(), h.stride(0), _ptr(h_recip),
+        tq, tr = _codes_empty(ffn, rows, _cdiv(rows, 128), h.device)
+    check(lib.fp8bw_swiglu_bwd(_ptr(dy), 0 if dy is None else dy.stride(0), h.data_ptr(), h.stride(0), _ptr(h_recip),
                                0 if h_recip is None else h_recip.stride(0),
                                0 if h_recip is None else h_recip.stride(1), rows, ffn, c, _ptr(tq), rows,
-                               _ptr(tr), 1, ffn, _stream(dy)))
+                               _ptr(tr), 1, ffn, _stream(h)))
     return SwigluGrads(*out, tq, tr)
 
 

@@ -714,15 +714,18 @@ def moe_bwd(dout: torch.Tensor, row: torch.Tensor, source: torch.Tensor, group_e
             need_dw13: bool, need_dw2: bool) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
     """(dx, dweight, dW13, dW2) of moe_fwd; one not asked for comes back empty.
     Every product is an FP8 one: the joined gradient and the activation's are
-    quantized into both layouts by the kernels that make them."""
+    quantized into both layouts by the kernels that make them.  dW2 alone needs
+    the activation but not its gradient."""
     table = ops.MoeTable(row, source, group_end)
     through = need_dx or need_dw13
     dy, dweight = ops.moe_combine_bwd(_aligned(dout), y if need_dweight else None, table, weight.contiguous(), dy=False,
-                                      q=through or need_dw2, qt=need_dw2, need_dweight=need_dweight)
+                                      q=through, qt=need_dw2, need_dweight=need_dweight)
     dx = dw13 = dw2 = None
     if through or need_dw2:
-        da = ops.fp8_scaled_grouped_gemm_blockwise(dy.q, dy.recip, *ops.fp8_blockwise_quant_grouped(w2, transpose=True),
-                                                   group_end)
+        da = None
+        if through:
+            da = ops.fp8_scaled_grouped_gemm_blockwise(
+                dy.q, dy.recip, *ops.fp8_blockwise_quant_grouped(w2, transpose=True), group_end)
         g = ops.swiglu_bwd(da, hq, h_recip, dh=False, q=need_dx, qt=need_dw13, act_qt=need_dw2)
     if need_dw2:
         dw2 = ops.fp8_scaled_grouped_gemm_blockwise_wgrad(dy.qt, dy.recip_t, g.act_qt, g.act_recip_t, group_end)

@@ -651,7 +651,7 @@ int fp8bw_moe_combine_bwd(const void* dout, int64_t ld_dout, const void* y, int6
  * fp8bw_swiglu_bwd -- its gradient, with s = sigmoid(g):
  *   dg = dy * u * s * (1 + g * (1 - s)),  du = dy * g * s
  *
- *   dy   device bf16 [rows, ffn].
+ *   dy   device bf16 [rows, ffn]; not read, and may be NULL, if dh asks for nothing.
  *   h    bf16 with h_recip NULL, else a checkpoint's codes and its scales; g and u are
  *        then the values that the codes stand for.
  *   dh   the layouts of [dg | du] [rows, 2 ffn]; q in 1x128 blocks of each half.
