@@ -36,6 +36,7 @@ from .ops import (  # noqa: F401
     fp8_tensorwise_quant_noalloc,
     fp8bw_gemm_num_configs,
     gemm_plan,
+    grouped_wgrad_plan,
     linear_saved_bytes,
     linear_workspace,
     linear_xent_bwd,

@@ -117,6 +117,7 @@ PROTOTYPES = {
                                                         c_i64, c_ptr, c_i64, c_i64, c_int, c_ptr,
                                                         c_size, c_ptr]),
     "fp8bw_grouped_wgrad_ws_bytes": (c_size, [c_i64, c_i64, c_i64, c_int]),
+    "fp8bw_grouped_wgrad_plan": (c_int, [c_i64, c_i64, c_i64, c_int, c_int, ctypes.POINTER(c_i64)]),
     "fp8_blockwise_quant_grouped": (c_int, [c_ptr, c_i64, c_i64, c_i64, c_i64, c_int, c_int, c_ptr,
                                             c_i64, c_i64, c_ptr, c_i64, c_i64, c_i64, c_ptr]),
 }

@@ -2247,11 +2247,20 @@ static void launch_wgrad_cfg(int cfg, const GemmArgs& a, dim3 grid, hipStream_t 
   }
 }
 
+WgradRun grouped_wgrad_run(const GemmProblem& p, int groups, int64_t out_s_group) {
+  const WgradPlan w = wgrad_plan(p, groups);
+  WgradRun r;
+  r.cfg = wgrad_config(p, w.cfg);
+  r.splits = w.splits;
+  r.tiles = wgrad_tiles(p, groups, r.cfg);
+  r.stream = r.splits == 1 && r.cfg == 3 && r.tiles > num_cus() && wgrad_stream_ok(p, groups, out_s_group);
+  return r;
+}
+
 hipError_t launch_grouped_wgrad(const GemmProblem& p, int groups, const int* group_end, int64_t out_s_group, void* ws,
                                 hipStream_t stream) {
-  const WgradPlan w = wgrad_plan(p, groups);
-  const int cfg = wgrad_config(p, w.cfg);
-  const int64_t tiles = wgrad_tiles(p, groups, cfg);
+  const WgradRun w = grouped_wgrad_run(p, groups, out_s_group);
+  const int cfg = w.cfg;
   const int bm = kCfgs[cfg].bm, bn = kCfgs[cfg].bn;
   GemmArgs a = {};
   a.a = (const uint8_t*)p.a;
@@ -2278,12 +2287,11 @@ hipError_t launch_grouped_wgrad(const GemmProblem& p, int groups, const int* gro
   a.group_end = group_end;
   a.out_s_group = out_s_group;
   a.kgroups = groups;
-  const int cus = num_cus();
-  if (w.splits == 1 && cfg == 3 && tiles > cus && wgrad_stream_ok(p, groups, out_s_group)) {
-    hipLaunchKernelGGL(wgrad_stream_kernel, dim3((unsigned)cus), dim3(512), 0, stream, a);
+  if (w.stream) {
+    hipLaunchKernelGGL(wgrad_stream_kernel, dim3((unsigned)num_cus()), dim3(512), 0, stream, a);
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)tiles, (unsigned)w.splits);
+  const dim3 grid((unsigned)w.tiles, (unsigned)w.splits);
   if (w.splits == 1) {
     if (p.out_kind == kOutBf16) launch_wgrad_cfg<kOutBf16, false>(cfg, a, grid, stream);
     else launch_wgrad_cfg<kOutF32, false>(cfg, a, grid, stream);

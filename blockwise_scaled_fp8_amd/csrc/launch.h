@@ -99,6 +99,15 @@ hipError_t launch_grouped_gemm(const GemmProblem& p, int groups, const int* grou
 // Weight gradients: out + g*out_s_group = A . B^T over the K blocks
 // [group_end[g-1] / 128, group_end[g] / 128), mode kBlockB1x128.
 bool grouped_wgrad_ok(const GemmProblem& p, int groups);
+// How launch_grouped_wgrad runs a call: the tile configuration, the pieces of every
+// group's contraction, the output tiles of all groups, and whether one workgroup per
+// compute unit takes them as a stream.
+struct WgradRun {
+  int cfg, splits;
+  int64_t tiles;
+  bool stream;
+};
+WgradRun grouped_wgrad_run(const GemmProblem& p, int groups, int64_t out_s_group);
 size_t grouped_wgrad_ws_bytes(const GemmProblem& p, int groups);
 hipError_t launch_grouped_wgrad(const GemmProblem& p, int groups, const int* group_end, int64_t out_s_group, void* ws,
                                 hipStream_t stream);

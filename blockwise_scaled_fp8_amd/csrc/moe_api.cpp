@@ -304,6 +304,30 @@ FP8BW_API size_t fp8bw_grouped_wgrad_ws_bytes(int64_t M, int64_t N, int64_t K, i
   return align_up(fp8bw::grouped_wgrad_ws_bytes(p, groups));
 }
 
+FP8BW_API int fp8bw_grouped_wgrad_plan(int64_t M, int64_t N, int64_t K, int groups, int out_dtype, int64_t* info) {
+  if (!info) return fail(FP8BW_ERR_NULL, "info must be non-null");
+  if (out_dtype != FP8BW_OUT_BF16 && out_dtype != FP8BW_OUT_F32)
+    return fail(FP8BW_ERR_UNSUPPORTED, "unknown output type %d", out_dtype);
+  if (groups < 1 || groups > (1 << 20) || M <= 0 || N <= 0 || K <= 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim ||
+      K % 128)
+    return fail(FP8BW_ERR_SHAPE, "plan needs 0 < M, N, K <= 2^30, K %% 128 == 0 and groups in [1, 2^20]");
+  fp8bw::GemmProblem p = {};
+  p.M = M; p.N = N; p.K = K; p.lda = K; p.ldb = K; p.ldo = N;
+  p.ra_s_row = 1; p.ra_s_kb = M;
+  p.rb_s_row = 1; p.rb_s_kb = N;
+  p.mode = fp8bw::kBlockB1x128;
+  p.out_kind = out_dtype == FP8BW_OUT_BF16 ? fp8bw::kOutBf16 : fp8bw::kOutF32;
+  if (!fp8bw::grouped_wgrad_ok(p, groups))
+    return fail(FP8BW_ERR_UNSUPPORTED, "%d groups of [%lld, %lld] are more output tiles than one launch takes", groups,
+                (long long)M, (long long)N);
+  const fp8bw::WgradRun w = fp8bw::grouped_wgrad_run(p, groups, groups > 1 ? M * N : 0);
+  info[0] = w.cfg;
+  info[1] = w.splits;
+  info[2] = w.tiles;
+  info[3] = w.stream;
+  return ok();
+}
+
 FP8BW_API int fp8_scaled_grouped_gemm_blockwise_wgrad(
     const void* a, int64_t lda, const float* ra, int64_t ra_s_row, int64_t ra_s_kb, const void* b,
     int64_t ldb, const float* rb, int64_t rb_s_row, int64_t rb_s_kb, int groups, const int* group_end,

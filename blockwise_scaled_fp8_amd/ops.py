@@ -1058,6 +1058,18 @@ def fp8_scaled_grouped_gemm_blockwise_wgrad(a, ra, b, rb, group_end, out_dtype=t
     return out
 
 
+def grouped_wgrad_plan(M, N, K, groups, out_dtype=torch.bfloat16):
+    """How the library runs such a call (contiguous operands and outputs,
+    column-major scales) on the current device: tile configuration (0: 128x128,
+    1: 64x64, 3: 256x256), pieces of every group's contraction, output tiles of all
+    groups, and whether one workgroup per compute unit runs them as one stream."""
+    import ctypes
+    info = (ctypes.c_int64 * 4)()
+    check(load_library().fp8bw_grouped_wgrad_plan(M, N, K, groups, OUT_DTYPES[out_dtype], info))
+    config, pieces, tiles, stream = (int(v) for v in info)
+    return {"config": config, "pieces": pieces, "tiles": tiles, "stream": bool(stream)}
+
+
 @_on_tensor_device
 def fp8_blockwise_quant_grouped(x, transpose=False):
     """fp8_blockwise_quant(x[g], "128x128", transpose) of every matrix of x bf16

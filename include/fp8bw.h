@@ -690,10 +690,18 @@ int fp8bw_swiglu_bwd(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h,
  *   ws         fp8bw_grouped_wgrad_ws_bytes(M, N, K, groups) bytes, 256-byte aligned:
  *              fp32 partials of few tiles over long contractions, joined in a fixed
  *              order (0 where there are none: ws may be NULL).
- *   Requires K % 128 == 0, 1 <= groups <= 2^20 and at most 2^23 output tiles; errors as
- *   fp8_scaled_gemm_blockwise.
+ *   Requires K % 128 == 0, 1 <= groups <= 2^20 and fewer than 2^23 output tiles (times the
+ *   pieces of their contractions); errors as fp8_scaled_gemm_blockwise.
+ *
+ * fp8bw_grouped_wgrad_plan -- how such a call runs with contiguous operands and outputs and
+ * column-major scales on the current device (host query, launches nothing; for profiling and
+ * tests).  Fills info[4] (caller-owned host array): tile configuration (0: 128x128, 1: 64x64,
+ * 3: 256x256), pieces of every group's contraction, output tiles of all groups, and 1 where
+ * one workgroup per compute unit runs the tiles as one stream, else 0.  Requires 0 < M, N, K
+ * and K % 128 == 0.
  */
 size_t fp8bw_grouped_wgrad_ws_bytes(int64_t M, int64_t N, int64_t K, int groups);
+int fp8bw_grouped_wgrad_plan(int64_t M, int64_t N, int64_t K, int groups, int out_dtype, int64_t* info);
 int fp8_scaled_grouped_gemm_blockwise_wgrad(const void* a, int64_t lda, const float* ra,
                                             int64_t ra_s_row, int64_t ra_s_kb, const void* b,
                                             int64_t ldb, const float* rb, int64_t rb_s_row,
