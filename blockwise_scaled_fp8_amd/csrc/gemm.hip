@@ -2133,8 +2133,10 @@ struct WgradPlan {
   int cfg, splits;
 };
 
-static int64_t wgrad_tiles(const GemmProblem& p, int groups, int c) {
-  return groups * ((p.M + kCfgs[c].bm - 1) / kCfgs[c].bm) * ((p.N + kCfgs[c].bn - 1) / kCfgs[c].bn);
+// Floating: the queries take sizes whose tiles pass 2^63 (exact below 2^53).
+static double wgrad_tiles(const GemmProblem& p, int groups, int c) {
+  return (double)groups * (double)((p.M + kCfgs[c].bm - 1) / kCfgs[c].bm) *
+         (double)((p.N + kCfgs[c].bn - 1) / kCfgs[c].bn);
 }
 
 // Microseconds of `n` tiles of configuration c (all groups and pieces) over kb K
@@ -2165,7 +2167,7 @@ static WgradPlan wgrad_plan(const GemmProblem& p, int groups) {
     // (the large tiles need a whole one; half of a smaller one may be empty)
     if (c == 3 && (p.M < 256 || p.N < 256)) continue;
     if (c == 0 && (p.M < 64 || p.N < 64)) continue;
-    const double n = (double)wgrad_tiles(p, groups, c);
+    const double n = wgrad_tiles(p, groups, c);
     for (int s = 1; s <= 32; s *= 2) {
       if (s > 1 && (s > kb || 4 * s * matrix > 256e6)) break;
       const double t = wgrad_cost(c, n * s, kb / s, cus) + (s > 1 ? 4 + s * matrix / 1e6 : 0);
@@ -2188,7 +2190,7 @@ size_t grouped_wgrad_ws_bytes(const GemmProblem& p, int groups) {
 bool grouped_wgrad_ok(const GemmProblem& p, int groups) {
   const WgradPlan w = wgrad_plan(p, groups);
   // fewer than 2^32 threads a launch, at most 512 a workgroup
-  return wgrad_tiles(p, groups, wgrad_config(p, w.cfg)) * w.splits < (int64_t)1 << 23;
+  return wgrad_tiles(p, groups, wgrad_config(p, w.cfg)) * w.splits < 8388608.0;
 }
 
 // out_g = the sum of the group's partials in order, four columns a thread where
@@ -2252,7 +2254,7 @@ WgradRun grouped_wgrad_run(const GemmProblem& p, int groups, int64_t out_s_group
   WgradRun r;
   r.cfg = wgrad_config(p, w.cfg);
   r.splits = w.splits;
-  r.tiles = wgrad_tiles(p, groups, r.cfg);
+  r.tiles = (int64_t)wgrad_tiles(p, groups, r.cfg);   // grouped_wgrad_ok: below 2^23
   r.stream = r.splits == 1 && r.cfg == 3 && r.tiles > num_cus() && wgrad_stream_ok(p, groups, out_s_group);
   return r;
 }

@@ -37,3 +37,11 @@ def test_agrees_with_the_workspace(M, N, blocks, groups):
         need = p["pieces"] * groups * M * N * 4 if p["pieces"] > 1 else 0
         assert ws == -(-need // 256) * 256
         assert not p["stream"] or (p["config"] == 3 and p["pieces"] == 1 and dtype == torch.bfloat16 and N % 8 == 0)
+
+
+@pytest.mark.parametrize("args", [(1 << 30, 1 << 30, 128, 1 << 20, 0), (1 << 30, 1 << 30, 128, 1 << 16, 0),
+                                  (1 << 29, 1 << 30, 1 << 20, 1 << 20, 1), (1 << 30, 1 << 30, 1 << 30, 1, 0)])
+def test_tiles_past_64_bits(args):
+    lib = fp8.load_library()
+    assert lib.fp8bw_grouped_wgrad_plan(*args, (ctypes.c_int64 * 4)()) == UNSUP
+    assert lib.fp8bw_grouped_wgrad_ws_bytes(*args[:4]) == 0
