@@ -73,7 +73,9 @@ __device__ __forceinline__ float row16_amax(const float (&f)[8]) {
 
 // Four E4M3 codes of values scaled by their own block's scale.  These need no
 // clamp: |f| <= amax and s = 448 / max(amax, 1e-12) rounded give |f s| <= 448
-// (1 + 2^-23), and what lies between 448 and 464 rounds to 448.
+// (1 + 2^-23), and what lies between 448 and 464 rounds to 448.  A NaN, which has no
+// part in amax, and an infinity times its block's scale 0 become the NaN code (the
+// quantizers' clamp would make them finite).
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   int r;
   asm("" : "=v"(r));   // any register: the two conversions write all of it

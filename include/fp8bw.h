@@ -587,7 +587,9 @@ int fp8bw_moe_sort(const void* expert, int index_bits, int64_t tokens, int64_t t
  *       recip[r*rs_row + kb*rs_kb]
  *   qt  device E4M3 [cols, rows]: codes of v^T in 1x128 blocks along the rows, with
  *       recip_t[c*rst_row + mb*rst_kb]; needs rows % 16 == 0
- * The codes follow the quantizers' recipe on v (not on y).
+ * The codes follow the quantizers' recipe on v (not on y), which is one of finite values.
+ * Here a NaN becomes the NaN code and has no part in its block's scale; an infinity makes
+ * its block's reciprocal scale infinite, its own code NaN and the block's finite codes 0.
  */
 typedef struct {
   void* y;
