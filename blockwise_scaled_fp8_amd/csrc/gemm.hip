@@ -1863,11 +1863,13 @@ hipError_t launch_grouped_gemm(const GemmProblem& p, int groups, const int* grou
 // launch: waves 0 and 1 issue the direct loads and wait for them, the others
 // store, and nothing waits for stores.
 //
-// Measured: 33280 tokens, 16 groups of 8192 x 5120: 1490 to 1550 us, 1.8 to 1.87
+// Measured: 33280 tokens, 16 groups of 8192 x 5120: 1490 to 1600 us, 1.75 to 1.87
 // PFLOP/s (the dense product of this recipe 2.14); 9001 tokens, 16 groups of
-// 1360 x 2064, three empty: 60 us.  Bound by the vector pipe in the K loop, 2.0 us a
-// block, and by 5 us a tile behind it: without the epilogue 1341 us, without its
-// stores 1453.  An epilogue that stages each wave's values in 2 KB of its own, with
+// 1360 x 2064, three empty: 59 to 64 us, of which the overlap of ragged windows is a
+// fifth (a tile at an edge computes all its 256 rows and columns again: 16 groups of
+// five blocks take 70 us at 1360 x 2064, 54 us at 1280 x 2048).  Bound by the vector
+// pipe in the K loop, 2.0 us a block, and by 5 us a tile behind it: without the
+// epilogue 1341 us, without its stores 1453.  An epilogue that stages each wave's values in 2 KB of its own, with
 // no barrier and two blocks loaded ahead of the stores, leaves 0.5 us beside the
 // stores but these then hold up the loads behind them: 1480 to 1487 us.
 constexpr int kStreamGroups = 1024;
@@ -2156,8 +2158,9 @@ static double wgrad_cost(int c, double n, double kb, double cus) {
 
 // The cheapest by that estimate for groups of equal length; a further launch joins
 // pieces (4 us) and the fp32 partials, at most 256 MB, are written and read (8 TB/s
-// out of the memory-side cache).  1 group, 512 x 512, 256 blocks: 149 us in one
-// piece, 33 in eight; 2048 x 2048: 220 to 149 us (256x256 tiles, four pieces).
+// out of the memory-side cache).  1 group, 512 x 512, 256 blocks: 150 us in one
+// piece, 34 in sixteen (27 and 6 for the join); 2048 x 2048: 289 us in one piece of
+// 64x64 tiles, 155 to 176 in four of 256x256 (140 and 15).
 static WgradPlan wgrad_plan(const GemmProblem& p, int groups) {
   const double cus = num_cus(), kb = std::max(1.0, (double)(p.K / 128) / groups);
   const double matrix = (double)groups * p.M * p.N;

@@ -375,8 +375,9 @@ __global__ __launch_bounds__(256) void moe_gather_rows_kernel(const MoeGatherArg
 // bytes).
 //
 // 16640 tokens of 8192 columns to 2 of 16 experts, both code layouts: 205 to 212 us
-// for 867 MB, 4.1 TB/s.  Its reads alone take 108 us and its writes 83 to 107: they
-// add up, though a token's second reading comes from the caches.  What leaves that
+// for 867 MB, 4.1 TB/s; a token's second reading misses the L2, and the 1147 MB that
+// pass it do so at 5.5.  4160 tokens to 8 of 64: 166 us for 767 MB (1168 past the L2).
+// Its reads alone take 108 us and its writes 83 to 107: they add up.  What leaves that
 // as it is: 30% fewer vector instructions (8 rows a thread, 256 threads, against 4
 // and 512), the tiles ordered so that a token's copies are read together (40% fewer
 // reads reach HBM: 219 us), several row blocks a workgroup with the next one's
@@ -456,9 +457,9 @@ __global__ __launch_bounds__(256, 4) void moe_gather_tile_kernel(const MoeGather
 
 // The router's weights' gradient: one workgroup a token, which reads its row of
 // x once and the rows of its slots.  HBM: 16640 tokens of 8192 columns, two slots
-// each, 121 to 130 us for 818 MB.  (Beside the copies in one kernel it would spare
-// one of the two readings of x, 273 MB of 1.7 GB, and read y in the tokens' order
-// while it writes in the experts'.)
+// each, 121 to 130 us for 818 MB.  (Together with the copies, 128 x 128 tiles of the
+// sorted rows could form the products with the rows of x that they hold, 273 MB of
+// 1.7 GB less to read, for partial sums of every tile and a launch that joins them.)
 __global__ __launch_bounds__(256) void moe_dweight_kernel(const MoeGatherArgs p) {
   constexpr int CH = 4;
   __shared__ float red[kMoeMaxTopk][4];
