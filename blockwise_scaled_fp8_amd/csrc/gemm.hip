@@ -1869,9 +1869,10 @@ hipError_t launch_grouped_gemm(const GemmProblem& p, int groups, const int* grou
 // fifth (a tile at an edge computes all its 256 rows and columns again: 16 groups of
 // five blocks take 70 us at 1360 x 2064, 54 us at 1280 x 2048).  Bound by the vector
 // pipe in the K loop, 2.0 us a block, and by 5 us a tile behind it: without the
-// epilogue 1341 us, without its stores 1453.  An epilogue that stages each wave's values in 2 KB of its own, with
-// no barrier and two blocks loaded ahead of the stores, leaves 0.5 us beside the
-// stores but these then hold up the loads behind them: 1480 to 1487 us.
+// epilogue 1341 us, without its stores 1453.  An epilogue that stages each wave's
+// values in 2 KB of its own, with no barrier and two blocks loaded ahead of the
+// stores, leaves 0.5 us beside the stores but these then hold up the loads behind
+// them: 1480 to 1487 us.
 constexpr int kStreamGroups = 1024;
 
 struct WgradTile {
